@@ -1,0 +1,99 @@
+"""Newton-Schulz orthogonalisation and the Muon step in float64 (numpy).
+
+TEST INFRASTRUCTURE: see oracle/__init__.py.  Written from the formulas:
+
+  X = U / (|U|_F + eps);   A = X X^T,  X <- a X + (b A + c A A) X  per step
+  (X^T X and X (b A + c A A) for more rows than columns)
+
+  g = mean of the W slices;  M = mu M + g;  U = g + mu M or M
+  master = master (1 - lr wd) - lr s orth(U);  param = bf16(master)
+
+`rounded` is the same iteration with fp16 roundings at the places the
+library documents for its precision: what they cost on given inputs is the
+measure its results are held to.
+"""
+
+from __future__ import annotations
+
+import numpy as np
+
+COEF = (3.4445, -4.7750, 2.0315)
+
+
+def rows_of(coef, steps):
+    return [tuple(coef)] * steps if np.ndim(coef[0]) == 0 else list(coef)
+
+
+def start(U, eps):
+    U = np.asarray(U, np.float64)
+    n = np.sqrt(np.sum(U * U))
+    return U / (n + np.float64(np.float32(eps)))
+
+
+def orthogonalize(U, steps=5, coef=COEF, eps=1e-7):
+    """One matrix, float64."""
+    U = np.asarray(U, np.float64)
+    if U.shape[0] > U.shape[1]:
+        return orthogonalize(U.T, steps, coef, eps).T
+    X = start(U, eps)
+    for a, b, c in rows_of(coef, steps):
+        A = X @ X.T
+        X = a * X + (b * A + c * (A @ A)) @ X
+    return X
+
+
+def _f16(x):
+    """Round to fp16 at the library's scale of 2^10."""
+    with np.errstate(over="ignore"):
+        return (x * 1024).astype(np.float16).astype(np.float64) / 1024
+
+
+def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False):
+    """One matrix, with the library's fp16 roundings and exact sums."""
+    U = np.asarray(U, np.float64)
+    if U.shape[0] > U.shape[1]:
+        return rounded(U.T, steps, coef, eps, full).T
+
+    def pair(x):
+        hi = _f16(x)
+        return hi, _f16(x - hi)
+
+    def product(p, q):
+        s = p[0] @ q[0]
+        return s + p[0] @ q[1] + p[1] @ q[0] if full else s
+
+    def parts(M):
+        """fp16 without the diagonal (a pair if full), and the diagonal."""
+        d = M.diagonal().copy()
+        R = M - np.diag(d)
+        h, l = pair(R)
+        return (h, l if full else np.zeros_like(l)), d
+
+    X = start(U, eps)
+    rows = rows_of(coef, steps)
+    for k, (a, b, c) in enumerate(rows):
+        x = pair(X)
+        R, d = parts(product(x, (x[0].T, x[1].T)))
+        r = R[0] + R[1]
+        S = product(R, R) + (d[:, None] + d[None]) * r + np.diag(d * d)
+        R, e = parts(b * (r + np.diag(d)) + c * S)
+        X = (a + e)[:, None] * (x[0] + x[1]) + product(R, x)
+    return X
+
+
+def scale(mode, rows, cols):
+    return {"none": 1.0, "shape": max(1.0, rows / cols) ** 0.5,
+            "rms": 0.2 * max(rows, cols) ** 0.5}[mode]
+
+
+def momentum(g, m, mu, nesterov):
+    """fp32, one rounding per operation: (M, U) from g and the old M."""
+    f = np.float32
+    m = f(mu) * m + g
+    return m, (g + f(mu) * m if nesterov else m)
+
+
+def apply(master, O, lr, wd, s):
+    """float64: the stepped weights, from fp32 ones and O."""
+    lr, wd = np.float64(np.float32(lr)), np.float64(np.float32(wd))
+    return master.astype(np.float64) * (1 - lr * wd) - lr * s * O

@@ -1,8 +1,16 @@
 """One data-parallel rank's ZeRO-1/2 optimizer step on MI355X (gfx950).
 
-The HIP library libzs.so (C-ABI in include/zs.h) does all the work; this
-package is its ctypes binding, with the same names.
+The HIP library libzs.so (C-ABI in include/zs.h, and include/zs_muon.h for
+the Muon step) does all the work; this package is its ctypes binding, with
+the same names.
 """
+
+from ._muon import (MUON_EXPORTS, ZS_BF16, ZS_F32, ZS_MUON_SCALE_NONE,
+                    ZS_MUON_SCALE_RMS, ZS_MUON_SCALE_SHAPE, ZS_NS_COEF,
+                    ZS_NS_FAST, ZS_NS_FULL, ZS_NS_MAX_STEPS, zs_muon,
+                    zs_muon_step, zs_muon_tensor, zs_muon_workspace,
+                    zs_newton_schulz, zs_ns_matrices, zs_orthogonalize,
+                    zs_orthogonalize_workspace)
 
 from ._zs import (EXPORTS, LIB_PATH, ZS_ACC_ADD, ZS_ACC_FIRST, ZS_ACC_LAST,
                   ZS_EIO, ZS_EMISMATCH, zs_checkpoint_load,
@@ -42,4 +50,10 @@ __all__ = ["EXPORTS", "LIB_PATH", "ZS_ACC_ADD", "ZS_ACC_FIRST", "ZS_ACC_LAST",
            "zs_state_mv_unpack", "zs_state_pack", "zs_state_unpack",
            "zs_step", "zs_step_bf16", "zs_step_plain", "zs_stream_arrive", "zs_stream_create",
            "zs_set_residency_cap", "zs_stream_free", "zs_stream_step_begin",
-           "zs_stream_step_end", "zs_strerror"]
+           "zs_stream_step_end", "zs_strerror",
+           "MUON_EXPORTS", "ZS_BF16", "ZS_F32", "ZS_MUON_SCALE_NONE",
+           "ZS_MUON_SCALE_RMS", "ZS_MUON_SCALE_SHAPE", "ZS_NS_COEF",
+           "ZS_NS_FAST", "ZS_NS_FULL", "ZS_NS_MAX_STEPS", "zs_muon",
+           "zs_muon_step", "zs_muon_tensor", "zs_muon_workspace",
+           "zs_newton_schulz", "zs_ns_matrices", "zs_orthogonalize",
+           "zs_orthogonalize_workspace"]

@@ -1,0 +1,1340 @@
+// Orthogonalisation by Newton-Schulz products and the Muon step over
+// whole-tensor layouts (include/zs_muon.h).  gfx950 (CDNA4, wave64).
+//
+// With X = U / (|U|_F + eps) and m <= n its sides, one step is
+//   gram     A = X X^T            symmetric: one triangle of tiles, m^2 n flops
+//   poly     B = b A + c A A      symmetric: one triangle of tiles, m^3
+//   update   X <- a X + B X       2 m^2 n
+// (X^T X and X B for a matrix with more rows than columns), on the matrix
+// cores: D[i][j] = sum_k P[i][k] Q[j][k] with both operands contiguous along
+// k.  gram multiplies the rows of X's shorter side, update needs the rows of
+// its longer side, so X is kept in both orientations: Xd [rows][cols] as the
+// caller has it and Xt [cols][rows].
+//
+// Numbers.  Operands are fp16 times 2^10: |X| <= 1, so entries reach from
+// 2^10 down to the mean 2^10 / sqrt(rows cols) = 0.07 of the largest shapes,
+// in fp16's normal range.  Sums are fp32.  What is rounded to fp16, and what
+// is not:
+//  - X is a pair (hi, lo), 22 bits; products use hi, the term a X uses both.
+//    Rounded to fp16 alone, the rounding of each step would enter the null
+//    directions of a matrix of low rank and grow by a = 3.4 a step.
+//  - The diagonals of A and B are fp32 vectors, and zero in the fp16
+//    matrices: near the end A is close to the identity, and the rounding of
+//    its diagonal would be most of the error.  (R + D)(R + D) = R R + D R +
+//    R D + D D, the last three element by element.
+//  - In full precision (FULL) A, B and X^T are pairs too and every product
+//    is three: hi hi + hi lo + lo hi.
+//
+// Padding.  Every matrix is stored with its sides rounded up to 64 and zeros
+// behind, which the products preserve, so the k loop has no edge; rows past
+// the end of an operand are read from its last row and their results are not
+// stored.
+
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+
+#include "zs_device.h"
+#include "zs_internal.h"
+#include "zs_muon.h"
+
+namespace {
+
+typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef _Float16 f16;
+typedef f16 f16x4 __attribute__((ext_vector_type(4)));
+typedef f16 f16x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kMaxMats = ZS_MAX_GROUP;
+constexpr int kPad = 64;                 // sides are stored rounded up to this
+constexpr float kScale = 1024.f, kUnscale = 1.f / 1024.f;
+constexpr float kUnscale2 = kUnscale * kUnscale;
+constexpr int64_t kTile = ZS_TILE;
+
+__host__ __device__ inline int32_t padded(int32_t n)
+{
+    return (n + kPad - 1) / kPad * kPad;
+}
+
+// One stack of matrices in the workspace.
+struct Mat {
+    char* ws;
+    int32_t R, C;           // rows, cols
+    int32_t batch;
+    int32_t nparts;         // partial sums of squares per matrix
+    int32_t chunk;          // elements behind each of them
+};
+
+// Where its parts lie: E elements of X, S of A, D of a diagonal, over the
+// whole stack.
+//   Xd[2] hi, lo | Xt[2] hi (lo) | A hi (lo) | B hi (lo) | diagonals of A, B
+//   | partial sums (double)
+// The momentum kernel's U (fp32) lies where Xd[1] will be: it is read by the
+// normalising kernel, before the first update writes there.
+template <bool FULL>
+struct Region {
+    char* ws;
+    int64_t E, S, D;
+    __host__ __device__ Region(char* w, int32_t R, int32_t C, int32_t batch)
+        : ws(w)
+    {
+        const int64_t rp = padded(R), cp = padded(C),
+                      mp = rp < cp ? rp : cp;
+        E = batch * rp * cp;
+        S = batch * mp * mp;
+        D = batch * mp;
+    }
+    __device__ f16* xd(int p) const { return (f16*)(ws + 4 * p * E); }
+    __device__ f16* xt(int p) const
+    {
+        return (f16*)(ws + 8 * E + (FULL ? 4 : 2) * p * E);
+    }
+    __host__ __device__ int64_t x_bytes() const { return (FULL ? 16 : 12) * E; }
+    __device__ f16* a() const { return (f16*)(ws + x_bytes()); }
+    __device__ f16* b() const
+    {
+        return (f16*)(ws + x_bytes() + (FULL ? 4 : 2) * S);
+    }
+    __host__ __device__ int64_t d_off() const
+    {
+        return x_bytes() + (FULL ? 8 : 4) * S;
+    }
+    __device__ float* da() const { return (float*)(ws + d_off()); }
+    __device__ float* db() const { return da() + D; }
+    __host__ __device__ int64_t parts_off() const { return d_off() + 8 * D; }
+    __device__ double* parts() const { return (double*)(ws + parts_off()); }
+    __device__ float* u() const { return (float*)xd(1); }
+};
+
+struct Group {
+    int32_t count;
+    uint32_t start[kMaxMats + 1];       // first workgroup of each stack
+    Mat m[kMaxMats];
+};
+
+// The stack of workgroup `bid`, and the workgroup's index within it.
+__device__ __forceinline__ int find(const Group& g, uint32_t& bid)
+{
+    int p = 0;
+    while (p + 1 < g.count && bid >= g.start[p + 1])
+        ++p;
+    bid -= g.start[p];
+    return p;
+}
+
+__device__ __forceinline__ float bf16_to_f32(uint32_t u)
+{
+    return __uint_as_float(u << 16);
+}
+
+__device__ __forceinline__ uint32_t to_bf16(float f)
+{
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7fffffffu) > 0x7f800000u)
+        return (u >> 16) | 0x40u;
+    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+}
+
+// ---- sums of squares ---------------------------------------------------------
+
+constexpr int kNT = 256;                // threads of the elementwise kernels
+
+// Sum over the workgroup in a fixed order; valid in thread 0.
+__device__ __forceinline__ double block_sum(double v)
+{
+    __shared__ double s[kNT / 64];
+    for (int d = 32; d; d >>= 1)
+        v += __shfl_down(v, d, 64);
+    if ((threadIdx.x & 63) == 0)
+        s[threadIdx.x >> 6] = v;
+    __syncthreads();
+    double t = 0;
+    for (int w = 0; w < kNT / 64; ++w)
+        t += s[w];
+    return t;
+}
+
+struct Source {                         // a caller's stack of matrices
+    const void* x;
+    int64_t batch, row;                 // strides in elements
+    int32_t vec;                        // four elements at a time
+};
+
+struct NormArgs {
+    Group g;
+    Source src[kMaxMats];
+};
+
+template <bool BF16>
+__device__ __forceinline__ f32x4 load4(const void* x, int64_t i)
+{
+    if constexpr (BF16) {
+        const u32x2 u = *reinterpret_cast<const u32x2*>(
+            static_cast<const uint16_t*>(x) + i);
+        return f32x4{bf16_to_f32(u.x), __uint_as_float(u.x & 0xffff0000u),
+                     bf16_to_f32(u.y), __uint_as_float(u.y & 0xffff0000u)};
+    } else {
+        return *reinterpret_cast<const f32x4*>(
+            static_cast<const float*>(x) + i);
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ float load1(const void* x, int64_t i)
+{
+    if constexpr (BF16)
+        return bf16_to_f32(static_cast<const uint16_t*>(x)[i]);
+    else
+        return static_cast<const float*>(x)[i];
+}
+
+__device__ __forceinline__ double sq4(f32x4 v)
+{
+    return (double)v.x * v.x + (double)v.y * v.y + (double)v.z * v.z +
+           (double)v.w * v.w;
+}
+
+// Partial sums of squares of the callers' matrices: workgroup = one chunk of
+// one matrix.  Squares and sums in 64 bits: a gradient's squares leave
+// fp32's range long before the gradient does.
+template <bool BF16, bool FULL>
+__global__ __launch_bounds__(kNT) void ns_norm_kernel(NormArgs a)
+{
+    uint32_t bid = blockIdx.x;
+    const int p = find(a.g, bid);
+    const Mat& m = a.g.m[p];
+    const Source& s = a.src[p];
+    const uint32_t b = bid / m.nparts, part = bid % m.nparts;
+    const uint32_t n = (uint32_t)m.R * m.C;
+    const uint32_t e0 = part * m.chunk;
+    const uint32_t e1 = n - e0 < (uint32_t)m.chunk ? n : e0 + m.chunk;
+    double sum = 0;
+    if (s.vec) {
+        for (uint32_t e = e0 + 4 * threadIdx.x; e < e1; e += 4 * kNT) {
+            const uint32_t r = e / m.C, c = e % m.C;
+            sum += sq4(load4<BF16>(s.x, b * s.batch + r * s.row + c));
+        }
+    } else {
+        for (uint32_t e = e0 + threadIdx.x; e < e1; e += kNT) {
+            const uint32_t r = e / m.C, c = e % m.C;
+            const double v =
+                load1<BF16>(s.x, b * s.batch + r * s.row + c);
+            sum += v * v;
+        }
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0)
+        Region<FULL>(m.ws, m.R, m.C, m.batch)
+            .parts()[(int64_t)b * m.nparts + part] = sum;
+}
+
+// ---- the step's momentum --------------------------------------------------------
+
+struct MomSrc {
+    const uint16_t* grads;
+    float* state;                       // the tensor's first tile
+};
+
+struct MomArgs {
+    Group g;
+    MomSrc src[kMaxMats];
+    int64_t gstride;                    // slices: elements between slices
+    int32_t W, nesterov;
+    float mu, fw, invw;
+    int32_t pow2;                       // W is a power of two (1/W exact)
+};
+
+// g = mean of the W slices, M <- mu M + g, U to the workspace, partial sums
+// of U's squares.  2W + 8 bytes read and written in the state and gradients
+// and 4 for U, per element; bound by HBM.  VEC: four elements a thread
+// (every row of four stays inside a tile, tiles being multiples of four).
+template <bool TILED, bool VEC, bool FULL>
+__device__ __forceinline__ void momentum_part(const MomArgs& a, const Mat& m,
+                                              const MomSrc& s, uint32_t bid)
+{
+    constexpr int V = VEC ? 4 : 1;
+    const uint32_t b = bid / m.nparts, part = bid % m.nparts;
+    const uint32_t n = (uint32_t)m.R * m.C;
+    const uint32_t e0 = part * m.chunk;
+    const uint32_t e1 = n - e0 < (uint32_t)m.chunk ? n : e0 + m.chunk;
+    const Region<FULL> w(m.ws, m.R, m.C, m.batch);
+    float* const u = w.u();
+    double sum = 0;
+    for (uint32_t e = e0 + V * threadIdx.x; e < e1; e += V * kNT) {
+        const int64_t ge = (int64_t)b * n + e;
+        const int64_t tile = ge / kTile, pos = ge % kTile;
+        const uint16_t* const gp =
+            TILED ? s.grads + tile * a.W * kTile + pos : s.grads + ge;
+        const int64_t gs = TILED ? kTile : a.gstride;
+        float* const mp = s.state + (tile * 3 + 1) * kTile + pos;
+        f32x4 mom, acc, up;             // V of the four in use
+        if constexpr (VEC)
+            mom = *reinterpret_cast<const f32x4*>(mp);
+        else
+            mom.x = *mp;
+        for (int s0 = 0; s0 < a.W; s0 += 8) {
+            f32x4 x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (s0 + i < a.W) {
+                    if constexpr (VEC)
+                        x[i] = load4<true>(gp, (s0 + i) * gs);
+                    else
+                        x[i].x = load1<true>(gp, (s0 + i) * gs);
+                }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (s0 + i < a.W) {
+#pragma unroll
+                    for (int k = 0; k < V; ++k)
+                        acc[k] = s0 + i == 0 ? x[i][k] : acc[k] + x[i][k];
+                }
+        }
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const float g = a.pow2 ? acc[k] * a.invw : acc[k] / a.fw;
+            const float t = a.mu * mom[k];
+            mom[k] = t + g;
+            const float t2 = a.mu * mom[k];
+            up[k] = a.nesterov ? g + t2 : mom[k];
+            sum += (double)up[k] * up[k];
+        }
+        if constexpr (VEC) {
+            *reinterpret_cast<f32x4*>(mp) = mom;
+            *reinterpret_cast<f32x4*>(u + ge) = up;
+        } else {
+            *mp = mom.x;
+            u[ge] = up.x;
+        }
+    }
+    sum = block_sum(sum);
+    if (threadIdx.x == 0)
+        w.parts()[(int64_t)b * m.nparts + part] = sum;
+}
+
+template <bool TILED, bool FULL>
+__global__ __launch_bounds__(kNT) void muon_momentum_kernel(MomArgs a)
+{
+    uint32_t bid = blockIdx.x;
+    const int p = find(a.g, bid);
+    const Mat& m = a.g.m[p];
+    if (((uint32_t)m.R * m.C) % 4 == 0)
+        momentum_part<TILED, true, FULL>(a, m, a.src[p], bid);
+    else
+        momentum_part<TILED, false, FULL>(a, m, a.src[p], bid);
+}
+
+// ---- X = U / (|U| + eps) into the workspace ---------------------------------------
+
+struct InitArgs {
+    Group g;
+    Source src[kMaxMats];
+    float eps;
+};
+
+__device__ __forceinline__ void split(float x, f16& hi, f16& lo)
+{
+    hi = (f16)x;
+    lo = (f16)(x - (float)hi);
+}
+
+// Workgroup = one 64 x 64 tile of one padded matrix: read U, scale, write Xd
+// (hi, lo) and, through LDS, Xt.  SRC: 0 bf16, 1 fp32, 2 the workspace's U.
+template <int SRC, bool FULL>
+__global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
+{
+    __shared__ f16 t[FULL ? 2 : 1][64][64 + 4];
+    uint32_t bid = blockIdx.x;
+    const int p = find(a.g, bid);
+    const Mat& m = a.g.m[p];
+    const Region<FULL> w(m.ws, m.R, m.C, m.batch);
+    const int32_t rp = padded(m.R), cp = padded(m.C);
+    const uint32_t tc = cp / 64, tiles = tc * (rp / 64);
+    const uint32_t b = bid / tiles;
+    bid %= tiles;
+    const int r0 = bid / tc * 64, c0 = bid % tc * 64;
+    // the matrix's sum of squares, every workgroup in the same order
+    double sum = 0;
+    const double* const parts = w.parts() + (int64_t)b * m.nparts;
+    for (int i = threadIdx.x; i < m.nparts; i += kNT)
+        sum += parts[i];
+    sum = block_sum(sum);
+    const double norm = sqrt(sum);
+    // a matrix with a NaN or an infinity is NaN everywhere
+    const double inv =
+        norm < HUGE_VAL ? (double)kScale / (norm + (double)a.eps) : NAN;
+    const Source& s = a.src[p];
+    const void* const x = SRC == 2 ? (const void*)w.u() : s.x;
+    const int64_t xr = SRC == 2 ? m.C : s.row;
+    const int64_t xb = SRC == 2 ? (int64_t)m.R * m.C : s.batch;
+    const int tx = threadIdx.x % 16 * 4, ty = threadIdx.x / 16;
+    const int64_t mat = (int64_t)b * rp * cp;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int r = r0 + ty + 16 * k, c = c0 + tx;
+        f32x4 v = {0, 0, 0, 0};
+        if (r < m.R && c < m.C) {
+            const int64_t i = b * xb + r * xr + c;
+            if (s.vec) {
+                v = load4<SRC == 0>(x, i);
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < m.C)
+                        v[q] = load1<SRC == 0>(x, i + q);
+            }
+        }
+        f16x4 hi, lo;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            f16 h, l;
+            split((float)((double)v[q] * inv), h, l);
+            hi[q] = h;
+            lo[q] = l;
+            t[0][tx + q][ty + 16 * k] = h;
+            if constexpr (FULL)
+                t[1][tx + q][ty + 16 * k] = l;
+        }
+        const int64_t o = mat + (int64_t)r * cp + c;
+        *reinterpret_cast<f16x4*>(w.xd(0) + o) = hi;
+        *reinterpret_cast<f16x4*>(w.xd(0) + w.E + o) = lo;
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const int c = ty + 16 * k;
+        const int64_t o = mat + (int64_t)(c0 + c) * rp + r0 + tx;
+        *reinterpret_cast<f16x4*>(w.xt(0) + o) =
+            *reinterpret_cast<const f16x4*>(&t[0][c][tx]);
+        if constexpr (FULL)
+            *reinterpret_cast<f16x4*>(w.xt(0) + w.E + o) =
+                *reinterpret_cast<const f16x4*>(&t[1][c][tx]);
+    }
+}
+
+// ---- the products ------------------------------------------------------------------
+
+enum Epi { kGram, kPoly, kUpdate, kOutBf16, kOutF32, kStep };
+
+struct OutMat {
+    void* o;
+    int64_t batch, row;
+    int32_t vec;
+};
+
+struct StepMat {
+    float* state;                       // the tensor's first tile
+    uint16_t* pshard;                   // nullable, at the tensor
+    uint16_t* flat;                     // nullable, at the tensor
+    float s;                            // lr * shape's scale
+};
+
+struct GemmArgs {
+    Group g;
+    union {
+        OutMat out[kMaxMats];
+        StepMat st[kMaxMats];
+    };
+    int32_t parity;                     // which of the two X is read
+    float a, b, c;
+    float dec;                          // 1 - lr*wd
+};
+static_assert(sizeof(GemmArgs) <= 4096 && sizeof(MomArgs) <= 4096 &&
+              sizeof(NormArgs) <= 4096, "kernel arguments");
+
+typedef __attribute__((address_space(1))) const void gptr;
+typedef __attribute__((address_space(3))) void lptr;
+
+// Workgroup shape of the products: a BT x BT tile of D, WI x WJ waves, each
+// with FI x FJ accumulators of 16 x 16.
+template <int BT_, int WI_, int WJ_>
+struct Shape {
+    static constexpr int BT = BT_, WI = WI_, WJ = WJ_;
+    static constexpr int kWaves = WI * WJ, kThreads = 64 * kWaves;
+    static constexpr int FI = BT / WI / 16, FJ = BT / WJ / 16;
+    static constexpr int BK = 64;                       // k per stage
+    static constexpr int kHalf = BT * BK * 2;           // bytes per operand
+    static constexpr int kLoads = 2 * kHalf / 1024 / kWaves;  // a wave's, per
+                                                              // stage
+};
+
+// Tiles of one matrix's D.
+template <int BT>
+__host__ __device__ inline uint32_t tri_tiles(int32_t mp)
+{
+    const uint32_t t = (mp + BT - 1) / BT;
+    return t * (t + 1) / 2;
+}
+
+// Workgroups go to the 8 XCDs in turn; give each XCD a run of neighbouring
+// tiles, whose operands its L2 then holds.
+__device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t n)
+{
+    const uint32_t x = bid & 7, per = n >> 3, rem = n & 7;
+    return x * per + (x < rem ? x : rem) + (bid >> 3);
+}
+
+template <class SH, int EPI, bool FULL>
+__global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
+{
+    constexpr int BT = SH::BT, FI = SH::FI, FJ = SH::FJ;
+    constexpr bool kTri = EPI == kGram || EPI == kPoly;
+    // two stages; separate objects, so that the compiler sees that reading
+    // one does not wait for the loads into the other
+    __shared__ __align__(1024) char lds0[2 * SH::kHalf];
+    __shared__ __align__(1024) char lds1[2 * SH::kHalf];
+
+    uint32_t bid = xcd_order(blockIdx.x, a.g.start[a.g.count]);
+    const int p = find(a.g, bid);
+    const Mat& m = a.g.m[p];
+    const Region<FULL> w(m.ws, m.R, m.C, m.batch);
+    const int32_t rp = padded(m.R), cp = padded(m.C);
+    const int32_t mp = rp < cp ? rp : cp;
+    const bool tall = m.R > m.C;
+
+    // D[i][j]: ti, tj its tile
+    uint32_t b, ti, tj;
+    int32_t ni, nj, nk;
+    const f16 *P, *Q;
+    int64_t plo, qlo;
+    if constexpr (kTri) {
+        const uint32_t tiles = tri_tiles<BT>(mp);
+        b = bid / tiles;
+        bid %= tiles;
+        // row of the lower triangle: ti (ti + 1) / 2 <= bid
+        ti = (uint32_t)((sqrtf(8.f * (float)bid + 1.f) - 1.f) * 0.5f);
+        while (ti * (ti + 1) / 2 > bid)
+            --ti;
+        while ((ti + 1) * (ti + 2) / 2 <= bid)
+            ++ti;
+        tj = bid - ti * (ti + 1) / 2;
+        ni = nj = mp;
+        if constexpr (EPI == kGram) {
+            P = (tall ? w.xt(a.parity) : w.xd(a.parity)) +
+                (int64_t)b * rp * cp;
+            nk = tall ? rp : cp;
+            plo = w.E;
+        } else {
+            P = w.a() + (int64_t)b * mp * mp;
+            nk = mp;
+            plo = w.S;
+        }
+        Q = P;
+        qlo = plo;
+    } else {
+        ni = cp;
+        nj = rp;
+        nk = mp;
+        const uint32_t tni = (ni + BT - 1) / BT, tnj = (nj + BT - 1) / BT;
+        b = bid / (tni * tnj);
+        bid %= tni * tnj;
+        // bands of 8 tiles along j, so that a run of tiles shares operands
+        const uint32_t band = bid / (8 * tni) * 8;
+        const uint32_t h = tnj - band < 8 ? tnj - band : 8;
+        bid -= band * tni;
+        tj = band + bid % h;
+        ti = bid / h;
+        const f16* const B = w.b() + (int64_t)b * mp * mp;
+        if (tall) {
+            P = B;
+            plo = w.S;
+            Q = w.xd(a.parity) + (int64_t)b * rp * cp;
+            qlo = w.E;
+        } else {
+            P = w.xt(a.parity) + (int64_t)b * rp * cp;
+            plo = w.E;
+            Q = B;
+            qlo = w.S;
+        }
+    }
+    const int i0 = ti * BT, j0 = tj * BT;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wi = wave / SH::WJ, wj = wave % SH::WJ;
+
+    // Loads of a stage.  One instruction fills 1 KiB of LDS in lane order: 8
+    // rows of 64 k.  Within a row the 16-byte pieces are stored permuted by
+    // the row (piece c at c ^ (row & 7)), so that the 16 rows a fragment read
+    // touches at one k spread over the banks; the lane fetches the piece that
+    // belongs at its place.
+    const char* base[SH::kLoads];
+    uint32_t voff[SH::kLoads];
+#pragma unroll
+    for (int q = 0; q < SH::kLoads; ++q) {
+        const int u = wave * SH::kLoads + q;
+        const bool isP = u < BT / 8;
+        const int row = (isP ? u : u - BT / 8) * 8 + lane / 8;
+        const int lim = isP ? ni - i0 : nj - j0;
+        const int r = row < lim ? row : lim - 1;
+        base[q] = reinterpret_cast<const char*>(
+            isP ? P + (int64_t)i0 * nk : Q + (int64_t)j0 * nk);
+        voff[q] = (uint32_t)r * nk * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
+    }
+    const int nkt = nk / SH::BK;
+    const int total = FULL ? 3 * nkt : nkt;
+    auto load = [&](char* lds, int kt) {
+        int64_t dp = 0, dq = 0;
+        if constexpr (FULL) {
+            const int seg = kt / nkt;
+            kt -= seg * nkt;
+            dq = seg == 1 ? 2 * qlo : 0;
+            dp = seg == 2 ? 2 * plo : 0;
+        }
+#pragma unroll
+        for (int q = 0; q < SH::kLoads; ++q) {
+            const int u = wave * SH::kLoads + q;
+            const char* const s = base[q] + (u < BT / 8 ? dp : dq) +
+                                  (int64_t)kt * (SH::BK * 2);
+            __builtin_amdgcn_global_load_lds((gptr*)(s + voff[q]),
+                                             (lptr*)(lds + u * 1024), 16, 0,
+                                             0);
+        }
+    };
+
+    f32x4 acc[FI][FJ];
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+            acc[i][j] = f32x4{0, 0, 0, 0};
+    const int frow = (lane & 15) * (SH::BK * 2);
+    const int fi = wi * FI * 16 * (SH::BK * 2) + frow;
+    const int fj = SH::kHalf + wj * FJ * 16 * (SH::BK * 2) + frow;
+    const int fc = ((lane >> 4) ^ (lane & 7)) * 16;
+    auto compute = [&](const char* lds) {
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks) {
+            f16x8 x[FI], y[FJ];
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+                x[i] = *reinterpret_cast<const f16x8*>(
+                    lds + fi + i * 16 * SH::BK * 2 + (fc ^ (ks * 64)));
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+                y[j] = *reinterpret_cast<const f16x8*>(
+                    lds + fj + j * 16 * SH::BK * 2 + (fc ^ (ks * 64)));
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        x[i], y[j], acc[i][j], 0, 0, 0);
+        }
+    };
+
+    // Two stages: at the top of a turn the barrier (which waits for this
+    // wave's loads) makes the stage to be read whole and the other one free.
+    load(lds0, 0);
+    for (int kt = 0; kt < total; kt += 2) {
+        __syncthreads();
+        if (kt + 1 < total)
+            load(lds1, kt + 1);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(lds0);
+        if (kt + 1 >= total)
+            break;
+        __syncthreads();
+        if (kt + 2 < total)
+            load(lds0, kt + 2);
+        __builtin_amdgcn_sched_barrier(0);
+        compute(lds1);
+    }
+    __syncthreads();
+
+    // Epilogue.  A lane holds D[i .. i+3][j]: i = 4 (lane / 16) + 0..3 and
+    // j = lane % 16 of each 16 x 16.  Row-major out[j][i] takes them as they
+    // are; out[i][j] goes through LDS, 32 rows of a wave at a time.
+    const int li = i0 + wi * FI * 16 + (lane >> 4) * 4;
+    const int lj = j0 + wj * FJ * 16 + (lane & 15);
+    constexpr int kLd = FJ * 16 + 8;            // halves per staged row
+    static_assert(32 * kLd * 2 * SH::kWaves <= 2 * SH::kHalf, "staging");
+    f16* const stage = reinterpret_cast<f16*>(lds0) + wave * 32 * kLd;
+    // out[i][j] for the wave's rows 16 f .. 16 f + 31, values v[2][FJ]
+    auto transposed = [&](f16* out, int64_t ld, int f,
+                          const f16x4 (&v)[2][FJ]) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    stage[(h * 16 + (lane >> 4) * 4 + q) * kLd + j * 16 +
+                          (lane & 15)] = v[h][j][q];
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        constexpr int kPer = FJ * 2;            // 16-byte pieces per row
+#pragma unroll
+        for (int q = 0; q < 32 * kPer / 64; ++q) {
+            const int s = q * 64 + lane;
+            const int r = s / kPer, c = s % kPer * 8;
+            const int i = i0 + wi * FI * 16 + f * 16 + r;
+            const int j = j0 + wj * FJ * 16 + c;
+            if (i < ni && j < nj)
+                *reinterpret_cast<f16x8*>(out + i * ld + j) =
+                    *reinterpret_cast<const f16x8*>(stage + r * kLd + c);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+    };
+
+    const int64_t mat = (int64_t)b * rp * cp;
+    const f16* const xin = w.xd(a.parity) + mat;
+    const f16* const am = w.a() + (int64_t)b * mp * mp;
+    const float* const da = w.da() + (int64_t)b * mp;
+    const float* const db = w.db() + (int64_t)b * mp;
+#pragma unroll
+    for (int f = 0; f < FI; f += 2) {
+        f16x4 vh[2][FJ], vl[2][FJ];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int jf = 0; jf < FJ; ++jf) {
+                const int i = li + (f + h) * 16, j = lj + jf * 16;
+                const f32x4 d = acc[f + h][jf];
+                vh[h][jf] = f16x4{0, 0, 0, 0};
+                vl[h][jf] = f16x4{0, 0, 0, 0};
+                if (i >= ni || j >= nj)
+                    continue;
+                f32x4 v;                        // the result, times kScale
+                if constexpr (EPI == kGram) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        v[q] = d[q] * kUnscale;
+                        if (i + q == j) {
+                            (w.da() + (int64_t)b * mp)[j] = d[q] * kUnscale2;
+                            v[q] = 0;
+                        }
+                    }
+                } else if constexpr (EPI == kPoly) {
+                    const int64_t o = (int64_t)j * mp + i;
+                    const f16x4 rh = *reinterpret_cast<const f16x4*>(am + o);
+                    f16x4 rl = {0, 0, 0, 0};
+                    if constexpr (FULL)
+                        rl = *reinterpret_cast<const f16x4*>(am + w.S + o);
+                    const f32x4 di =
+                        *reinterpret_cast<const f32x4*>(da + i);
+                    const float dj = da[j];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const float r = (float)rh[q] + (float)rl[q];
+                        const float sq = d[q] * kUnscale + (di[q] + dj) * r;
+                        v[q] = a.b * r + a.c * sq;
+                        if (i + q == j) {
+                            (w.db() + (int64_t)b * mp)[j] =
+                                a.a + (a.b * dj + a.c * (d[q] * kUnscale2 +
+                                                         dj * dj));
+                            v[q] = 0;
+                        }
+                    }
+                } else {
+                    const int64_t o = (int64_t)j * cp + i;
+                    const f16x4 xh = *reinterpret_cast<const f16x4*>(xin + o);
+                    const f16x4 xl =
+                        *reinterpret_cast<const f16x4*>(xin + w.E + o);
+                    f32x4 di;
+                    if (tall)
+                        di = *reinterpret_cast<const f32x4*>(db + i);
+                    else
+                        di = f32x4{1, 1, 1, 1} * db[j];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        v[q] = di[q] * ((float)xh[q] + (float)xl[q]) +
+                               d[q] * kUnscale;
+                }
+                if constexpr (EPI == kGram || EPI == kPoly ||
+                              EPI == kUpdate) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f16 x, y;
+                        split(v[q], x, y);
+                        vh[h][jf][q] = x;
+                        vl[h][jf][q] = y;
+                    }
+                    f16* const out = EPI == kGram
+                                         ? w.a() + (int64_t)b * mp * mp
+                                     : EPI == kPoly
+                                         ? w.b() + (int64_t)b * mp * mp
+                                         : w.xd(1 - a.parity) + mat;
+                    const int64_t o =
+                        (int64_t)j * (EPI == kUpdate ? cp : mp) + i;
+                    *reinterpret_cast<f16x4*>(out + o) = vh[h][jf];
+                    if constexpr (FULL || EPI == kUpdate)
+                        *reinterpret_cast<f16x4*>(
+                            out + (EPI == kUpdate ? w.E : w.S) + o) =
+                            vl[h][jf];
+                } else if constexpr (EPI == kOutBf16 || EPI == kOutF32) {
+                    const OutMat& om = a.out[p];
+                    if (i >= m.C || j >= m.R)
+                        continue;
+                    const int64_t o = b * om.batch + j * om.row + i;
+                    f32x4 x;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+                        x[q] = v[q] * kUnscale;
+                    if constexpr (EPI == kOutF32) {
+                        float* const op = static_cast<float*>(om.o) + o;
+                        if (om.vec) {
+                            *reinterpret_cast<f32x4*>(op) = x;
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (i + q < m.C)
+                                    op[q] = x[q];
+                        }
+                    } else {
+                        uint16_t* const op =
+                            static_cast<uint16_t*>(om.o) + o;
+                        if (om.vec) {
+                            *reinterpret_cast<u32x2*>(op) =
+                                u32x2{to_bf16(x[0]) | (to_bf16(x[1]) << 16),
+                                      to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
+                        } else {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                if (i + q < m.C)
+                                    op[q] = (uint16_t)to_bf16(x[q]);
+                        }
+                    }
+                } else {
+                    const StepMat& sm = a.st[p];
+                    if (i >= m.C || j >= m.R)
+                        continue;
+                    const int64_t e =
+                        ((int64_t)b * m.R + j) * m.C + i;
+                    if (m.C % 4 == 0) {
+                        f32x4* const mp4 = reinterpret_cast<f32x4*>(
+                            sm.state + e / kTile * 3 * kTile + e % kTile);
+                        f32x4 x = *mp4;
+                        uint32_t h4[4];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float t = x[q] * a.dec;
+                            const float u = sm.s * (v[q] * kUnscale);
+                            x[q] = t - u;
+                            h4[q] = to_bf16(x[q]);
+                        }
+                        *mp4 = x;
+                        const u32x2 hb = {h4[0] | (h4[1] << 16),
+                                          h4[2] | (h4[3] << 16)};
+                        if (sm.pshard)
+                            *reinterpret_cast<u32x2*>(sm.pshard + e) = hb;
+                        if (sm.flat)
+                            *reinterpret_cast<u32x2*>(sm.flat + e) = hb;
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            if (i + q >= m.C)
+                                continue;
+                            const int64_t eq = e + q;
+                            float* const m1 = sm.state +
+                                              eq / kTile * 3 * kTile +
+                                              eq % kTile;
+                            const float t = *m1 * a.dec;
+                            const float u = sm.s * (v[q] * kUnscale);
+                            const float x = t - u;
+                            *m1 = x;
+                            const uint16_t hb = (uint16_t)to_bf16(x);
+                            if (sm.pshard)
+                                sm.pshard[eq] = hb;
+                            if (sm.flat)
+                                sm.flat[eq] = hb;
+                        }
+                    }
+                }
+            }
+        if constexpr (EPI == kGram || EPI == kPoly) {
+            // the other triangle
+            if (ti != tj) {
+                f16* const out = (EPI == kGram ? w.a() : w.b()) +
+                                 (int64_t)b * mp * mp;
+                transposed(out, mp, f, vh);
+                if constexpr (FULL)
+                    transposed(out + w.S, mp, f, vl);
+            }
+        } else if constexpr (EPI == kUpdate) {
+            f16* const out = w.xt(1 - a.parity) + mat;
+            transposed(out, rp, f, vh);
+            if constexpr (FULL)
+                transposed(out + w.E, rp, f, vl);
+        }
+    }
+}
+
+// ---- host ---------------------------------------------------------------------------
+
+int check_launch(const char* what)
+{
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess)
+        return zs::fail(ZS_EDEVICE, "%s: %s", what, hipGetErrorString(err));
+    return ZS_OK;
+}
+
+constexpr int64_t kMaxSide = 32768;             // of the smaller side
+constexpr int64_t kMaxLong = (int64_t)1 << 22;  // of the larger: a tile's rows
+                                                // span less than 4 GiB
+constexpr int64_t kMaxTiles = (int64_t)1 << 23; // 64 x 64 tiles of a call
+constexpr int32_t kMaxParts = 1024;             // partial sums per matrix
+constexpr int32_t kMinChunk = 2048;
+
+// One member's sizes, checked; tiles: 64 x 64 tiles of X or of A.
+int check_sizes(int32_t i, int64_t batch, int64_t rows, int64_t cols,
+                int64_t& tiles)
+{
+    using zs::fail;
+    if (batch < 0 || rows < 0 || cols < 0)
+        return fail(ZS_EINVAL, "matrices %d: negative size", i);
+    if (batch == 0 || rows == 0 || cols == 0)
+        return ZS_OK;
+    if (rows > INT32_MAX / cols)
+        return fail(ZS_ERANGE, "matrices %d: %lld x %lld elements in one "
+                    "matrix", i, (long long)rows, (long long)cols);
+    const int64_t lo = rows < cols ? rows : cols;
+    const int64_t hi = rows < cols ? cols : rows;
+    if (lo > kMaxSide || hi > kMaxLong)
+        return fail(ZS_ERANGE, "matrices %d: %lld x %lld is above %lld on "
+                    "the smaller or %lld on the larger side", i,
+                    (long long)rows, (long long)cols, (long long)kMaxSide,
+                    (long long)kMaxLong);
+    const int64_t per = ((rows + 63) / 64) * ((cols + 63) / 64);
+    const int64_t parts = rows * cols / kMinChunk + 1;
+    const int64_t most = per > parts ? per : parts;
+    if (batch > kMaxTiles / most || (tiles += batch * most) > kMaxTiles)
+        return fail(ZS_ERANGE, "more than %lld matrix tiles in one call",
+                    (long long)kMaxTiles);
+    return ZS_OK;
+}
+
+int check_precision(int32_t precision)
+{
+    if (precision != ZS_NS_FAST && precision != ZS_NS_FULL)
+        return zs::fail(ZS_EINVAL, "unknown precision %d", precision);
+    return ZS_OK;
+}
+
+int check_ns(const zs_newton_schulz* ns)
+{
+    using zs::fail;
+    if (!ns) return fail(ZS_EINVAL, "ns is NULL");
+    if (ns->steps < 1 || ns->steps > ZS_NS_MAX_STEPS)
+        return fail(ZS_EINVAL, "steps %d outside [1, %d]", ns->steps,
+                    ZS_NS_MAX_STEPS);
+    if (const int rc = check_precision(ns->precision)) return rc;
+    if (!(ns->eps > 0) || !std::isfinite(ns->eps))
+        return fail(ZS_EINVAL, "eps must be positive and finite");
+    for (int k = 0; k < ns->steps; ++k)
+        for (int q = 0; q < 3; ++q)
+            if (!std::isfinite(ns->coef[k][q]))
+                return fail(ZS_EINVAL, "coef[%d][%d] is not finite", k, q);
+    return ZS_OK;
+}
+
+bool aligned(const void* p, uintptr_t n)
+{
+    return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
+}
+
+void set_parts(Mat& m)
+{
+    const int64_t n = (int64_t)m.R * m.C;
+    int64_t chunk = (n + kMaxParts - 1) / kMaxParts;
+    chunk = (chunk + 4 * kNT - 1) / (4 * kNT) * (4 * kNT);
+    m.chunk = (int32_t)(chunk < kMinChunk ? kMinChunk : chunk);
+    m.nparts = (int32_t)((n + m.chunk - 1) / m.chunk);
+}
+
+// A stack's bytes of workspace.
+int64_t mat_bytes(const Mat& m, bool full)
+{
+    const int64_t parts = 8 * (int64_t)m.batch * m.nparts;
+    const int64_t off =
+        full ? Region<true>(nullptr, m.R, m.C, m.batch).parts_off()
+             : Region<false>(nullptr, m.R, m.C, m.batch).parts_off();
+    return (off + parts + 255) / 256 * 256;
+}
+
+// Appends a stack to the group, with its part of the workspace.
+void add_mat(Group& g, int64_t batch, int64_t rows, int64_t cols, bool full,
+             char* ws, int64_t& used)
+{
+    Mat& m = g.m[g.count++];
+    m.R = (int32_t)rows;
+    m.C = (int32_t)cols;
+    m.batch = (int32_t)batch;
+    set_parts(m);
+    m.ws = ws + used;
+    used += mat_bytes(m, full);
+}
+
+int64_t group_bytes(const Group& g, bool full)
+{
+    int64_t n = 0;
+    for (int i = 0; i < g.count; ++i)
+        n += mat_bytes(g.m[i], full);
+    return n;
+}
+
+// Workgroup prefix sums: fn(mat) workgroups per matrix of the stack.
+template <class Fn>
+uint32_t set_starts(Group& g, Fn fn)
+{
+    uint32_t n = 0;
+    for (int i = 0; i < g.count; ++i) {
+        g.start[i] = n;
+        n += (uint32_t)g.m[i].batch * (uint32_t)fn(g.m[i]);
+    }
+    g.start[g.count] = n;
+    return n;
+}
+
+typedef Shape<128, 2, 2> Shape128;
+
+template <class SH, int EPI, bool FULL>
+int launch_gemm(GemmArgs& a, hipStream_t s)
+{
+    const uint32_t n = set_starts(a.g, [](const Mat& m) -> uint32_t {
+        const int32_t rp = padded(m.R), cp = padded(m.C);
+        if (EPI == kGram || EPI == kPoly)
+            return tri_tiles<SH::BT>(rp < cp ? rp : cp);
+        return ((rp + SH::BT - 1) / SH::BT) * ((cp + SH::BT - 1) / SH::BT);
+    });
+    hipLaunchKernelGGL((ns_gemm_kernel<SH, EPI, FULL>), dim3(n),
+                       dim3(SH::kThreads), 0, s, a);
+    return check_launch("Newton-Schulz product");
+}
+
+// The steps on a group whose X[0] is in the workspace; LAST: the epilogue of
+// the last update.
+template <int LAST, bool FULL>
+int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
+{
+    for (int k = 0; k < ns.steps; ++k) {
+        a.parity = k & 1;
+        a.a = ns.coef[k][0];
+        a.b = ns.coef[k][1];
+        a.c = ns.coef[k][2];
+        int rc = launch_gemm<Shape128, kGram, FULL>(a, s);
+        if (!rc) rc = launch_gemm<Shape128, kPoly, FULL>(a, s);
+        if (!rc)
+            rc = k + 1 < ns.steps
+                     ? launch_gemm<Shape128, kUpdate, FULL>(a, s)
+                     : launch_gemm<Shape128, LAST, FULL>(a, s);
+        if (rc) return rc;
+    }
+    return ZS_OK;
+}
+
+uint32_t init_tiles(const Mat& m)
+{
+    return (uint32_t)(padded(m.R) / 64) * (uint32_t)(padded(m.C) / 64);
+}
+
+template <int SRC, bool FULL>
+int launch_init(const Group& g, const Source* src, float eps, hipStream_t s)
+{
+    InitArgs a;
+    a.g = g;
+    for (int i = 0; i < g.count; ++i)
+        a.src[i] = src[i];
+    a.eps = eps;
+    const uint32_t n = set_starts(a.g, init_tiles);
+    hipLaunchKernelGGL((ns_init_kernel<SRC, FULL>), dim3(n), dim3(kNT), 0, s,
+                       a);
+    return check_launch("Newton-Schulz start");
+}
+
+template <bool BF16, bool FULL>
+int orthogonalize(const Group& g, const Source* src, const OutMat* out,
+                  int32_t o_type, const zs_newton_schulz& ns, hipStream_t s)
+{
+    NormArgs na;
+    na.g = g;
+    for (int i = 0; i < g.count; ++i)
+        na.src[i] = src[i];
+    const uint32_t n =
+        set_starts(na.g, [](const Mat& m) { return m.nparts; });
+    hipLaunchKernelGGL((ns_norm_kernel<BF16, FULL>), dim3(n), dim3(kNT), 0,
+                       s, na);
+    int rc = check_launch("norm kernel");
+    if (!rc) rc = launch_init<BF16 ? 0 : 1, FULL>(g, src, ns.eps, s);
+    if (rc) return rc;
+    GemmArgs a;
+    a.g = g;
+    for (int i = 0; i < g.count; ++i)
+        a.out[i] = out[i];
+    a.dec = 1;
+    return o_type == ZS_BF16 ? run_steps<kOutBf16, FULL>(a, ns, s)
+                             : run_steps<kOutF32, FULL>(a, ns, s);
+}
+
+}  // namespace
+
+extern "C" int zs_orthogonalize_workspace(int32_t count,
+                                          const zs_ns_matrices* mats,
+                                          int32_t precision, int64_t* bytes)
+{
+    using zs::fail;
+    zs::clear_error();
+    if (!mats || !bytes) return fail(ZS_EINVAL, "NULL pointer");
+    if (count < 1 || count > kMaxMats)
+        return fail(ZS_EINVAL, "count %d outside [1, %d]", count, kMaxMats);
+    if (const int rc = check_precision(precision)) return rc;
+    Group g;
+    g.count = 0;
+    int64_t tiles = 0, used = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const zs_ns_matrices& m = mats[i];
+        const int rc = check_sizes(i, m.batch, m.rows, m.cols, tiles);
+        if (rc) return rc;
+        if (m.batch && m.rows && m.cols)
+            add_mat(g, m.batch, m.rows, m.cols, precision == ZS_NS_FULL,
+                    nullptr, used);
+    }
+    *bytes = group_bytes(g, precision == ZS_NS_FULL);
+    return ZS_OK;
+}
+
+extern "C" int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
+                                int32_t x_type, int32_t o_type,
+                                const zs_newton_schulz* ns, void* workspace,
+                                int64_t workspace_bytes, void* hip_stream)
+{
+    using zs::fail;
+    zs::clear_error();
+    if (!mats) return fail(ZS_EINVAL, "mats is NULL");
+    if (count < 1 || count > kMaxMats)
+        return fail(ZS_EINVAL, "count %d outside [1, %d]", count, kMaxMats);
+    if ((x_type != ZS_BF16 && x_type != ZS_F32) ||
+        (o_type != ZS_BF16 && o_type != ZS_F32))
+        return fail(ZS_EINVAL, "unknown element type %d or %d", x_type,
+                    o_type);
+    if (const int rc = check_ns(ns)) return rc;
+    const bool full = ns->precision == ZS_NS_FULL;
+    const uintptr_t xe = x_type == ZS_BF16 ? 2 : 4;
+    const uintptr_t oe = o_type == ZS_BF16 ? 2 : 4;
+    Group g;
+    g.count = 0;
+    Source src[kMaxMats];
+    OutMat out[kMaxMats];
+    int64_t tiles = 0, used = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const zs_ns_matrices& m = mats[i];
+        if (const int rc = check_sizes(i, m.batch, m.rows, m.cols, tiles))
+            return rc;
+        if (!(m.batch && m.rows && m.cols))
+            continue;
+        if (!m.x || !m.o)
+            return fail(ZS_EINVAL, "matrices %d: NULL pointer", i);
+        if (!aligned(m.x, xe) || !aligned(m.o, oe))
+            return fail(ZS_EALIGN, "matrices %d: pointer not aligned to its "
+                        "elements", i);
+        if (m.x_row_stride < m.cols || m.o_row_stride < m.cols ||
+            m.x_batch_stride < 0)
+            return fail(ZS_EINVAL, "matrices %d: row stride below cols, or "
+                        "a negative batch stride", i);
+        // the furthest element has to have an address
+        constexpr int64_t kFar = (int64_t)1 << 46;
+        if (m.x_row_stride > kFar / m.rows || m.o_row_stride > kFar / m.rows ||
+            m.x_batch_stride > kFar / m.batch ||
+            m.o_batch_stride > kFar / m.batch)
+            return fail(ZS_ERANGE, "matrices %d: strides too large", i);
+        if (m.batch > 1 &&
+            m.o_batch_stride < (m.rows - 1) * m.o_row_stride + m.cols)
+            return fail(ZS_EINVAL, "matrices %d: outputs overlap", i);
+        Source& s = src[g.count];
+        s.x = m.x;
+        s.batch = m.x_batch_stride;
+        s.row = m.x_row_stride;
+        s.vec = m.cols % 4 == 0 && s.row % 4 == 0 &&
+                (m.batch == 1 || s.batch % 4 == 0) && aligned(m.x, 4 * xe);
+        OutMat& o = out[g.count];
+        o.o = m.o;
+        o.batch = m.o_batch_stride;
+        o.row = m.o_row_stride;
+        o.vec = m.cols % 4 == 0 && o.row % 4 == 0 &&
+                (m.batch == 1 || o.batch % 4 == 0) && aligned(m.o, 4 * oe);
+        add_mat(g, m.batch, m.rows, m.cols, full,
+                static_cast<char*>(workspace), used);
+    }
+    if (g.count == 0) return ZS_OK;
+    if (!workspace) return fail(ZS_EINVAL, "workspace is NULL");
+    if (!aligned(workspace, 256))
+        return fail(ZS_EALIGN, "workspace must be 256-byte aligned");
+    if (workspace_bytes < used)
+        return fail(ZS_ERANGE, "workspace of %lld bytes, %lld needed",
+                    (long long)workspace_bytes, (long long)used);
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    if (x_type == ZS_BF16)
+        return full ? orthogonalize<true, true>(g, src, out, o_type, *ns, s)
+                    : orthogonalize<true, false>(g, src, out, o_type, *ns, s);
+    return full ? orthogonalize<false, true>(g, src, out, o_type, *ns, s)
+                : orthogonalize<false, false>(g, src, out, o_type, *ns, s);
+}
+
+namespace {
+
+// The members of a muon call, checked against the layout.
+int muon_group(const zs_layout* L, int32_t count, const zs_muon_tensor* t,
+               bool full, char* ws, Group& g, int64_t& used)
+{
+    using zs::fail;
+    if (!L) return fail(ZS_EINVAL, "layout is NULL");
+    if (!t) return fail(ZS_EINVAL, "tensors is NULL");
+    if (!L->whole_tensors)
+        return fail(ZS_EINVAL, "the layout is not whole-tensor");
+    if (count < 1 || count > kMaxMats)
+        return fail(ZS_EINVAL, "count %d outside [1, %d]", count, kMaxMats);
+    const int32_t nb = (int32_t)L->buckets.size();
+    g.count = 0;
+    used = 0;
+    int64_t tiles = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const int32_t b = t[i].bucket_id;
+        if (b < 0 || b >= nb)
+            return fail(ZS_ERANGE, "tensors[%d]: bucket %d outside [0, %d)",
+                        i, b, nb);
+        for (int32_t k = 0; k < i; ++k)
+            if (t[k].bucket_id == b)
+                return fail(ZS_EINVAL, "bucket %d appears twice", b);
+        if (const int rc = check_sizes(i, t[i].batch, t[i].rows, t[i].cols,
+                                       tiles))
+            return rc;
+        // sizes are in range, and so is their product (kMaxTiles)
+        const int64_t n = t[i].batch * t[i].rows * t[i].cols;
+        if (n != L->chunks[b].numel)
+            return fail(ZS_EINVAL, "tensors[%d]: %lld x %lld x %lld is not "
+                        "the tensor's %lld elements", i,
+                        (long long)t[i].batch, (long long)t[i].rows,
+                        (long long)t[i].cols, (long long)L->chunks[b].numel);
+        add_mat(g, t[i].batch, t[i].rows, t[i].cols, full, ws, used);
+    }
+    return ZS_OK;
+}
+
+template <bool FULL>
+int muon_step(const Group& g, MomArgs& ma, const StepMat* st, bool tiled,
+              const zs_muon& hp, hipStream_t s)
+{
+    ma.g = g;
+    const uint32_t n =
+        set_starts(ma.g, [](const Mat& m) { return m.nparts; });
+    if (tiled)
+        hipLaunchKernelGGL((muon_momentum_kernel<true, FULL>), dim3(n),
+                           dim3(kNT), 0, s, ma);
+    else
+        hipLaunchKernelGGL((muon_momentum_kernel<false, FULL>), dim3(n),
+                           dim3(kNT), 0, s, ma);
+    if (const int rc = check_launch("momentum kernel")) return rc;
+    Source src[kMaxMats] = {};
+    for (int i = 0; i < g.count; ++i)
+        src[i].vec = g.m[i].C % 4 == 0;
+    if (const int rc = launch_init<2, FULL>(g, src, hp.ns.eps, s)) return rc;
+    GemmArgs a;
+    a.g = g;
+    for (int i = 0; i < g.count; ++i)
+        a.st[i] = st[i];
+    a.dec = (float)(1.0 - (double)hp.lr * (double)hp.weight_decay);
+    return run_steps<kStep, FULL>(a, hp.ns, s);
+}
+
+}  // namespace
+
+extern "C" int zs_muon_workspace(const zs_layout* L, int32_t count,
+                                 const zs_muon_tensor* tensors,
+                                 int32_t precision, int64_t* bytes)
+{
+    zs::clear_error();
+    if (!bytes) return zs::fail(ZS_EINVAL, "bytes is NULL");
+    if (const int rc = check_precision(precision)) return rc;
+    Group g;
+    int64_t used;
+    const int rc = muon_group(L, count, tensors, precision == ZS_NS_FULL,
+                              nullptr, g, used);
+    if (!rc) *bytes = used;
+    return rc;
+}
+
+extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
+                            const zs_muon_tensor* tensors,
+                            const uint16_t* const* grads, int32_t grad_layout,
+                            int64_t grad_stride, float* state,
+                            uint16_t* param_shard, uint16_t* full_flat,
+                            const zs_muon* hp, void* workspace,
+                            int64_t workspace_bytes, void* hip_stream)
+{
+    using zs::fail;
+    zs::clear_error();
+    if (!hp) return fail(ZS_EINVAL, "hp is NULL");
+    if (const int rc = check_ns(&hp->ns)) return rc;
+    if (!std::isfinite(hp->lr) || !std::isfinite(hp->momentum) ||
+        !std::isfinite(hp->weight_decay))
+        return fail(ZS_EINVAL, "lr, momentum or weight_decay is not finite");
+    if (hp->scale != ZS_MUON_SCALE_NONE && hp->scale != ZS_MUON_SCALE_SHAPE &&
+        hp->scale != ZS_MUON_SCALE_RMS)
+        return fail(ZS_EINVAL, "unknown scale %d", hp->scale);
+    const bool full = hp->ns.precision == ZS_NS_FULL;
+    Group g;
+    int64_t used;
+    if (const int rc = muon_group(L, count, tensors, full,
+                                  static_cast<char*>(workspace), g, used))
+        return rc;
+    if (grad_layout != ZS_GRADS_SLICES && grad_layout != ZS_GRADS_TILED)
+        return fail(ZS_EINVAL, "unknown grad_layout %d", grad_layout);
+    if (!grads || !state || !workspace)
+        return fail(ZS_EINVAL, "grads, state and workspace must be non-NULL");
+    if (!param_shard && !full_flat)
+        return fail(ZS_EINVAL, "need param_shard or full_flat");
+    if (!aligned(state, 16) || !aligned(param_shard, 16) ||
+        !aligned(full_flat, 16))
+        return fail(ZS_EALIGN, "device pointers must be 16-byte aligned");
+    if (!aligned(workspace, 256))
+        return fail(ZS_EALIGN, "workspace must be 256-byte aligned");
+    const bool tiled = grad_layout == ZS_GRADS_TILED;
+    MomArgs ma;
+    StepMat st[kMaxMats];
+    for (int32_t i = 0; i < count; ++i) {
+        const zs_bucket& b = L->buckets[tensors[i].bucket_id];
+        if (!grads[i]) return fail(ZS_EINVAL, "grads[%d] is NULL", i);
+        if (!aligned(grads[i], 16))
+            return fail(ZS_EALIGN, "grads[%d] is not 16-byte aligned", i);
+        if (!tiled) {
+            if (grad_stride % 8)
+                return fail(ZS_EALIGN, "grad_stride %lld is not a multiple "
+                            "of 8", (long long)grad_stride);
+            if (grad_stride < b.slice_numel)
+                return fail(ZS_ERANGE, "grad_stride %lld < %lld elements per "
+                            "slice", (long long)grad_stride,
+                            (long long)b.slice_numel);
+            if (grad_stride > INT64_MAX / 2 / L->world)
+                return fail(ZS_ERANGE, "W * grad_stride overflows");
+        }
+        ma.src[i].grads = grads[i];
+        ma.src[i].state = state + b.tile_off * 3 * kTile;
+        st[i].state = ma.src[i].state;
+        st[i].pshard = param_shard ? param_shard + b.shard_off : nullptr;
+        st[i].flat = full_flat ? full_flat + slice_flat_pos(L, b) : nullptr;
+        const double r = (double)tensors[i].rows, c = (double)tensors[i].cols;
+        const double scale =
+            hp->scale == ZS_MUON_SCALE_SHAPE ? std::sqrt(r > c ? r / c : 1.0)
+            : hp->scale == ZS_MUON_SCALE_RMS
+                ? 0.2 * std::sqrt(r > c ? r : c)
+                : 1.0;
+        st[i].s = (float)((double)hp->lr * scale);
+    }
+    if (workspace_bytes < used)
+        return fail(ZS_ERANGE, "workspace of %lld bytes, %lld needed",
+                    (long long)workspace_bytes, (long long)used);
+    ma.gstride = grad_stride;
+    ma.W = L->world;
+    ma.nesterov = hp->nesterov != 0;
+    ma.mu = hp->momentum;
+    ma.fw = (float)L->world;
+    ma.invw = 1.f / (float)L->world;
+    ma.pow2 = (L->world & (L->world - 1)) == 0;
+    const hipStream_t s = static_cast<hipStream_t>(hip_stream);
+    return full ? muon_step<true>(g, ma, st, tiled, *hp, s)
+                : muon_step<false>(g, ma, st, tiled, *hp, s);
+}

@@ -51,7 +51,6 @@ typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 constexpr int kMaxMats = ZS_MAX_GROUP;
 constexpr int kPad = 64;                 // sides are stored rounded up to this
 constexpr float kScale = 1024.f, kUnscale = 1.f / 1024.f;
-constexpr float kUnscale2 = kUnscale * kUnscale;
 constexpr int64_t kTile = ZS_TILE;
 
 __host__ __device__ inline int32_t padded(int32_t n)
@@ -449,17 +448,41 @@ typedef __attribute__((address_space(1))) const void gptr;
 typedef __attribute__((address_space(3))) void lptr;
 
 // Workgroup shape of the products: a BT x BT tile of D, WI x WJ waves, each
-// with FI x FJ accumulators of 16 x 16.
-template <int BT_, int WI_, int WJ_>
+// with FI x FJ accumulators of 16 x 16, ST stages of 64 k in LDS.
+template <int BT_, int WI_, int WJ_, int ST_>
 struct Shape {
-    static constexpr int BT = BT_, WI = WI_, WJ = WJ_;
+    static constexpr int BT = BT_, WI = WI_, WJ = WJ_, ST = ST_;
     static constexpr int kWaves = WI * WJ, kThreads = 64 * kWaves;
     static constexpr int FI = BT / WI / 16, FJ = BT / WJ / 16;
-    static constexpr int BK = 64;                       // k per stage
-    static constexpr int kHalf = BT * BK * 2;           // bytes per operand
-    static constexpr int kLoads = 2 * kHalf / 1024 / kWaves;  // a wave's, per
-                                                              // stage
+    static constexpr int kRow = 128;                // bytes of a stage's row
+    static constexpr int kHalf = BT * kRow;         // bytes per operand
+    // 1 KiB load instructions of a wave per stage; the first half of the
+    // waves loads P, the second Q
+    static constexpr int kLoads = 2 * kHalf / 1024 / kWaves;
+    static_assert(kLoads * 512 * kWaves == kHalf && FI % 2 == 0, "shape");
 };
+
+// Two waves a SIMD taking turns (the loop is described in the kernel): the
+// large tile feeds the matrix cores best (4096^3: 1300 TFLOP/s, 8192^3: 1380;
+// the 128 tile 1090 and 1100, the 64 tile 740), the smaller ones fill the
+// chip where there are few of the larger.
+typedef Shape<256, 2, 4, 2> Shape256;
+typedef Shape<128, 2, 4, 2> Shape128;
+// Few tiles, bound by the latency of a stage: three in flight.
+typedef Shape<64, 2, 2, 4> Shape64;
+
+// s_waitcnt immediate: at most vm vector loads and lg LDS operations out.
+constexpr int wait_count(int vm, int lg)
+{
+    return (vm & 15) | ((vm >> 4) << 14) | (7 << 4) | (lg << 8);
+}
+
+__device__ __forceinline__ void slot_barrier()
+{
+    __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+}
 
 // Tiles of one matrix's D.
 template <int BT>
@@ -477,15 +500,100 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t n)
     return x * per + (x < rem ? x : rem) + (bid >> 3);
 }
 
+// The last update's results v[0..3], times kScale, at row j and columns
+// i .. i+3 of matrix b (i a multiple of 4; columns past the last are not
+// there).
+template <int EPI>
+__device__ __forceinline__ void finish(const GemmArgs& a, int p, const Mat& m,
+                                       uint32_t b, int j, int i,
+                                       const float* v)
+{
+    if constexpr (EPI == kOutBf16 || EPI == kOutF32) {
+        const OutMat& om = a.out[p];
+        const int64_t o = b * om.batch + j * om.row + i;
+        float x[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+            x[q] = v[q] * kUnscale;
+        if constexpr (EPI == kOutF32) {
+            float* const op = static_cast<float*>(om.o) + o;
+            if (om.vec) {
+                *reinterpret_cast<f32x4*>(op) = f32x4{x[0], x[1], x[2], x[3]};
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (i + q < m.C)
+                        op[q] = x[q];
+            }
+        } else {
+            uint16_t* const op = static_cast<uint16_t*>(om.o) + o;
+            if (om.vec) {
+                *reinterpret_cast<u32x2*>(op) =
+                    u32x2{to_bf16(x[0]) | (to_bf16(x[1]) << 16),
+                          to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (i + q < m.C)
+                        op[q] = (uint16_t)to_bf16(x[q]);
+            }
+        }
+    } else {
+        const StepMat& sm = a.st[p];
+        const int64_t e = ((int64_t)b * m.R + j) * m.C + i;
+        float x[4];
+        uint32_t h[4];
+        if (m.C % 4 == 0) {
+            f32x4* const s4 = reinterpret_cast<f32x4*>(
+                sm.state + e / kTile * 3 * kTile + e % kTile);
+            const f32x4 old = *s4;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const float t = old[q] * a.dec;
+                const float u = sm.s * (v[q] * kUnscale);
+                x[q] = t - u;
+                h[q] = to_bf16(x[q]);
+            }
+            *s4 = f32x4{x[0], x[1], x[2], x[3]};
+            const u32x2 hb = {h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
+            if (sm.pshard)
+                *reinterpret_cast<u32x2*>(sm.pshard + e) = hb;
+            if (sm.flat)
+                *reinterpret_cast<u32x2*>(sm.flat + e) = hb;
+        } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                if (i + q >= m.C)
+                    continue;
+                const int64_t eq = e + q;
+                float* const s1 =
+                    sm.state + eq / kTile * 3 * kTile + eq % kTile;
+                const float t = *s1 * a.dec;
+                const float u = sm.s * (v[q] * kUnscale);
+                x[q] = t - u;
+                *s1 = x[q];
+                h[q] = to_bf16(x[q]);
+                if (sm.pshard)
+                    sm.pshard[eq] = (uint16_t)h[q];
+                if (sm.flat)
+                    sm.flat[eq] = (uint16_t)h[q];
+            }
+        }
+    }
+}
+
 template <class SH, int EPI, bool FULL>
 __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
 {
-    constexpr int BT = SH::BT, FI = SH::FI, FJ = SH::FJ;
+    constexpr int BT = SH::BT, FI = SH::FI, FJ = SH::FJ, ST = SH::ST;
+    constexpr int kRow = SH::kRow, NL = SH::kLoads;
     constexpr bool kTri = EPI == kGram || EPI == kPoly;
-    // two stages; separate objects, so that the compiler sees that reading
-    // one does not wait for the loads into the other
+    // the stages; separate objects, so that the compiler sees that reading
+    // one does not wait for the loads into another
     __shared__ __align__(1024) char lds0[2 * SH::kHalf];
     __shared__ __align__(1024) char lds1[2 * SH::kHalf];
+    __shared__ __align__(1024) char lds2[ST > 2 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(1024) char lds3[ST > 3 ? 2 * SH::kHalf : 16];
 
     uint32_t bid = xcd_order(blockIdx.x, a.g.start[a.g.count]);
     const int p = find(a.g, bid);
@@ -555,43 +663,55 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wi = wave / SH::WJ, wj = wave % SH::WJ;
 
-    // Loads of a stage.  One instruction fills 1 KiB of LDS in lane order: 8
-    // rows of 64 k.  Within a row the 16-byte pieces are stored permuted by
-    // the row (piece c at c ^ (row & 7)), so that the 16 rows a fragment read
-    // touches at one k spread over the banks; the lane fetches the piece that
-    // belongs at its place.
-    const char* base[SH::kLoads];
-    uint32_t voff[SH::kLoads];
+    // Which rows a fragment holds.  D's lane of a 16 x 16 has 4 rows 4 g ..
+    // 4 g + 3 (g = lane / 16) of column lane % 16.  Rows and columns of D are
+    // dealt to the fragments so that a lane's values lie side by side:
+    //   fragments f, f + 1 (f even): its 4 + 4 rows are 8 in a row of P,
+    //     32 (f / 2) + 8 g + 4 (f % 2) + 0..3
+    //   fragments 0 .. FJ-1 along j: its columns are FJ in a row of Q,
+    //     FJ (lane % 16) + 0..FJ-1
+    // so out[j][i] is written 16 bytes a lane, 64 in a row, and its transpose
+    // out[i][j] 2 FJ bytes a lane, 32 FJ in a row, straight from registers.
+    //
+    // A stage's row is 64 k, 128 bytes, in 16-byte pieces.  Piece c of a row
+    // is stored at c ^ sw(row), with sw(row) spreading the 16 rows that a
+    // fragment reads at one k over all eight places.  A load instruction
+    // fills 1 KiB of LDS in lane order, 8 rows, so the lane fetches the piece
+    // that belongs at its place.
+    const bool isP = wave < SH::kWaves / 2;
+    const char* const base = reinterpret_cast<const char*>(
+        isP ? P + (int64_t)i0 * nk : Q + (int64_t)j0 * nk);
+    const int64_t lo = 2 * (isP ? plo : qlo);       // bytes to the low parts
+    const int loSeg = isP ? 2 : 1;                  // and when they are read
+    uint32_t voff[NL];
 #pragma unroll
-    for (int q = 0; q < SH::kLoads; ++q) {
-        const int u = wave * SH::kLoads + q;
-        const bool isP = u < BT / 8;
+    for (int q = 0; q < NL; ++q) {
+        const int u = wave * NL + q;
         const int row = (isP ? u : u - BT / 8) * 8 + lane / 8;
         const int lim = isP ? ni - i0 : nj - j0;
         const int r = row < lim ? row : lim - 1;
-        base[q] = reinterpret_cast<const char*>(
-            isP ? P + (int64_t)i0 * nk : Q + (int64_t)j0 * nk);
-        voff[q] = (uint32_t)r * nk * 2 + ((lane & 7) ^ (lane >> 3)) * 16;
+        const int sw = isP ? (row & 3) | ((row >> 1) & 4) : (row / FJ) & 7;
+        voff[q] = (uint32_t)r * nk * 2 + ((lane & 7) ^ sw) * 16;
     }
-    const int nkt = nk / SH::BK;
+    const int nkt = nk / 64;
     const int total = FULL ? 3 * nkt : nkt;
-    auto load = [&](char* lds, int kt) {
-        int64_t dp = 0, dq = 0;
+    int seg = 0, kseg = 0;                          // of the next stage
+    auto load = [&](char* lds) {
+        const char* s = base + (int64_t)kseg * kRow;
         if constexpr (FULL) {
-            const int seg = kt / nkt;
-            kt -= seg * nkt;
-            dq = seg == 1 ? 2 * qlo : 0;
-            dp = seg == 2 ? 2 * plo : 0;
+            s += seg == loSeg ? lo : 0;
+            if (++kseg == nkt) {
+                kseg = 0;
+                ++seg;
+            }
+        } else {
+            ++kseg;
         }
 #pragma unroll
-        for (int q = 0; q < SH::kLoads; ++q) {
-            const int u = wave * SH::kLoads + q;
-            const char* const s = base[q] + (u < BT / 8 ? dp : dq) +
-                                  (int64_t)kt * (SH::BK * 2);
-            __builtin_amdgcn_global_load_lds((gptr*)(s + voff[q]),
-                                             (lptr*)(lds + u * 1024), 16, 0,
-                                             0);
-        }
+        for (int q = 0; q < NL; ++q)
+            __builtin_amdgcn_global_load_lds(
+                (gptr*)(s + voff[q]), (lptr*)(lds + (wave * NL + q) * 1024),
+                16, 0, 0);
     };
 
     f32x4 acc[FI][FJ];
@@ -600,265 +720,227 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
             acc[i][j] = f32x4{0, 0, 0, 0};
-    const int frow = (lane & 15) * (SH::BK * 2);
-    const int fi = wi * FI * 16 * (SH::BK * 2) + frow;
-    const int fj = SH::kHalf + wj * FJ * 16 * (SH::BK * 2) + frow;
-    const int fc = ((lane >> 4) ^ (lane & 7)) * 16;
-    auto compute = [&](const char* lds) {
+    const int l16 = lane & 15, g = lane >> 4;
+    const int fi = (wi * FI * 16 + (l16 >> 2) * 8 + (l16 & 3)) * kRow;
+    const int fj = SH::kHalf + (wj * FJ * 16 + l16 * FJ) * kRow;
+    const int fc = (g ^ (l16 & 7)) * 16;    // sw(row) = l16 & 7 for both
+    f16x8 x[FI], y[FJ];
+    auto read = [&](const char* lds, int ks) {
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-            f16x8 x[FI], y[FJ];
+        for (int j = 0; j < FJ; ++j)
+            y[j] = *reinterpret_cast<const f16x8*>(lds + fj + j * kRow +
+                                                   (fc ^ (ks * 64)));
 #pragma unroll
-            for (int i = 0; i < FI; ++i)
-                x[i] = *reinterpret_cast<const f16x8*>(
-                    lds + fi + i * 16 * SH::BK * 2 + (fc ^ (ks * 64)));
+        for (int i = 0; i < FI; ++i)
+            x[i] = *reinterpret_cast<const f16x8*>(
+                lds + fi + (i / 2 * 32 + i % 2 * 4) * kRow + (fc ^ (ks * 64)));
+    };
+    auto multiply = [&]() {
+#pragma unroll
+        for (int i = 0; i < FI; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
-                y[j] = *reinterpret_cast<const f16x8*>(
-                    lds + fj + j * 16 * SH::BK * 2 + (fc ^ (ks * 64)));
-#pragma unroll
-            for (int i = 0; i < FI; ++i)
-#pragma unroll
-                for (int j = 0; j < FJ; ++j)
-                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                        x[i], y[j], acc[i][j], 0, 0, 0);
-        }
+                acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                    x[i], y[j], acc[i][j], 0, 0, 0);
     };
 
-    // Two stages: at the top of a turn the barrier (which waits for this
-    // wave's loads) makes the stage to be read whole and the other one free.
-    load(lds0, 0);
-    for (int kt = 0; kt < total; kt += 2) {
-        __syncthreads();
-        if (kt + 1 < total)
-            load(lds1, kt + 1);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(lds0);
-        if (kt + 1 >= total)
-            break;
-        __syncthreads();
-        if (kt + 2 < total)
-            load(lds0, kt + 2);
-        __builtin_amdgcn_sched_barrier(0);
-        compute(lds1);
+    if constexpr (SH::kWaves == 8) {
+        // The waves of a SIMD (w and w + 4) run one slot apart: while one
+        // multiplies, the other reads its fragments and issues loads.  A
+        // stage takes a wave four slots: read, multiply (k 0..31), read,
+        // multiply (k 32..63), each ended by a barrier.  The loads for the
+        // next stage go out in the first; they have landed for every wave
+        // when it waits for its own before the barrier that ends the third,
+        // the later half one slot before the earlier half reads them.  They
+        // overwrite what was read two slots earlier or before, and each read
+        // has returned before the barrier that ends its slot.
+        auto stage = [&](const char* cur, char* next, int kt) {
+            if (kt + 1 < total)
+                load(next);
+            read(cur, 0);
+            __builtin_amdgcn_s_waitcnt(wait_count(63, 0));
+            slot_barrier();
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            slot_barrier();
+            read(cur, 1);
+            __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+            slot_barrier();
+            __builtin_amdgcn_s_setprio(1);
+            multiply();
+            __builtin_amdgcn_s_setprio(0);
+            slot_barrier();
+        };
+        load(lds0);
+        __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+        slot_barrier();
+        if (wave >= 4)
+            slot_barrier();
+        for (int kt = 0; kt < total; kt += 2) {
+            stage(lds0, lds1, kt);
+            if (kt + 1 < total)
+                stage(lds1, lds0, kt + 1);
+        }
+        if (wave < 4)
+            slot_barrier();
+    } else {
+        // ST - 1 stages in flight: stage kt is whole when at most the loads
+        // of the ST - 2 younger ones are out, and the barrier, which every
+        // wave reaches with its reads returned, also frees the stage before.
+        auto stage = [&](const char* cur, char* next, int kt) {
+            if (kt + ST - 2 < total)
+                __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 0));
+            else
+                __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+            slot_barrier();
+            if (kt + ST - 1 < total)
+                load(next);
+#pragma unroll
+            for (int ks = 0; ks < 2; ++ks) {
+                read(cur, ks);
+                multiply();
+            }
+        };
+        static_assert(SH::kWaves == 8 || ST == 4, "four stages");
+        load(lds0);
+        if (total > 1)
+            load(lds1);
+        if (total > 2)
+            load(lds2);
+        for (int kt = 0; kt < total; kt += 4) {
+            stage(lds0, lds3, kt);
+            if (kt + 1 < total)
+                stage(lds1, lds0, kt + 1);
+            if (kt + 2 < total)
+                stage(lds2, lds1, kt + 2);
+            if (kt + 3 < total)
+                stage(lds3, lds2, kt + 3);
+        }
     }
-    __syncthreads();
 
-    // Epilogue.  A lane holds D[i .. i+3][j]: i = 4 (lane / 16) + 0..3 and
-    // j = lane % 16 of each 16 x 16.  Row-major out[j][i] takes them as they
-    // are; out[i][j] goes through LDS, 32 rows of a wave at a time.
-    const int li = i0 + wi * FI * 16 + (lane >> 4) * 4;
-    const int lj = j0 + wj * FJ * 16 + (lane & 15);
-    constexpr int kLd = FJ * 16 + 8;            // halves per staged row
-    static_assert(32 * kLd * 2 * SH::kWaves <= 2 * SH::kHalf, "staging");
-    f16* const stage = reinterpret_cast<f16*>(lds0) + wave * 32 * kLd;
-    // out[i][j] for the wave's rows 16 f .. 16 f + 31, values v[2][FJ]
-    auto transposed = [&](f16* out, int64_t ld, int f,
-                          const f16x4 (&v)[2][FJ]) {
-#pragma unroll
-        for (int h = 0; h < 2; ++h)
-#pragma unroll
-            for (int j = 0; j < FJ; ++j)
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    stage[(h * 16 + (lane >> 4) * 4 + q) * kLd + j * 16 +
-                          (lane & 15)] = v[h][j][q];
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-        constexpr int kPer = FJ * 2;            // 16-byte pieces per row
-#pragma unroll
-        for (int q = 0; q < 32 * kPer / 64; ++q) {
-            const int s = q * 64 + lane;
-            const int r = s / kPer, c = s % kPer * 8;
-            const int i = i0 + wi * FI * 16 + f * 16 + r;
-            const int j = j0 + wj * FJ * 16 + c;
-            if (i < ni && j < nj)
-                *reinterpret_cast<f16x8*>(out + i * ld + j) =
-                    *reinterpret_cast<const f16x8*>(stage + r * kLd + c);
-        }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
-    };
-
+    // Epilogue, from registers (the map of rows and columns is above).
     const int64_t mat = (int64_t)b * rp * cp;
     const f16* const xin = w.xd(a.parity) + mat;
-    const f16* const am = w.a() + (int64_t)b * mp * mp;
-    const float* const da = w.da() + (int64_t)b * mp;
-    const float* const db = w.db() + (int64_t)b * mp;
+    f16* const am = w.a() + (int64_t)b * mp * mp;
+    f16* const bm = w.b() + (int64_t)b * mp * mp;
+    float* const da = w.da() + (int64_t)b * mp;
+    float* const db = w.db() + (int64_t)b * mp;
+    f16* const out = EPI == kGram ? am
+                     : EPI == kPoly ? bm : w.xd(1 - a.parity) + mat;
+    f16* const outT = kTri ? out : w.xt(1 - a.parity) + mat;
+    const int64_t olo = kTri ? w.S : w.E;
+    const int ld = kTri ? mp : cp, ldT = kTri ? mp : rp;
+    const int jb = j0 + (wj * 16 + l16) * FJ;
 #pragma unroll
     for (int f = 0; f < FI; f += 2) {
-        f16x4 vh[2][FJ], vl[2][FJ];
+        const int i = i0 + wi * FI * 16 + f * 16 + g * 8;
+        if (i >= ni)
+            continue;
+        f16x8 vh[FJ], vl[FJ];
 #pragma unroll
-        for (int h = 0; h < 2; ++h)
+        for (int jf = 0; jf < FJ; ++jf) {
+            const int j = jb + jf;
+            if (j >= nj)
+                continue;
+            float d[8], v[8];               // v: the result, times kScale
 #pragma unroll
-            for (int jf = 0; jf < FJ; ++jf) {
-                const int i = li + (f + h) * 16, j = lj + jf * 16;
-                const f32x4 d = acc[f + h][jf];
-                vh[h][jf] = f16x4{0, 0, 0, 0};
-                vl[h][jf] = f16x4{0, 0, 0, 0};
-                if (i >= ni || j >= nj)
-                    continue;
-                f32x4 v;                        // the result, times kScale
-                if constexpr (EPI == kGram) {
+            for (int q = 0; q < 8; ++q)
+                d[q] = acc[f + q / 4][jf][q % 4] * kUnscale;
+            if constexpr (EPI == kGram) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        v[q] = d[q] * kUnscale;
-                        if (i + q == j) {
-                            (w.da() + (int64_t)b * mp)[j] = d[q] * kUnscale2;
-                            v[q] = 0;
-                        }
-                    }
-                } else if constexpr (EPI == kPoly) {
-                    const int64_t o = (int64_t)j * mp + i;
-                    const f16x4 rh = *reinterpret_cast<const f16x4*>(am + o);
-                    f16x4 rl = {0, 0, 0, 0};
-                    if constexpr (FULL)
-                        rl = *reinterpret_cast<const f16x4*>(am + w.S + o);
-                    const f32x4 di =
-                        *reinterpret_cast<const f32x4*>(da + i);
-                    const float dj = da[j];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float r = (float)rh[q] + (float)rl[q];
-                        const float sq = d[q] * kUnscale + (di[q] + dj) * r;
-                        v[q] = a.b * r + a.c * sq;
-                        if (i + q == j) {
-                            (w.db() + (int64_t)b * mp)[j] =
-                                a.a + (a.b * dj + a.c * (d[q] * kUnscale2 +
-                                                         dj * dj));
-                            v[q] = 0;
-                        }
-                    }
-                } else {
-                    const int64_t o = (int64_t)j * cp + i;
-                    const f16x4 xh = *reinterpret_cast<const f16x4*>(xin + o);
-                    const f16x4 xl =
-                        *reinterpret_cast<const f16x4*>(xin + w.E + o);
-                    f32x4 di;
-                    if (tall)
-                        di = *reinterpret_cast<const f32x4*>(db + i);
-                    else
-                        di = f32x4{1, 1, 1, 1} * db[j];
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        v[q] = di[q] * ((float)xh[q] + (float)xl[q]) +
-                               d[q] * kUnscale;
-                }
-                if constexpr (EPI == kGram || EPI == kPoly ||
-                              EPI == kUpdate) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        f16 x, y;
-                        split(v[q], x, y);
-                        vh[h][jf][q] = x;
-                        vl[h][jf][q] = y;
-                    }
-                    f16* const out = EPI == kGram
-                                         ? w.a() + (int64_t)b * mp * mp
-                                     : EPI == kPoly
-                                         ? w.b() + (int64_t)b * mp * mp
-                                         : w.xd(1 - a.parity) + mat;
-                    const int64_t o =
-                        (int64_t)j * (EPI == kUpdate ? cp : mp) + i;
-                    *reinterpret_cast<f16x4*>(out + o) = vh[h][jf];
-                    if constexpr (FULL || EPI == kUpdate)
-                        *reinterpret_cast<f16x4*>(
-                            out + (EPI == kUpdate ? w.E : w.S) + o) =
-                            vl[h][jf];
-                } else if constexpr (EPI == kOutBf16 || EPI == kOutF32) {
-                    const OutMat& om = a.out[p];
-                    if (i >= m.C || j >= m.R)
-                        continue;
-                    const int64_t o = b * om.batch + j * om.row + i;
-                    f32x4 x;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        x[q] = v[q] * kUnscale;
-                    if constexpr (EPI == kOutF32) {
-                        float* const op = static_cast<float*>(om.o) + o;
-                        if (om.vec) {
-                            *reinterpret_cast<f32x4*>(op) = x;
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (i + q < m.C)
-                                    op[q] = x[q];
-                        }
-                    } else {
-                        uint16_t* const op =
-                            static_cast<uint16_t*>(om.o) + o;
-                        if (om.vec) {
-                            *reinterpret_cast<u32x2*>(op) =
-                                u32x2{to_bf16(x[0]) | (to_bf16(x[1]) << 16),
-                                      to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
-                        } else {
-#pragma unroll
-                            for (int q = 0; q < 4; ++q)
-                                if (i + q < m.C)
-                                    op[q] = (uint16_t)to_bf16(x[q]);
-                        }
-                    }
-                } else {
-                    const StepMat& sm = a.st[p];
-                    if (i >= m.C || j >= m.R)
-                        continue;
-                    const int64_t e =
-                        ((int64_t)b * m.R + j) * m.C + i;
-                    if (m.C % 4 == 0) {
-                        f32x4* const mp4 = reinterpret_cast<f32x4*>(
-                            sm.state + e / kTile * 3 * kTile + e % kTile);
-                        f32x4 x = *mp4;
-                        uint32_t h4[4];
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            const float t = x[q] * a.dec;
-                            const float u = sm.s * (v[q] * kUnscale);
-                            x[q] = t - u;
-                            h4[q] = to_bf16(x[q]);
-                        }
-                        *mp4 = x;
-                        const u32x2 hb = {h4[0] | (h4[1] << 16),
-                                          h4[2] | (h4[3] << 16)};
-                        if (sm.pshard)
-                            *reinterpret_cast<u32x2*>(sm.pshard + e) = hb;
-                        if (sm.flat)
-                            *reinterpret_cast<u32x2*>(sm.flat + e) = hb;
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 4; ++q) {
-                            if (i + q >= m.C)
-                                continue;
-                            const int64_t eq = e + q;
-                            float* const m1 = sm.state +
-                                              eq / kTile * 3 * kTile +
-                                              eq % kTile;
-                            const float t = *m1 * a.dec;
-                            const float u = sm.s * (v[q] * kUnscale);
-                            const float x = t - u;
-                            *m1 = x;
-                            const uint16_t hb = (uint16_t)to_bf16(x);
-                            if (sm.pshard)
-                                sm.pshard[eq] = hb;
-                            if (sm.flat)
-                                sm.flat[eq] = hb;
-                        }
+                for (int q = 0; q < 8; ++q) {
+                    v[q] = d[q];
+                    if (i + q == j) {
+                        da[j] = d[q] * kUnscale;
+                        v[q] = 0;
                     }
                 }
-            }
-        if constexpr (EPI == kGram || EPI == kPoly) {
-            // the other triangle
-            if (ti != tj) {
-                f16* const out = (EPI == kGram ? w.a() : w.b()) +
-                                 (int64_t)b * mp * mp;
-                transposed(out, mp, f, vh);
+            } else if constexpr (EPI == kPoly) {
+                const int64_t o = (int64_t)j * mp + i;
+                const f16x8 rh = *reinterpret_cast<const f16x8*>(am + o);
+                f16x8 rl;
                 if constexpr (FULL)
-                    transposed(out + w.S, mp, f, vl);
+                    rl = *reinterpret_cast<const f16x8*>(am + w.S + o);
+                alignas(16) float di[8];
+                *reinterpret_cast<f32x4*>(di) =
+                    *reinterpret_cast<const f32x4*>(da + i);
+                *reinterpret_cast<f32x4*>(di + 4) =
+                    *reinterpret_cast<const f32x4*>(da + i + 4);
+                const float dj = da[j];
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    float r = (float)rh[q];
+                    if constexpr (FULL)
+                        r = r + (float)rl[q];
+                    v[q] = a.b * r + a.c * (d[q] + (di[q] + dj) * r);
+                    if (i + q == j) {
+                        db[j] = a.a + (a.b * dj +
+                                       a.c * (d[q] * kUnscale + dj * dj));
+                        v[q] = 0;
+                    }
+                }
+            } else {
+                const int64_t o = (int64_t)j * cp + i;
+                const f16x8 xh = *reinterpret_cast<const f16x8*>(xin + o);
+                const f16x8 xl =
+                    *reinterpret_cast<const f16x8*>(xin + w.E + o);
+                alignas(16) float di[8];
+                if (tall) {
+                    *reinterpret_cast<f32x4*>(di) =
+                        *reinterpret_cast<const f32x4*>(db + i);
+                    *reinterpret_cast<f32x4*>(di + 4) =
+                        *reinterpret_cast<const f32x4*>(db + i + 4);
+                } else {
+                    const float dj = db[j];
+#pragma unroll
+                    for (int q = 0; q < 8; ++q)
+                        di[q] = dj;
+                }
+#pragma unroll
+                for (int q = 0; q < 8; ++q)
+                    v[q] = di[q] * ((float)xh[q] + (float)xl[q]) + d[q];
             }
-        } else if constexpr (EPI == kUpdate) {
-            f16* const out = w.xt(1 - a.parity) + mat;
-            transposed(out, rp, f, vh);
-            if constexpr (FULL)
-                transposed(out + w.E, rp, f, vl);
+            if constexpr (EPI == kGram || EPI == kPoly || EPI == kUpdate) {
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    f16 h, l;
+                    split(v[q], h, l);
+                    vh[jf][q] = h;
+                    vl[jf][q] = l;
+                }
+                const int64_t o = (int64_t)j * ld + i;
+                *reinterpret_cast<f16x8*>(out + o) = vh[jf];
+                if constexpr (FULL || EPI == kUpdate)
+                    *reinterpret_cast<f16x8*>(out + olo + o) = vl[jf];
+            } else if (j < m.R) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (i + 4 * h < m.C)
+                        finish<EPI>(a, p, m, b, j, i + 4 * h, v + 4 * h);
+            }
+        }
+        // the other triangle (a tile on the diagonal holds both), or X^T
+        if constexpr (EPI == kGram || EPI == kPoly || EPI == kUpdate) {
+            if (jb < nj && (!kTri || ti != tj)) {
+                static_assert(FJ == 2 || FJ == 4, "columns of a lane");
+                typedef f16 cols __attribute__((ext_vector_type(FJ)));
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int64_t o = (int64_t)(i + q) * ldT + jb;
+                    cols t;
+#pragma unroll
+                    for (int jf = 0; jf < FJ; ++jf)
+                        t[jf] = vh[jf][q];
+                    *reinterpret_cast<cols*>(outT + o) = t;
+                    if constexpr (FULL) {
+#pragma unroll
+                        for (int jf = 0; jf < FJ; ++jf)
+                            t[jf] = vl[jf][q];
+                        *reinterpret_cast<cols*>(outT + olo + o) = t;
+                    }
+                }
+            }
         }
     }
 }
@@ -990,20 +1072,60 @@ uint32_t set_starts(Group& g, Fn fn)
     return n;
 }
 
-typedef Shape<128, 2, 2> Shape128;
+// Tiles of one matrix's D in a product.
+template <int BT, int EPI>
+uint32_t d_tiles(const Mat& m)
+{
+    const int32_t rp = padded(m.R), cp = padded(m.C);
+    if (EPI == kGram || EPI == kPoly)
+        return tri_tiles<BT>(rp < cp ? rp : cp);
+    return ((rp + BT - 1) / BT) * ((cp + BT - 1) / BT);
+}
 
 template <class SH, int EPI, bool FULL>
 int launch_gemm(GemmArgs& a, hipStream_t s)
 {
-    const uint32_t n = set_starts(a.g, [](const Mat& m) -> uint32_t {
-        const int32_t rp = padded(m.R), cp = padded(m.C);
-        if (EPI == kGram || EPI == kPoly)
-            return tri_tiles<SH::BT>(rp < cp ? rp : cp);
-        return ((rp + SH::BT - 1) / SH::BT) * ((cp + SH::BT - 1) / SH::BT);
-    });
+    const uint32_t n = set_starts(a.g, d_tiles<SH::BT, EPI>);
     hipLaunchKernelGGL((ns_gemm_kernel<SH, EPI, FULL>), dim3(n),
                        dim3(SH::kThreads), 0, s, a);
     return check_launch("Newton-Schulz product");
+}
+
+// Time of a launch in tiles of one size, in us: `stage` per 64 k and `fixed`
+// per tile, both with `resident` tiles on each of the 256 CUs, or `alone`
+// per 64 k while there is at most one.
+template <int BT, int EPI>
+double estimate(const Group& g, double stage, double alone, double fixed,
+                int resident)
+{
+    double work = 0, longest = 0;
+    int64_t n = 0;
+    for (int p = 0; p < g.count; ++p) {
+        const Mat& m = g.m[p];
+        const int32_t rp = padded(m.R), cp = padded(m.C);
+        const int nk = ((EPI == kGram) == (rp < cp) ? cp : rp) / 64;
+        const int64_t t = (int64_t)m.batch * d_tiles<BT, EPI>(m);
+        n += t;
+        work += (double)t * (nk * stage + fixed);
+        const double one = nk * alone + fixed;
+        longest = one > longest ? one : longest;
+    }
+    if (n <= 256) return longest;
+    const int64_t slots = 256 * resident;
+    return (double)((n + slots - 1) / slots) * (work / (double)n);
+}
+
+template <int EPI, bool FULL>
+int launch_product(GemmArgs& a, hipStream_t s)
+{
+    const double t256 = estimate<256, EPI>(a.g, 1.6, 1.6, 12, 1);
+    const double t128 = estimate<128, EPI>(a.g, 0.98, 0.6, 6, 2);
+    const double t64 = estimate<64, EPI>(a.g, 0.36, 0.25, 3, 2);
+    if (t256 <= t128 && t256 <= t64)
+        return launch_gemm<Shape256, EPI, FULL>(a, s);
+    if (t128 <= t64)
+        return launch_gemm<Shape128, EPI, FULL>(a, s);
+    return launch_gemm<Shape64, EPI, FULL>(a, s);
 }
 
 // The steps on a group whose X[0] is in the workspace; LAST: the epilogue of
@@ -1016,12 +1138,12 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         a.a = ns.coef[k][0];
         a.b = ns.coef[k][1];
         a.c = ns.coef[k][2];
-        int rc = launch_gemm<Shape128, kGram, FULL>(a, s);
-        if (!rc) rc = launch_gemm<Shape128, kPoly, FULL>(a, s);
+        int rc = launch_product<kGram, FULL>(a, s);
+        if (!rc) rc = launch_product<kPoly, FULL>(a, s);
         if (!rc)
             rc = k + 1 < ns.steps
-                     ? launch_gemm<Shape128, kUpdate, FULL>(a, s)
-                     : launch_gemm<Shape128, LAST, FULL>(a, s);
+                     ? launch_product<kUpdate, FULL>(a, s)
+                     : launch_product<LAST, FULL>(a, s);
         if (rc) return rc;
     }
     return ZS_OK;

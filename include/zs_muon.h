@@ -46,11 +46,15 @@ extern "C" {
  *   ZS_NS_FAST  one product each.  X itself is kept in 22 bits (a pair of
  *     fp16 values) and enters the a X term and the diagonals of A and of
  *     b A + c A A enter exactly, so that rounding does not pile up from
- *     step to step: about 1e-3 of the result's norm or less after five
- *     standard steps, also for matrices of low rank, where rounding X alone
- *     to bf16 loses a third of it.
+ *     step to step: about 1e-3 of the result's norm after five standard
+ *     steps, 3e-3 at most in the matrices tried, also those of low rank,
+ *     where rounding X alone to bf16 loses a third of it.
  *   ZS_NS_FULL  three products each (high x high, high x low, low x high),
  *     22 bits throughout: about 1e-5 or less, what fp32 products give.
+ * Two steps are taken together, as products of m x m matrices, where that is
+ * less work (m the smaller side; it goes by the shapes of all matrices of a
+ * call, so a matrix's result may differ by its rounding from one call's
+ * company to another's).
  * Range: the entries of X, A and b A + c A A must stay below 63 in
  * magnitude, which singular values under 2 and the usual coefficients never
  * leave; past it the result is not finite. */

@@ -48,36 +48,64 @@ def _f16(x):
         return (x * 1024).astype(np.float16).astype(np.float64) / 1024
 
 
-def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False):
-    """One matrix, with the library's fp16 roundings and exact sums."""
+def chain_of(steps, pairs):
+    """Steps taken together: twos, an odd count's single one second."""
+    if not pairs:
+        return [1] * steps
+    out = [2] * (steps // 2)
+    if steps % 2:
+        out.insert(1, 1)
+    return out
+
+
+def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):
+    """One matrix, with the library's fp16 roundings and exact sums; `pairs`:
+    two steps taken together on the smaller side, as the library does where
+    that is less work."""
     U = np.asarray(U, np.float64)
     if U.shape[0] > U.shape[1]:
-        return rounded(U.T, steps, coef, eps, full).T
+        return rounded(U.T, steps, coef, eps, full, pairs).T
 
     def pair(x):
         hi = _f16(x)
         return hi, _f16(x - hi)
 
-    def product(p, q):
+    def times(p, q):
         s = p[0] @ q[0]
         return s + p[0] @ q[1] + p[1] @ q[0] if full else s
 
-    def parts(M):
-        """fp16 without the diagonal (a pair if full), and the diagonal."""
+    def square(M):
+        """fp16 without the diagonal (a pair if full), and the diagonal; one
+        triangle counts for both."""
+        M = np.tril(M) + np.tril(M, -1).T
         d = M.diagonal().copy()
-        R = M - np.diag(d)
-        h, l = pair(R)
+        h, l = pair(M - np.diag(d))
         return (h, l if full else np.zeros_like(l)), d
+
+    def whole(M):
+        return M[0][0] + M[0][1] + np.diag(M[1])
+
+    def product(M, N):
+        (R, d), (S, f) = M, N
+        return (times(R, S) + d[:, None] * (S[0] + S[1]) +
+                (R[0] + R[1]) * f[None] + np.diag(d * f))
 
     X = start(U, eps)
     rows = rows_of(coef, steps)
-    for k, (a, b, c) in enumerate(rows):
+    k = 0
+    for many in chain_of(steps, pairs):
         x = pair(X)
-        R, d = parts(product(x, (x[0].T, x[1].T)))
-        r = R[0] + R[1]
-        S = product(R, R) + (d[:, None] + d[None]) * r + np.diag(d * d)
-        R, e = parts(b * (r + np.diag(d)) + c * S)
-        X = (a + e)[:, None] * (x[0] + x[1]) + product(R, x)
+        A = square(times(x, (x[0].T, x[1].T)))
+        E = None
+        for q in range(many):
+            a, b, c = rows[k]
+            k += 1
+            M = b * whole(A) + c * product(A, A)
+            C = square(M + a * np.eye(len(M)))
+            E = C if E is None else square(product(C, E))
+            if q + 1 < many:
+                A = square(product(square(product(C, A)), C))
+        X = E[1][:, None] * (x[0] + x[1]) + times(E[0], x)
     return X
 
 

@@ -1,7 +1,9 @@
 """zs_orthogonalize and zs_muon_step on the GPU against the float64 oracle.
 
 Tolerances.  What the documented fp16 roundings cost on a test's own inputs
-is computed on the CPU (oracle.muon.rounded: float64 with those roundings).
+is computed on the CPU (oracle.muon.rounded: float64 with those roundings,
+steps one by one and in twos: which of them a call takes goes by the sizes of
+all its matrices).
 The kernels make the same roundings of values that differ in their last
 bits, so their error is another draw of the same size: they are held to
 twice the oracle's, plus 2^-18 for fp32 sums and the statistics of small
@@ -72,7 +74,8 @@ def bound(U, exact, precision, out, steps=5, coef=OM.COEF, eps=1e-7):
     if precision == "full":
         t = 2.0 ** -13
     else:
-        t = 2 * rel(OM.rounded(U, steps, coef, eps), exact) + 2.0 ** -18
+        t = 2 * max(rel(OM.rounded(U, steps, coef, eps, pairs=p), exact)
+                    for p in (False, True)) + 2.0 ** -18
     return t + (2.0 ** -8 if out == torch.bfloat16 else 0)
 
 
@@ -163,6 +166,35 @@ def test_strides_and_alignment(dtype, pitch, off):
     assert torch.equal(ob, keep)            # nothing else was written
 
 
+@pytest.mark.parametrize("precision", ["fast", "full"])
+@pytest.mark.parametrize("shape", [(2, 1984, 2050), (5, 900, 2304),
+                                   (3, 2304, 1100), (36, 700, 330),
+                                   (1, 256, 20000)],
+                         ids=lambda s: "%dx%dx%d" % s)
+def test_large_tiles(shape, precision):
+    """Sizes at which the larger tiles carry the products, one matrix of the
+    stack against float64 on the GPU."""
+    g = torch.Generator(device="cuda").manual_seed(sum(shape))
+    x = torch.randn(shape, generator=g, device="cuda")
+    o = run([x], [torch.empty_like(x)], precision)[0]
+    for k in (0, shape[0] - 1):
+        U = x[k].double()
+        U = (U.t() if shape[1] > shape[2] else U).contiguous()
+        X = U / (U.norm() + np.float64(np.float32(1e-7)))
+        a, b, c = OM.COEF
+        for _ in range(5):
+            A = X @ X.t().contiguous()
+            X = a * X + (b * A + c * (A @ A)) @ X
+        got = (o[k].t() if shape[1] > shape[2] else o[k]).double()
+        r = ((got - X).norm() / X.norm()).item()
+        # roundings drawn by the million: those of a smaller matrix of the
+        # same proportions, whose errors are the larger ones
+        small = [max(8, s // 8) for s in U.shape]
+        V = matrix(gen(1), *small)
+        t = bound(V, OM.orthogonalize(V), precision, torch.float32)
+        assert r <= t, (r, t)
+
+
 def test_in_place_and_broadcast_input():
     U = matrix(gen(7), 130, 70)
     x = torch.from_numpy(U).cuda()
@@ -187,8 +219,8 @@ def test_group_of_shapes_equals_single_calls():
             if x.numel():
                 s = run([x], [torch.empty_like(x)], precision)[0]
                 ref = s.cpu().numpy()
-                # other tile sizes may carry the product: other order of sums
-                assert rel(o.cpu().numpy(), ref.astype(np.float64)) < 2e-3
+                # steps in twos or one by one, by all sizes of the call
+                assert rel(o.cpu().numpy(), ref.astype(np.float64)) < 2.0 ** -7
                 m = x if x.dim() == 2 else x[-1]
                 check(m.cpu().numpy(), o if x.dim() == 2 else o[-1],
                       precision)

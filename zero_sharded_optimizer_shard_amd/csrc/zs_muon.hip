@@ -69,10 +69,13 @@ struct Mat {
 
 // Where its parts lie: E elements of X, S of A, D of a diagonal, over the
 // whole stack.
-//   Xd[2] hi, lo | Xt[2] hi (lo) | A hi (lo) | B hi (lo) | diagonals of A, B
-//   | partial sums (double)
+//   Xd[2] hi, lo | Xt[2] hi (lo) | kSquares m x m matrices, each hi (lo)
+//   | their diagonals | partial sums (double)
 // The momentum kernel's U (fp32) lies where Xd[1] will be: it is read by the
 // normalising kernel, before the first update writes there.
+constexpr int kSquares = 4;
+enum Square { kA, kC, kT, kC2 };         // what they hold: run_steps
+
 template <bool FULL>
 struct Region {
     char* ws;
@@ -92,18 +95,22 @@ struct Region {
         return (f16*)(ws + 8 * E + (FULL ? 4 : 2) * p * E);
     }
     __host__ __device__ int64_t x_bytes() const { return (FULL ? 16 : 12) * E; }
-    __device__ f16* a() const { return (f16*)(ws + x_bytes()); }
-    __device__ f16* b() const
-    {
-        return (f16*)(ws + x_bytes() + (FULL ? 4 : 2) * S);
-    }
     __host__ __device__ int64_t d_off() const
     {
-        return x_bytes() + (FULL ? 8 : 4) * S;
+        return x_bytes() + (FULL ? 4 : 2) * kSquares * S;
     }
-    __device__ float* da() const { return (float*)(ws + d_off()); }
-    __device__ float* db() const { return da() + D; }
-    __host__ __device__ int64_t parts_off() const { return d_off() + 8 * D; }
+    __host__ __device__ int64_t parts_off() const
+    {
+        return d_off() + 4 * kSquares * D;
+    }
+    __device__ f16* square(int k) const
+    {
+        return (f16*)(ws + x_bytes() + (FULL ? 4 : 2) * k * S);
+    }
+    __device__ float* diag(int k) const
+    {
+        return (float*)(ws + d_off() + 4 * k * D);
+    }
     __device__ double* parts() const { return (double*)(ws + parts_off()); }
     __device__ float* u() const { return (float*)xd(1); }
 };
@@ -416,7 +423,15 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
 
 // ---- the products ------------------------------------------------------------------
 
-enum Epi { kGram, kPoly, kUpdate, kOutBf16, kOutF32, kStep };
+// What a product's epilogue makes of D, and which operands it has:
+//   kGram     A = X X^T
+//   kPoly     C = a + b A + c A A
+//   kProd     the product of two of the squares, which commute
+//   kUpdate   X <- C X; the last one goes to the caller instead: kOutBf16,
+//             kOutF32, or kStep, which steps the weights by it
+enum Epi { kGram, kPoly, kProd, kUpdate, kOutBf16, kOutF32, kStep };
+
+__host__ __device__ constexpr bool symmetric(int epi) { return epi <= kProd; }
 
 struct OutMat {
     void* o;
@@ -438,6 +453,7 @@ struct GemmArgs {
         StepMat st[kMaxMats];
     };
     int32_t parity;                     // which of the two X is read
+    int8_t sp, sq, so;                  // squares: operands and result
     float a, b, c;
     float dec;                          // 1 - lr*wd
 };
@@ -467,6 +483,7 @@ struct Shape {
 // the 128 tile 1090 and 1100, the 64 tile 740), the smaller ones fill the
 // chip where there are few of the larger.
 typedef Shape<256, 2, 4, 2> Shape256;
+typedef Shape<192, 2, 4, 2> Shape192;
 typedef Shape<128, 2, 4, 2> Shape128;
 // Few tiles, bound by the latency of a stage: three in flight.
 typedef Shape<64, 2, 2, 4> Shape64;
@@ -498,6 +515,43 @@ __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t n)
 {
     const uint32_t x = bid & 7, per = n >> 3, rem = n & 7;
     return x * per + (x < rem ? x : rem) + (bid >> 3);
+}
+
+// Eight values of a square, times kScale, from its fp16 parts.
+template <bool FULL>
+__device__ __forceinline__ void load_pair(const f16* p, int64_t lo,
+                                          float (&v)[8])
+{
+    const f16x8 h = *reinterpret_cast<const f16x8*>(p);
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+        v[q] = (float)h[q];
+    if constexpr (FULL) {
+        const f16x8 l = *reinterpret_cast<const f16x8*>(p + lo);
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+            v[q] = v[q] + (float)l[q];
+    }
+}
+
+// A lane's FJ columns of one row, v[0..FJ-1][q]; `left` columns are there.
+template <int FJ>
+__device__ __forceinline__ void store_cols(f16* o, const f16x8 (&v)[FJ],
+                                           int q, int left)
+{
+    if constexpr (FJ == 3) {            // not a vector's size
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+            if (j < left)
+                o[j] = v[j][q];
+    } else {
+        typedef f16 cols __attribute__((ext_vector_type(FJ)));
+        cols t;
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+            t[j] = v[j][q];
+        *reinterpret_cast<cols*>(o) = t;
+    }
 }
 
 // The last update's results v[0..3], times kScale, at row j and columns
@@ -587,7 +641,7 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
 {
     constexpr int BT = SH::BT, FI = SH::FI, FJ = SH::FJ, ST = SH::ST;
     constexpr int kRow = SH::kRow, NL = SH::kLoads;
-    constexpr bool kTri = EPI == kGram || EPI == kPoly;
+    constexpr bool kTri = symmetric(EPI);
     // the stages; separate objects, so that the compiler sees that reading
     // one does not wait for the loads into another
     __shared__ __align__(1024) char lds0[2 * SH::kHalf];
@@ -625,12 +679,13 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                 (int64_t)b * rp * cp;
             nk = tall ? rp : cp;
             plo = w.E;
+            Q = P;
         } else {
-            P = w.a() + (int64_t)b * mp * mp;
+            P = w.square(a.sp) + (int64_t)b * mp * mp;
+            Q = w.square(a.sq) + (int64_t)b * mp * mp;
             nk = mp;
             plo = w.S;
         }
-        Q = P;
         qlo = plo;
     } else {
         ni = cp;
@@ -645,16 +700,16 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         bid -= band * tni;
         tj = band + bid % h;
         ti = bid / h;
-        const f16* const B = w.b() + (int64_t)b * mp * mp;
+        const f16* const C = w.square(a.sp) + (int64_t)b * mp * mp;
         if (tall) {
-            P = B;
+            P = C;
             plo = w.S;
             Q = w.xd(a.parity) + (int64_t)b * rp * cp;
             qlo = w.E;
         } else {
             P = w.xt(a.parity) + (int64_t)b * rp * cp;
             plo = w.E;
-            Q = B;
+            Q = C;
             qlo = w.S;
         }
     }
@@ -822,12 +877,13 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     // Epilogue, from registers (the map of rows and columns is above).
     const int64_t mat = (int64_t)b * rp * cp;
     const f16* const xin = w.xd(a.parity) + mat;
-    f16* const am = w.a() + (int64_t)b * mp * mp;
-    f16* const bm = w.b() + (int64_t)b * mp * mp;
-    float* const da = w.da() + (int64_t)b * mp;
-    float* const db = w.db() + (int64_t)b * mp;
-    f16* const out = EPI == kGram ? am
-                     : EPI == kPoly ? bm : w.xd(1 - a.parity) + mat;
+    const f16* const pm = w.square(a.sp) + (int64_t)b * mp * mp;
+    const f16* const qm = w.square(a.sq) + (int64_t)b * mp * mp;
+    const float* const dp = w.diag(a.sp) + (int64_t)b * mp;
+    const float* const dq = w.diag(a.sq) + (int64_t)b * mp;
+    float* const dout = w.diag(a.so) + (int64_t)b * mp;
+    f16* const out = kTri ? w.square(a.so) + (int64_t)b * mp * mp
+                          : w.xd(1 - a.parity) + mat;
     f16* const outT = kTri ? out : w.xt(1 - a.parity) + mat;
     const int64_t olo = kTri ? w.S : w.E;
     const int ld = kTri ? mp : cp, ldT = kTri ? mp : rp;
@@ -852,31 +908,33 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                 for (int q = 0; q < 8; ++q) {
                     v[q] = d[q];
                     if (i + q == j) {
-                        da[j] = d[q] * kUnscale;
+                        dout[j] = d[q] * kUnscale;
                         v[q] = 0;
                     }
                 }
-            } else if constexpr (EPI == kPoly) {
+            } else if constexpr (EPI == kPoly || EPI == kProd) {
+                // (R + D)(S + F) = R S + D S + R F + D F, D and F diagonal
                 const int64_t o = (int64_t)j * mp + i;
-                const f16x8 rh = *reinterpret_cast<const f16x8*>(am + o);
-                f16x8 rl;
-                if constexpr (FULL)
-                    rl = *reinterpret_cast<const f16x8*>(am + w.S + o);
+                float r[8], t[8];
+                load_pair<FULL>(pm + o, w.S, r);
+                if constexpr (EPI == kProd)
+                    load_pair<FULL>(qm + o, w.S, t);
                 alignas(16) float di[8];
                 *reinterpret_cast<f32x4*>(di) =
-                    *reinterpret_cast<const f32x4*>(da + i);
+                    *reinterpret_cast<const f32x4*>(dp + i);
                 *reinterpret_cast<f32x4*>(di + 4) =
-                    *reinterpret_cast<const f32x4*>(da + i + 4);
-                const float dj = da[j];
+                    *reinterpret_cast<const f32x4*>(dp + i + 4);
+                const float dj = dq[j];
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    float r = (float)rh[q];
-                    if constexpr (FULL)
-                        r = r + (float)rl[q];
-                    v[q] = a.b * r + a.c * (d[q] + (di[q] + dj) * r);
+                    const float sq =
+                        d[q] + (EPI == kProd ? di[q] * t[q] + r[q] * dj
+                                             : (di[q] + dj) * r[q]);
+                    v[q] = EPI == kProd ? sq : a.b * r[q] + a.c * sq;
                     if (i + q == j) {
-                        db[j] = a.a + (a.b * dj +
-                                       a.c * (d[q] * kUnscale + dj * dj));
+                        const float dd = d[q] * kUnscale + di[q] * dj;
+                        dout[j] = EPI == kProd
+                                      ? dd : a.a + (a.b * dj + a.c * dd);
                         v[q] = 0;
                     }
                 }
@@ -888,11 +946,11 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                 alignas(16) float di[8];
                 if (tall) {
                     *reinterpret_cast<f32x4*>(di) =
-                        *reinterpret_cast<const f32x4*>(db + i);
+                        *reinterpret_cast<const f32x4*>(dp + i);
                     *reinterpret_cast<f32x4*>(di + 4) =
-                        *reinterpret_cast<const f32x4*>(db + i + 4);
+                        *reinterpret_cast<const f32x4*>(dp + i + 4);
                 } else {
-                    const float dj = db[j];
+                    const float dj = dp[j];
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
                         di[q] = dj;
@@ -901,7 +959,7 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                 for (int q = 0; q < 8; ++q)
                     v[q] = di[q] * ((float)xh[q] + (float)xl[q]) + d[q];
             }
-            if constexpr (EPI == kGram || EPI == kPoly || EPI == kUpdate) {
+            if constexpr (EPI <= kUpdate) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     f16 h, l;
@@ -921,24 +979,14 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
             }
         }
         // the other triangle (a tile on the diagonal holds both), or X^T
-        if constexpr (EPI == kGram || EPI == kPoly || EPI == kUpdate) {
+        if constexpr (EPI <= kUpdate) {
             if (jb < nj && (!kTri || ti != tj)) {
-                static_assert(FJ == 2 || FJ == 4, "columns of a lane");
-                typedef f16 cols __attribute__((ext_vector_type(FJ)));
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
-                    const int64_t o = (int64_t)(i + q) * ldT + jb;
-                    cols t;
-#pragma unroll
-                    for (int jf = 0; jf < FJ; ++jf)
-                        t[jf] = vh[jf][q];
-                    *reinterpret_cast<cols*>(outT + o) = t;
-                    if constexpr (FULL) {
-#pragma unroll
-                        for (int jf = 0; jf < FJ; ++jf)
-                            t[jf] = vl[jf][q];
-                        *reinterpret_cast<cols*>(outT + olo + o) = t;
-                    }
+                    f16* const o = outT + (int64_t)(i + q) * ldT + jb;
+                    store_cols<FJ>(o, vh, q, nj - jb);
+                    if constexpr (FULL)
+                        store_cols<FJ>(o + olo, vl, q, nj - jb);
                 }
             }
         }
@@ -1077,7 +1125,7 @@ template <int BT, int EPI>
 uint32_t d_tiles(const Mat& m)
 {
     const int32_t rp = padded(m.R), cp = padded(m.C);
-    if (EPI == kGram || EPI == kPoly)
+    if (symmetric(EPI))
         return tri_tiles<BT>(rp < cp ? rp : cp);
     return ((rp + BT - 1) / BT) * ((cp + BT - 1) / BT);
 }
@@ -1119,8 +1167,11 @@ template <int EPI, bool FULL>
 int launch_product(GemmArgs& a, hipStream_t s)
 {
     const double t256 = estimate<256, EPI>(a.g, 1.6, 1.6, 12, 1);
+    const double t192 = estimate<192, EPI>(a.g, 1.0, 1.0, 9, 1);
     const double t128 = estimate<128, EPI>(a.g, 0.98, 0.6, 6, 2);
     const double t64 = estimate<64, EPI>(a.g, 0.36, 0.25, 3, 2);
+    if (t192 < t256 && t192 <= t128 && t192 <= t64)
+        return launch_gemm<Shape192, EPI, FULL>(a, s);
     if (t256 <= t128 && t256 <= t64)
         return launch_gemm<Shape256, EPI, FULL>(a, s);
     if (t128 <= t64)
@@ -1128,25 +1179,76 @@ int launch_product(GemmArgs& a, hipStream_t s)
     return launch_gemm<Shape64, EPI, FULL>(a, s);
 }
 
+// Whether two steps taken on the m x m side cost less than one by one.  In
+// units of m^3 flops with r = n/m, a symmetric product being 1:
+//   one by one   A = X X^T (r), C = a + b A + c A A (1), X <- C X (2 r),
+//                twice: 6 r + 2
+//   together     A (r), C (1), T = C A (1), A' = T C (1), C' from A' (1),
+//                E = C' C (1), X <- E X (2 r): 3 r + 5
+// for A' = C A C is the next step's A: polynomials of one matrix commute.
+// The small directions of A' carry the rounding of the large ones, a^2 times,
+// but only into C', where they count for a^2 b 2^-12; X itself stays exact.  A
+// third step in the same way would multiply that by a^2 = 12 again (a matrix
+// of 1024 x 3584 with singular values 1/k: 2.2e-4 one by one, 1e-3 in twos,
+// 5e-3 in threes), so it is at most two.
+bool in_pairs(const Group& g)
+{
+    double pairs = 0, singles = 0;
+    for (int p = 0; p < g.count; ++p) {
+        const Mat& m = g.m[p];
+        const double rp = padded(m.R), cp = padded(m.C);
+        const double s = rp < cp ? rp : cp, r = (rp < cp ? cp : rp) / s;
+        pairs += m.batch * s * s * s * (3 * r + 5);
+        singles += m.batch * s * s * s * (6 * r + 2);
+    }
+    return pairs < 0.8 * singles;
+}
+
 // The steps on a group whose X[0] is in the workspace; LAST: the epilogue of
 // the last update.
 template <int LAST, bool FULL>
 int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
 {
-    for (int k = 0; k < ns.steps; ++k) {
-        a.parity = k & 1;
+    const bool pairs = in_pairs(a.g);
+    a.parity = 0;
+    int rc = ZS_OK;
+    auto poly = [&](int k, Square out) {
         a.a = ns.coef[k][0];
         a.b = ns.coef[k][1];
         a.c = ns.coef[k][2];
-        int rc = launch_product<kGram, FULL>(a, s);
+        a.sp = a.sq = kA;
+        a.so = out;
         if (!rc) rc = launch_product<kPoly, FULL>(a, s);
+    };
+    auto prod = [&](Square p, Square q, Square out) {
+        a.sp = p;
+        a.sq = q;
+        a.so = out;
+        if (!rc) rc = launch_product<kProd, FULL>(a, s);
+    };
+    for (int k = 0; k < ns.steps && !rc;) {
+        // an odd number of steps: the second by itself, or the only one.  E
+        // is about a a' where A is small and has to stay in fp16's range.
+        const bool two = pairs && k + 1 < ns.steps &&
+                         !(ns.steps % 2 && k == 2) &&
+                         std::fabs(ns.coef[k][0] * ns.coef[k + 1][0]) < 24;
+        a.so = kA;
+        rc = launch_product<kGram, FULL>(a, s);
+        poly(k, kC);
+        if (two) {
+            prod(kC, kA, kT);
+            prod(kT, kC, kA);
+            poly(k + 1, kC2);
+            prod(kC2, kC, kT);
+        }
+        k += two ? 2 : 1;
+        a.sp = two ? kT : kC;
         if (!rc)
-            rc = k + 1 < ns.steps
-                     ? launch_product<kUpdate, FULL>(a, s)
-                     : launch_product<LAST, FULL>(a, s);
-        if (rc) return rc;
+            rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, s)
+                              : launch_product<LAST, FULL>(a, s);
+        a.parity ^= 1;
     }
-    return ZS_OK;
+    return rc;
 }
 
 uint32_t init_tiles(const Mat& m)

@@ -65,6 +65,7 @@ struct Mat {
     int32_t batch;
     int32_t nparts;         // partial sums of squares per matrix
     int32_t chunk;          // elements behind each of them
+    uint32_t tiles;         // workgroups of the present launch
 };
 
 // Where its parts lie: E elements of X, S of A, D of a diagonal, over the
@@ -510,28 +511,12 @@ __host__ __device__ inline uint32_t tri_tiles(int32_t mp)
 }
 
 // Workgroups go to the 8 XCDs in turn; give each XCD a run of neighbouring
-// tiles, whose operands its L2 then holds.
+// tiles of each stack, whose operands its L2 then holds.  A stack's first
+// workgroup is a multiple of 8.
 __device__ __forceinline__ uint32_t xcd_order(uint32_t bid, uint32_t n)
 {
     const uint32_t x = bid & 7, per = n >> 3, rem = n & 7;
     return x * per + (x < rem ? x : rem) + (bid >> 3);
-}
-
-// Eight values of a square, times kScale, from its fp16 parts.
-template <bool FULL>
-__device__ __forceinline__ void load_pair(const f16* p, int64_t lo,
-                                          float (&v)[8])
-{
-    const f16x8 h = *reinterpret_cast<const f16x8*>(p);
-#pragma unroll
-    for (int q = 0; q < 8; ++q)
-        v[q] = (float)h[q];
-    if constexpr (FULL) {
-        const f16x8 l = *reinterpret_cast<const f16x8*>(p + lo);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-            v[q] = v[q] + (float)l[q];
-    }
 }
 
 // A lane's FJ columns of one row, v[0..FJ-1][q]; `left` columns are there.
@@ -556,82 +541,76 @@ __device__ __forceinline__ void store_cols(f16* o, const f16x8 (&v)[FJ],
 
 // The last update's results v[0..3], times kScale, at row j and columns
 // i .. i+3 of matrix b (i a multiple of 4; columns past the last are not
-// there).
+// there), to the caller's matrix.
 template <int EPI>
-__device__ __forceinline__ void finish(const GemmArgs& a, int p, const Mat& m,
-                                       uint32_t b, int j, int i,
-                                       const float* v)
+__device__ __forceinline__ void finish_out(const OutMat& om, const Mat& m,
+                                           uint32_t b, int j, int i,
+                                           const float* v)
 {
-    if constexpr (EPI == kOutBf16 || EPI == kOutF32) {
-        const OutMat& om = a.out[p];
-        const int64_t o = b * om.batch + j * om.row + i;
-        float x[4];
+    const int64_t o = b * om.batch + j * om.row + i;
+    float x[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q)
-            x[q] = v[q] * kUnscale;
-        if constexpr (EPI == kOutF32) {
-            float* const op = static_cast<float*>(om.o) + o;
-            if (om.vec) {
-                *reinterpret_cast<f32x4*>(op) = f32x4{x[0], x[1], x[2], x[3]};
-            } else {
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (i + q < m.C)
-                        op[q] = x[q];
-            }
+    for (int q = 0; q < 4; ++q)
+        x[q] = v[q] * kUnscale;
+    if constexpr (EPI == kOutF32) {
+        float* const op = static_cast<float*>(om.o) + o;
+        if (om.vec) {
+            *reinterpret_cast<f32x4*>(op) = f32x4{x[0], x[1], x[2], x[3]};
         } else {
-            uint16_t* const op = static_cast<uint16_t*>(om.o) + o;
-            if (om.vec) {
-                *reinterpret_cast<u32x2*>(op) =
-                    u32x2{to_bf16(x[0]) | (to_bf16(x[1]) << 16),
-                          to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
-            } else {
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
-                    if (i + q < m.C)
-                        op[q] = (uint16_t)to_bf16(x[q]);
-            }
+            for (int q = 0; q < 4; ++q)
+                if (i + q < m.C)
+                    op[q] = x[q];
         }
     } else {
-        const StepMat& sm = a.st[p];
-        const int64_t e = ((int64_t)b * m.R + j) * m.C + i;
-        float x[4];
-        uint32_t h[4];
-        if (m.C % 4 == 0) {
-            f32x4* const s4 = reinterpret_cast<f32x4*>(
-                sm.state + e / kTile * 3 * kTile + e % kTile);
-            const f32x4 old = *s4;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float t = old[q] * a.dec;
-                const float u = sm.s * (v[q] * kUnscale);
-                x[q] = t - u;
-                h[q] = to_bf16(x[q]);
-            }
-            *s4 = f32x4{x[0], x[1], x[2], x[3]};
-            const u32x2 hb = {h[0] | (h[1] << 16), h[2] | (h[3] << 16)};
-            if (sm.pshard)
-                *reinterpret_cast<u32x2*>(sm.pshard + e) = hb;
-            if (sm.flat)
-                *reinterpret_cast<u32x2*>(sm.flat + e) = hb;
+        uint16_t* const op = static_cast<uint16_t*>(om.o) + o;
+        if (om.vec) {
+            *reinterpret_cast<u32x2*>(op) =
+                u32x2{to_bf16(x[0]) | (to_bf16(x[1]) << 16),
+                      to_bf16(x[2]) | (to_bf16(x[3]) << 16)};
         } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                if (i + q >= m.C)
-                    continue;
-                const int64_t eq = e + q;
-                float* const s1 =
-                    sm.state + eq / kTile * 3 * kTile + eq % kTile;
-                const float t = *s1 * a.dec;
-                const float u = sm.s * (v[q] * kUnscale);
-                x[q] = t - u;
-                *s1 = x[q];
-                h[q] = to_bf16(x[q]);
-                if (sm.pshard)
-                    sm.pshard[eq] = (uint16_t)h[q];
-                if (sm.flat)
-                    sm.flat[eq] = (uint16_t)h[q];
-            }
+            for (int q = 0; q < 4; ++q)
+                if (i + q < m.C)
+                    op[q] = (uint16_t)to_bf16(x[q]);
+        }
+    }
+}
+
+// The same into the weights: by fours where rows are (`st`, already
+// stepped), else one by one.
+__device__ __forceinline__ void finish_step(const GemmArgs& a, int p,
+                                            const Mat& m, uint32_t b, int j,
+                                            int i, bool vec4, const float* v,
+                                            f32x4 st)
+{
+    const StepMat& sm = a.st[p];
+    const int64_t e = ((int64_t)b * m.R + j) * m.C + i;
+    if (vec4) {
+        *reinterpret_cast<f32x4*>(sm.state + e / kTile * 3 * kTile +
+                                  e % kTile) = st;
+        const u32x2 h = {to_bf16(st[0]) | (to_bf16(st[1]) << 16),
+                         to_bf16(st[2]) | (to_bf16(st[3]) << 16)};
+        if (sm.pshard)
+            *reinterpret_cast<u32x2*>(sm.pshard + e) = h;
+        if (sm.flat)
+            *reinterpret_cast<u32x2*>(sm.flat + e) = h;
+    } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            if (i + q >= m.C)
+                continue;
+            const int64_t eq = e + q;
+            float* const s1 = sm.state + eq / kTile * 3 * kTile + eq % kTile;
+            const float t = *s1 * a.dec;
+            const float u = sm.s * (v[q] * kUnscale);
+            const float x = t - u;
+            *s1 = x;
+            const uint16_t h = (uint16_t)to_bf16(x);
+            if (sm.pshard)
+                sm.pshard[eq] = h;
+            if (sm.flat)
+                sm.flat[eq] = h;
         }
     }
 }
@@ -649,9 +628,12 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     __shared__ __align__(1024) char lds2[ST > 2 ? 2 * SH::kHalf : 16];
     __shared__ __align__(1024) char lds3[ST > 3 ? 2 * SH::kHalf : 16];
 
-    uint32_t bid = xcd_order(blockIdx.x, a.g.start[a.g.count]);
+    uint32_t bid = blockIdx.x;
     const int p = find(a.g, bid);
     const Mat& m = a.g.m[p];
+    if (bid >= m.tiles)
+        return;                         // the whole workgroup
+    bid = xcd_order(bid, m.tiles);
     const Region<FULL> w(m.ws, m.R, m.C, m.batch);
     const int32_t rp = padded(m.R), cp = padded(m.C);
     const int32_t mp = rp < cp ? rp : cp;
@@ -888,98 +870,150 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     const int64_t olo = kTri ? w.S : w.E;
     const int ld = kTri ? mp : cp, ldT = kTri ? mp : rp;
     const int jb = j0 + (wj * 16 + l16) * FJ;
+    // What the epilogue reads, fetched for fragments f, f + 1 before the
+    // results of f - 2, f - 1 are stored: vector memory completes in order,
+    // and a load behind a store waits for it.  Past the edges the nearest
+    // values inside are read, and dropped.
+    constexpr bool kX = EPI >= kUpdate;
+    f16x8 inh[FJ], inl[FJ], inh2[FJ], inl2[FJ];
+    f32x4 inS[FJ][2], di0, di1;
+    float dj[FJ];
+    const bool vec4 = m.C % 4 == 0;             // kStep's state by fours
+    auto fetch = [&](int f) {
+        if constexpr (EPI == kGram)
+            return;
+        int i = i0 + wi * FI * 16 + f * 16 + g * 8;
+        i = i < ni ? i : ni - 8;
+        if (!kX || tall) {
+            di0 = *reinterpret_cast<const f32x4*>(dp + i);
+            di1 = *reinterpret_cast<const f32x4*>(dp + i + 4);
+        }
+#pragma unroll
+        for (int jf = 0; jf < FJ; ++jf) {
+            const int j = jb + jf < nj ? jb + jf : nj - 1;
+            const int64_t o = (int64_t)j * ld + i;
+            const f16* const in = kX ? xin : pm;
+            inh[jf] = *reinterpret_cast<const f16x8*>(in + o);
+            if constexpr (FULL || kX)
+                inl[jf] = *reinterpret_cast<const f16x8*>(in + olo + o);
+            if constexpr (EPI == kProd) {
+                inh2[jf] = *reinterpret_cast<const f16x8*>(qm + o);
+                if constexpr (FULL)
+                    inl2[jf] =
+                        *reinterpret_cast<const f16x8*>(qm + olo + o);
+            }
+            if constexpr (EPI == kStep) {
+                if (vec4) {
+                    const int js = j < m.R ? j : m.R - 1;
+                    const int64_t r = ((int64_t)b * m.R + js) * m.C;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int is = i + 4 * h;
+                        const int64_t e = r + (is < m.C ? is : m.C - 4);
+                        inS[jf][h] = *reinterpret_cast<const f32x4*>(
+                            a.st[p].state + e / kTile * 3 * kTile +
+                            e % kTile);
+                    }
+                }
+            }
+        }
+    };
+    if constexpr (EPI != kGram)
+#pragma unroll
+        for (int jf = 0; jf < FJ; ++jf)
+            dj[jf] = (kX ? dp : dq)[jb + jf < nj ? jb + jf : nj - 1];
+    fetch(0);
 #pragma unroll
     for (int f = 0; f < FI; f += 2) {
         const int i = i0 + wi * FI * 16 + f * 16 + g * 8;
-        if (i >= ni)
-            continue;
-        f16x8 vh[FJ], vl[FJ];
+        float v[FJ][8];                     // the results, times kScale
 #pragma unroll
-        for (int jf = 0; jf < FJ; ++jf) {
-            const int j = jb + jf;
-            if (j >= nj)
-                continue;
-            float d[8], v[8];               // v: the result, times kScale
+        for (int jf = 0; jf < FJ; ++jf)
 #pragma unroll
-            for (int q = 0; q < 8; ++q)
-                d[q] = acc[f + q / 4][jf][q % 4] * kUnscale;
-            if constexpr (EPI == kGram) {
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    v[q] = d[q];
-                    if (i + q == j) {
-                        dout[j] = d[q] * kUnscale;
-                        v[q] = 0;
+            for (int q = 0; q < 8; ++q) {
+                const float d = acc[f + q / 4][jf][q % 4] * kUnscale;
+                const float di = q < 4 ? di0[q % 4] : di1[q % 4];
+                if constexpr (EPI == kGram) {
+                    v[jf][q] = d;
+                } else if constexpr (EPI == kPoly || EPI == kProd) {
+                    // (R + D)(S + F) = R S + D S + R F + D F, with D and F
+                    // the diagonals
+                    float r = (float)inh[jf][q];
+                    if constexpr (FULL)
+                        r = r + (float)inl[jf][q];
+                    if constexpr (EPI == kPoly) {
+                        v[jf][q] =
+                            a.b * r + a.c * (d + (di + dj[jf]) * r);
+                    } else {
+                        float t = (float)inh2[jf][q];
+                        if constexpr (FULL)
+                            t = t + (float)inl2[jf][q];
+                        v[jf][q] = d + (di * t + r * dj[jf]);
                     }
-                }
-            } else if constexpr (EPI == kPoly || EPI == kProd) {
-                // (R + D)(S + F) = R S + D S + R F + D F, D and F diagonal
-                const int64_t o = (int64_t)j * mp + i;
-                float r[8], t[8];
-                load_pair<FULL>(pm + o, w.S, r);
-                if constexpr (EPI == kProd)
-                    load_pair<FULL>(qm + o, w.S, t);
-                alignas(16) float di[8];
-                *reinterpret_cast<f32x4*>(di) =
-                    *reinterpret_cast<const f32x4*>(dp + i);
-                *reinterpret_cast<f32x4*>(di + 4) =
-                    *reinterpret_cast<const f32x4*>(dp + i + 4);
-                const float dj = dq[j];
-#pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const float sq =
-                        d[q] + (EPI == kProd ? di[q] * t[q] + r[q] * dj
-                                             : (di[q] + dj) * r[q]);
-                    v[q] = EPI == kProd ? sq : a.b * r[q] + a.c * sq;
-                    if (i + q == j) {
-                        const float dd = d[q] * kUnscale + di[q] * dj;
-                        dout[j] = EPI == kProd
-                                      ? dd : a.a + (a.b * dj + a.c * dd);
-                        v[q] = 0;
-                    }
-                }
-            } else {
-                const int64_t o = (int64_t)j * cp + i;
-                const f16x8 xh = *reinterpret_cast<const f16x8*>(xin + o);
-                const f16x8 xl =
-                    *reinterpret_cast<const f16x8*>(xin + w.E + o);
-                alignas(16) float di[8];
-                if (tall) {
-                    *reinterpret_cast<f32x4*>(di) =
-                        *reinterpret_cast<const f32x4*>(dp + i);
-                    *reinterpret_cast<f32x4*>(di + 4) =
-                        *reinterpret_cast<const f32x4*>(dp + i + 4);
                 } else {
-                    const float dj = dp[j];
+                    v[jf][q] = (tall ? di : dj[jf]) *
+                                   ((float)inh[jf][q] + (float)inl[jf][q]) +
+                               d;
+                }
+            }
+        if constexpr (kTri) {
+            // the diagonal, apart
+            if (ti == tj) {
+#pragma unroll
+                for (int jf = 0; jf < FJ; ++jf)
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        di[q] = dj;
-                }
-#pragma unroll
-                for (int q = 0; q < 8; ++q)
-                    v[q] = di[q] * ((float)xh[q] + (float)xl[q]) + d[q];
+                        if (i + q == jb + jf && i < ni) {
+                            const float d =
+                                acc[f + q / 4][jf][q % 4] * kUnscale *
+                                kUnscale;
+                            const float di = q < 4 ? di0[q % 4] : di1[q % 4];
+                            const float dd =
+                                EPI == kGram ? d : d + di * dj[jf];
+                            dout[i + q] =
+                                EPI == kPoly
+                                    ? a.a + (a.b * dj[jf] + a.c * dd)
+                                    : dd;
+                            v[jf][q] = 0;
+                        }
             }
-            if constexpr (EPI <= kUpdate) {
+        }
+        f32x4 st[FJ][2];
+        if constexpr (EPI == kStep) {
+            if (vec4) {
+#pragma unroll
+                for (int jf = 0; jf < FJ; ++jf)
+#pragma unroll
+                    for (int q = 0; q < 8; ++q) {
+                        const float t = inS[jf][q / 4][q % 4] * a.dec;
+                        const float u = a.st[p].s * (v[jf][q] * kUnscale);
+                        st[jf][q / 4][q % 4] = t - u;
+                    }
+            }
+        }
+        if (f + 2 < FI)
+            fetch(f + 2);
+        if (i >= ni)
+            continue;
+        if constexpr (EPI <= kUpdate) {
+            f16x8 vh[FJ], vl[FJ];
+#pragma unroll
+            for (int jf = 0; jf < FJ; ++jf) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     f16 h, l;
-                    split(v[q], h, l);
+                    split(v[jf][q], h, l);
                     vh[jf][q] = h;
                     vl[jf][q] = l;
                 }
-                const int64_t o = (int64_t)j * ld + i;
-                *reinterpret_cast<f16x8*>(out + o) = vh[jf];
-                if constexpr (FULL || EPI == kUpdate)
-                    *reinterpret_cast<f16x8*>(out + olo + o) = vl[jf];
-            } else if (j < m.R) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (i + 4 * h < m.C)
-                        finish<EPI>(a, p, m, b, j, i + 4 * h, v + 4 * h);
+                if (jb + jf < nj) {
+                    const int64_t o = (int64_t)(jb + jf) * ld + i;
+                    *reinterpret_cast<f16x8*>(out + o) = vh[jf];
+                    if constexpr (FULL || EPI == kUpdate)
+                        *reinterpret_cast<f16x8*>(out + olo + o) = vl[jf];
+                }
             }
-        }
-        // the other triangle (a tile on the diagonal holds both), or X^T
-        if constexpr (EPI <= kUpdate) {
+            // the other triangle (a tile on the diagonal holds both), or X^T
             if (jb < nj && (!kTri || ti != tj)) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
@@ -989,6 +1023,19 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                         store_cols<FJ>(o + olo, vl, q, nj - jb);
                 }
             }
+        } else {
+#pragma unroll
+            for (int jf = 0; jf < FJ; ++jf)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    if (jb + jf < m.R && i + 4 * h < m.C) {
+                        if constexpr (EPI == kStep)
+                            finish_step(a, p, m, b, jb + jf, i + 4 * h, vec4,
+                                        v[jf] + 4 * h, st[jf][h]);
+                        else
+                            finish_out<EPI>(a.out[p], m, b, jb + jf,
+                                            i + 4 * h, v[jf] + 4 * h);
+                    }
         }
     }
 }
@@ -1086,6 +1133,27 @@ int64_t mat_bytes(const Mat& m, bool full)
     return (off + parts + 255) / 256 * 256;
 }
 
+// The order in which the members enter the group: by the larger side, then
+// the smaller, so that the tiles with the longest sums start first.
+template <class Sides>
+void sort_members(int32_t* order, int32_t count, Sides sides)
+{
+    for (int32_t i = 0; i < count; ++i) {
+        int64_t r, c;
+        sides(i, r, c);
+        int32_t k = i;
+        for (; k > 0; --k) {
+            int64_t qr, qc;
+            sides(order[k - 1], qr, qc);
+            const int64_t hi = r > c ? r : c, lo = r > c ? c : r;
+            const int64_t qh = qr > qc ? qr : qc, ql = qr > qc ? qc : qr;
+            if (qh > hi || (qh == hi && ql >= lo)) break;
+            order[k] = order[k - 1];
+        }
+        order[k] = i;
+    }
+}
+
 // Appends a stack to the group, with its part of the workspace.
 void add_mat(Group& g, int64_t batch, int64_t rows, int64_t cols, bool full,
              char* ws, int64_t& used)
@@ -1107,14 +1175,16 @@ int64_t group_bytes(const Group& g, bool full)
     return n;
 }
 
-// Workgroup prefix sums: fn(mat) workgroups per matrix of the stack.
+// Workgroup prefix sums: fn(mat) workgroups per matrix of the stack, each
+// stack's from a multiple of `align` on.
 template <class Fn>
-uint32_t set_starts(Group& g, Fn fn)
+uint32_t set_starts(Group& g, Fn fn, uint32_t align = 1)
 {
     uint32_t n = 0;
     for (int i = 0; i < g.count; ++i) {
         g.start[i] = n;
-        n += (uint32_t)g.m[i].batch * (uint32_t)fn(g.m[i]);
+        g.m[i].tiles = (uint32_t)g.m[i].batch * (uint32_t)fn(g.m[i]);
+        n += (g.m[i].tiles + align - 1) / align * align;
     }
     g.start[g.count] = n;
     return n;
@@ -1133,50 +1203,86 @@ uint32_t d_tiles(const Mat& m)
 template <class SH, int EPI, bool FULL>
 int launch_gemm(GemmArgs& a, hipStream_t s)
 {
-    const uint32_t n = set_starts(a.g, d_tiles<SH::BT, EPI>);
+    const uint32_t n = set_starts(a.g, d_tiles<SH::BT, EPI>, 8);
     hipLaunchKernelGGL((ns_gemm_kernel<SH, EPI, FULL>), dim3(n),
                        dim3(SH::kThreads), 0, s, a);
     return check_launch("Newton-Schulz product");
 }
 
 // Time of a launch in tiles of one size, in us: `stage` per 64 k and `fixed`
-// per tile, both with `resident` tiles on each of the 256 CUs, or `alone`
-// per 64 k while there is at most one.
+// per tile with `resident` tiles on each of the 256 CUs, or `alone` per 64 k
+// while there is at most one.  The stacks' tiles go to the free places in
+// order, longest first (the group is sorted so).
 template <int BT, int EPI>
 double estimate(const Group& g, double stage, double alone, double fixed,
                 int resident)
 {
-    double work = 0, longest = 0;
+    struct Places {
+        double free;
+        int64_t n;
+    } at[64];
     int64_t n = 0;
+    for (int p = 0; p < g.count; ++p)
+        n += (int64_t)g.m[p].batch * d_tiles<BT, EPI>(g.m[p]);
+    const double per = n <= 256 ? alone : stage;
+    int used = 1;
+    at[0] = {0, 256 * (int64_t)resident};
+    double end = 0;
     for (int p = 0; p < g.count; ++p) {
         const Mat& m = g.m[p];
         const int32_t rp = padded(m.R), cp = padded(m.C);
         const int nk = ((EPI == kGram) == (rp < cp) ? cp : rp) / 64;
-        const int64_t t = (int64_t)m.batch * d_tiles<BT, EPI>(m);
-        n += t;
-        work += (double)t * (nk * stage + fixed);
-        const double one = nk * alone + fixed;
-        longest = one > longest ? one : longest;
+        const double t = nk * per + fixed;
+        int64_t left = (int64_t)m.batch * d_tiles<BT, EPI>(m);
+        // whole rounds of everything, then the rest
+        const int64_t rounds = left / (256 * resident);
+        for (int k = 0; k < used; ++k)
+            at[k].free += (double)rounds * t;
+        left -= rounds * 256 * resident;
+        while (left > 0) {
+            int k = 0;
+            for (int q = 1; q < used; ++q)
+                if (at[q].free < at[k].free) k = q;
+            if (at[k].n > left && used < 64) {
+                at[used++] = {at[k].free, at[k].n - left};
+                at[k].n = left;
+            }
+            left -= at[k].n;
+            at[k].free += t;
+        }
     }
-    if (n <= 256) return longest;
-    const int64_t slots = 256 * resident;
-    return (double)((n + slots - 1) / slots) * (work / (double)n);
+    for (int k = 0; k < used; ++k)
+        end = at[k].free > end ? at[k].free : end;
+    return end;
+}
+
+// The tile for a product on these stacks, by estimated time.
+template <int EPI>
+int choose_tile(const Group& g)
+{
+    double best = estimate<64, EPI>(g, 0.36, 0.25, 3, 2);
+    int tile = 64;
+    auto offer = [&](int t, double us) {
+        if (us < best) {
+            best = us;
+            tile = t;
+        }
+    };
+    offer(128, estimate<128, EPI>(g, 0.98, 0.6, 6, 2));
+    offer(192, estimate<192, EPI>(g, 1.0, 1.0, 9, 1));
+    offer(256, estimate<256, EPI>(g, 1.6, 1.6, 12, 1));
+    return tile;
 }
 
 template <int EPI, bool FULL>
-int launch_product(GemmArgs& a, hipStream_t s)
+int launch_product(GemmArgs& a, int tile, hipStream_t s)
 {
-    const double t256 = estimate<256, EPI>(a.g, 1.6, 1.6, 12, 1);
-    const double t192 = estimate<192, EPI>(a.g, 1.0, 1.0, 9, 1);
-    const double t128 = estimate<128, EPI>(a.g, 0.98, 0.6, 6, 2);
-    const double t64 = estimate<64, EPI>(a.g, 0.36, 0.25, 3, 2);
-    if (t192 < t256 && t192 <= t128 && t192 <= t64)
-        return launch_gemm<Shape192, EPI, FULL>(a, s);
-    if (t256 <= t128 && t256 <= t64)
-        return launch_gemm<Shape256, EPI, FULL>(a, s);
-    if (t128 <= t64)
-        return launch_gemm<Shape128, EPI, FULL>(a, s);
-    return launch_gemm<Shape64, EPI, FULL>(a, s);
+    switch (tile) {
+    case 64: return launch_gemm<Shape64, EPI, FULL>(a, s);
+    case 128: return launch_gemm<Shape128, EPI, FULL>(a, s);
+    case 192: return launch_gemm<Shape192, EPI, FULL>(a, s);
+    default: return launch_gemm<Shape256, EPI, FULL>(a, s);
+    }
 }
 
 // Whether two steps taken on the m x m side cost less than one by one.  In
@@ -1210,6 +1316,8 @@ template <int LAST, bool FULL>
 int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
 {
     const bool pairs = in_pairs(a.g);
+    const int tGram = choose_tile<kGram>(a.g), tPoly = choose_tile<kPoly>(a.g),
+              tUpdate = choose_tile<kUpdate>(a.g);
     a.parity = 0;
     int rc = ZS_OK;
     auto poly = [&](int k, Square out) {
@@ -1218,13 +1326,13 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         a.c = ns.coef[k][2];
         a.sp = a.sq = kA;
         a.so = out;
-        if (!rc) rc = launch_product<kPoly, FULL>(a, s);
+        if (!rc) rc = launch_product<kPoly, FULL>(a, tPoly, s);
     };
     auto prod = [&](Square p, Square q, Square out) {
         a.sp = p;
         a.sq = q;
         a.so = out;
-        if (!rc) rc = launch_product<kProd, FULL>(a, s);
+        if (!rc) rc = launch_product<kProd, FULL>(a, tPoly, s);
     };
     for (int k = 0; k < ns.steps && !rc;) {
         // an odd number of steps: the second by itself, or the only one.  E
@@ -1233,7 +1341,7 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
                          !(ns.steps % 2 && k == 2) &&
                          std::fabs(ns.coef[k][0] * ns.coef[k + 1][0]) < 24;
         a.so = kA;
-        rc = launch_product<kGram, FULL>(a, s);
+        rc = launch_product<kGram, FULL>(a, tGram, s);
         poly(k, kC);
         if (two) {
             prod(kC, kA, kT);
@@ -1244,8 +1352,8 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         k += two ? 2 : 1;
         a.sp = two ? kT : kC;
         if (!rc)
-            rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, s)
-                              : launch_product<LAST, FULL>(a, s);
+            rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, tUpdate, s)
+                              : launch_product<LAST, FULL>(a, tUpdate, s);
         a.parity ^= 1;
     }
     return rc;
@@ -1344,7 +1452,13 @@ extern "C" int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
     Source src[kMaxMats];
     OutMat out[kMaxMats];
     int64_t tiles = 0, used = 0;
-    for (int32_t i = 0; i < count; ++i) {
+    int32_t order[kMaxMats];
+    sort_members(order, count, [&](int32_t i, int64_t& r, int64_t& c) {
+        r = mats[i].rows;
+        c = mats[i].cols;
+    });
+    for (int32_t n = 0; n < count; ++n) {
+        const int32_t i = order[n];
         const zs_ns_matrices& m = mats[i];
         if (const int rc = check_sizes(i, m.batch, m.rows, m.cols, tiles))
             return rc;
@@ -1400,9 +1514,10 @@ extern "C" int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
 
 namespace {
 
-// The members of a muon call, checked against the layout.
+// The members of a muon call, checked against the layout; order[n]: which
+// tensor the group's n-th stack is.
 int muon_group(const zs_layout* L, int32_t count, const zs_muon_tensor* t,
-               bool full, char* ws, Group& g, int64_t& used)
+               bool full, char* ws, Group& g, int32_t* order, int64_t& used)
 {
     using zs::fail;
     if (!L) return fail(ZS_EINVAL, "layout is NULL");
@@ -1433,7 +1548,14 @@ int muon_group(const zs_layout* L, int32_t count, const zs_muon_tensor* t,
                         "the tensor's %lld elements", i,
                         (long long)t[i].batch, (long long)t[i].rows,
                         (long long)t[i].cols, (long long)L->chunks[b].numel);
-        add_mat(g, t[i].batch, t[i].rows, t[i].cols, full, ws, used);
+    }
+    sort_members(order, count, [&](int32_t i, int64_t& r, int64_t& c) {
+        r = t[i].rows;
+        c = t[i].cols;
+    });
+    for (int32_t n = 0; n < count; ++n) {
+        const zs_muon_tensor& m = t[order[n]];
+        add_mat(g, m.batch, m.rows, m.cols, full, ws, used);
     }
     return ZS_OK;
 }
@@ -1475,8 +1597,9 @@ extern "C" int zs_muon_workspace(const zs_layout* L, int32_t count,
     if (const int rc = check_precision(precision)) return rc;
     Group g;
     int64_t used;
+    int32_t order[kMaxMats];
     const int rc = muon_group(L, count, tensors, precision == ZS_NS_FULL,
-                              nullptr, g, used);
+                              nullptr, g, order, used);
     if (!rc) *bytes = used;
     return rc;
 }
@@ -1502,8 +1625,10 @@ extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
     const bool full = hp->ns.precision == ZS_NS_FULL;
     Group g;
     int64_t used;
+    int32_t order[kMaxMats];
     if (const int rc = muon_group(L, count, tensors, full,
-                                  static_cast<char*>(workspace), g, used))
+                                  static_cast<char*>(workspace), g, order,
+                                  used))
         return rc;
     if (grad_layout != ZS_GRADS_SLICES && grad_layout != ZS_GRADS_TILED)
         return fail(ZS_EINVAL, "unknown grad_layout %d", grad_layout);
@@ -1519,7 +1644,8 @@ extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
     const bool tiled = grad_layout == ZS_GRADS_TILED;
     MomArgs ma;
     StepMat st[kMaxMats];
-    for (int32_t i = 0; i < count; ++i) {
+    for (int32_t n = 0; n < count; ++n) {
+        const int32_t i = order[n];
         const zs_bucket& b = L->buckets[tensors[i].bucket_id];
         if (!grads[i]) return fail(ZS_EINVAL, "grads[%d] is NULL", i);
         if (!aligned(grads[i], 16))
@@ -1535,18 +1661,18 @@ extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
             if (grad_stride > INT64_MAX / 2 / L->world)
                 return fail(ZS_ERANGE, "W * grad_stride overflows");
         }
-        ma.src[i].grads = grads[i];
-        ma.src[i].state = state + b.tile_off * 3 * kTile;
-        st[i].state = ma.src[i].state;
-        st[i].pshard = param_shard ? param_shard + b.shard_off : nullptr;
-        st[i].flat = full_flat ? full_flat + slice_flat_pos(L, b) : nullptr;
+        ma.src[n].grads = grads[i];
+        ma.src[n].state = state + b.tile_off * 3 * kTile;
+        st[n].state = ma.src[n].state;
+        st[n].pshard = param_shard ? param_shard + b.shard_off : nullptr;
+        st[n].flat = full_flat ? full_flat + slice_flat_pos(L, b) : nullptr;
         const double r = (double)tensors[i].rows, c = (double)tensors[i].cols;
         const double scale =
             hp->scale == ZS_MUON_SCALE_SHAPE ? std::sqrt(r > c ? r / c : 1.0)
             : hp->scale == ZS_MUON_SCALE_RMS
                 ? 0.2 * std::sqrt(r > c ? r : c)
                 : 1.0;
-        st[i].s = (float)((double)hp->lr * scale);
+        st[n].s = (float)((double)hp->lr * scale);
     }
     if (workspace_bytes < used)
         return fail(ZS_ERANGE, "workspace of %lld bytes, %lld needed",

@@ -68,8 +68,8 @@ struct Mat {
     uint32_t tiles;         // workgroups of the present launch
 };
 
-// Where its parts lie: E elements of X, S of A, D of a diagonal, over the
-// whole stack.
+// Where its parts lie: E elements of X, S of a square, D of a diagonal, over
+// the whole stack, and in one matrix e, s and mp.
 //   Xd[2] hi, lo | Xt[2] hi (lo) | kSquares m x m matrices, each hi (lo)
 //   | their diagonals | partial sums (double)
 // The momentum kernel's U (fp32) lies where Xd[1] will be: it is read by the
@@ -80,22 +80,29 @@ enum Square { kA, kC, kT, kC2 };         // what they hold: run_steps
 template <bool FULL>
 struct Region {
     char* ws;
-    int64_t E, S, D;
+    int32_t rp, cp, mp;                 // padded sides, the smaller one
+    int64_t e, s, E, S, D;
     __host__ __device__ Region(char* w, int32_t R, int32_t C, int32_t batch)
         : ws(w)
     {
-        const int64_t rp = padded(R), cp = padded(C),
-                      mp = rp < cp ? rp : cp;
-        E = batch * rp * cp;
-        S = batch * mp * mp;
-        D = batch * mp;
+        rp = padded(R);
+        cp = padded(C);
+        mp = rp < cp ? rp : cp;
+        e = (int64_t)rp * cp;
+        s = (int64_t)mp * mp;
+        E = batch * e;
+        S = batch * s;
+        D = (int64_t)batch * mp;
     }
     __device__ f16* xd(int p) const { return (f16*)(ws + 4 * p * E); }
     __device__ f16* xt(int p) const
     {
         return (f16*)(ws + 8 * E + (FULL ? 4 : 2) * p * E);
     }
-    __host__ __device__ int64_t x_bytes() const { return (FULL ? 16 : 12) * E; }
+    __host__ __device__ int64_t x_bytes() const
+    {
+        return (FULL ? 16 : 12) * E;
+    }
     __host__ __device__ int64_t d_off() const
     {
         return x_bytes() + (FULL ? 4 : 2) * kSquares * S;
@@ -358,8 +365,7 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
     const int p = find(a.g, bid);
     const Mat& m = a.g.m[p];
     const Region<FULL> w(m.ws, m.R, m.C, m.batch);
-    const int32_t rp = padded(m.R), cp = padded(m.C);
-    const uint32_t tc = cp / 64, tiles = tc * (rp / 64);
+    const uint32_t tc = w.cp / 64, tiles = tc * (w.rp / 64);
     const uint32_t b = bid / tiles;
     bid %= tiles;
     const int r0 = bid / tc * 64, c0 = bid % tc * 64;
@@ -378,7 +384,6 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
     const int64_t xr = SRC == 2 ? m.C : s.row;
     const int64_t xb = SRC == 2 ? (int64_t)m.R * m.C : s.batch;
     const int tx = threadIdx.x % 16 * 4, ty = threadIdx.x / 16;
-    const int64_t mat = (int64_t)b * rp * cp;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int r = r0 + ty + 16 * k, c = c0 + tx;
@@ -405,7 +410,7 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
             if constexpr (FULL)
                 t[1][tx + q][ty + 16 * k] = l;
         }
-        const int64_t o = mat + (int64_t)r * cp + c;
+        const int64_t o = b * w.e + (int64_t)r * w.cp + c;
         *reinterpret_cast<f16x4*>(w.xd(0) + o) = hi;
         *reinterpret_cast<f16x4*>(w.xd(0) + w.E + o) = lo;
     }
@@ -413,7 +418,7 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int c = ty + 16 * k;
-        const int64_t o = mat + (int64_t)(c0 + c) * rp + r0 + tx;
+        const int64_t o = b * w.e + (int64_t)(c0 + c) * w.rp + r0 + tx;
         *reinterpret_cast<f16x4*>(w.xt(0) + o) =
             *reinterpret_cast<const f16x4*>(&t[0][c][tx]);
         if constexpr (FULL)
@@ -596,14 +601,14 @@ __device__ __forceinline__ void finish_step(const GemmArgs& a, int p,
         if (sm.flat)
             *reinterpret_cast<u32x2*>(sm.flat + e) = h;
     } else {
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-            if (i + q >= m.C)
-                continue;
+        const f32x4 vv = {v[0], v[1], v[2], v[3]};
+        const int n = m.C - i < 4 ? m.C - i : 4;
+#pragma unroll 1
+        for (int q = 0; q < n; ++q) {
             const int64_t eq = e + q;
             float* const s1 = sm.state + eq / kTile * 3 * kTile + eq % kTile;
             const float t = *s1 * a.dec;
-            const float u = sm.s * (v[q] * kUnscale);
+            const float u = sm.s * (vv[q] * kUnscale);
             const float x = t - u;
             *s1 = x;
             const uint16_t h = (uint16_t)to_bf16(x);
@@ -613,6 +618,34 @@ __device__ __forceinline__ void finish_step(const GemmArgs& a, int p,
                 sm.flat[eq] = h;
         }
     }
+}
+
+// Tiles go in bands of kBand along one side, the band's tiles of a column
+// first: the 32 CUs of an XCD then work on about 8 x 4 tiles, 12 panels of the
+// operands, where a row of 32 tiles would read 33.
+constexpr uint32_t kBand = 8;
+
+// Tile `n` of a lower triangle of t tiles a side.
+__device__ __forceinline__ void lower_tile(uint32_t n, uint32_t t,
+                                           uint32_t& ti, uint32_t& tj)
+{
+    // the band: rows r0 .. r0 + h - 1, after r0 (r0 + 1) / 2 tiles
+    uint32_t r0 = 0;
+    while (r0 + kBand < t && (r0 + kBand) * (r0 + kBand + 1) / 2 <= n)
+        r0 += kBand;
+    const uint32_t h = t - r0 < kBand ? t - r0 : kBand;
+    n -= r0 * (r0 + 1) / 2;
+    if (n < (r0 + 1) * h) {             // columns that the whole band has
+        tj = n / h;
+        ti = r0 + n % h;
+        return;
+    }
+    n -= (r0 + 1) * h;                  // column r0 + k: h - k tiles
+    uint32_t k = 1;
+    while (n >= h - k)
+        n -= h - k++;
+    tj = r0 + k;
+    ti = r0 + k + n;
 }
 
 template <class SH, int EPI, bool FULL>
@@ -627,6 +660,7 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     __shared__ __align__(1024) char lds1[2 * SH::kHalf];
     __shared__ __align__(1024) char lds2[ST > 2 ? 2 * SH::kHalf : 16];
     __shared__ __align__(1024) char lds3[ST > 3 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(16) float diag[2][BT];        // of the epilogue's squares
 
     uint32_t bid = blockIdx.x;
     const int p = find(a.g, bid);
@@ -635,8 +669,7 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         return;                         // the whole workgroup
     bid = xcd_order(bid, m.tiles);
     const Region<FULL> w(m.ws, m.R, m.C, m.batch);
-    const int32_t rp = padded(m.R), cp = padded(m.C);
-    const int32_t mp = rp < cp ? rp : cp;
+    const int32_t rp = w.rp, cp = w.cp, mp = w.mp;
     const bool tall = m.R > m.C;
 
     // D[i][j]: ti, tj its tile
@@ -648,23 +681,16 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         const uint32_t tiles = tri_tiles<BT>(mp);
         b = bid / tiles;
         bid %= tiles;
-        // row of the lower triangle: ti (ti + 1) / 2 <= bid
-        ti = (uint32_t)((sqrtf(8.f * (float)bid + 1.f) - 1.f) * 0.5f);
-        while (ti * (ti + 1) / 2 > bid)
-            --ti;
-        while ((ti + 1) * (ti + 2) / 2 <= bid)
-            ++ti;
-        tj = bid - ti * (ti + 1) / 2;
+        lower_tile(bid, (mp + BT - 1) / BT, ti, tj);
         ni = nj = mp;
         if constexpr (EPI == kGram) {
-            P = (tall ? w.xt(a.parity) : w.xd(a.parity)) +
-                (int64_t)b * rp * cp;
+            P = (tall ? w.xt(a.parity) : w.xd(a.parity)) + b * w.e;
             nk = tall ? rp : cp;
             plo = w.E;
             Q = P;
         } else {
-            P = w.square(a.sp) + (int64_t)b * mp * mp;
-            Q = w.square(a.sq) + (int64_t)b * mp * mp;
+            P = w.square(a.sp) + b * w.s;
+            Q = w.square(a.sq) + b * w.s;
             nk = mp;
             plo = w.S;
         }
@@ -676,20 +702,19 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         const uint32_t tni = (ni + BT - 1) / BT, tnj = (nj + BT - 1) / BT;
         b = bid / (tni * tnj);
         bid %= tni * tnj;
-        // bands of 8 tiles along j, so that a run of tiles shares operands
-        const uint32_t band = bid / (8 * tni) * 8;
-        const uint32_t h = tnj - band < 8 ? tnj - band : 8;
+        const uint32_t band = bid / (kBand * tni) * kBand;
+        const uint32_t h = tnj - band < kBand ? tnj - band : kBand;
         bid -= band * tni;
         tj = band + bid % h;
         ti = bid / h;
-        const f16* const C = w.square(a.sp) + (int64_t)b * mp * mp;
+        const f16* const C = w.square(a.sp) + b * w.s;
         if (tall) {
             P = C;
             plo = w.S;
-            Q = w.xd(a.parity) + (int64_t)b * rp * cp;
+            Q = w.xd(a.parity) + b * w.e;
             qlo = w.E;
         } else {
-            P = w.xt(a.parity) + (int64_t)b * rp * cp;
+            P = w.xt(a.parity) + b * w.e;
             plo = w.E;
             Q = C;
             qlo = w.S;
@@ -761,6 +786,78 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     const int fi = (wi * FI * 16 + (l16 >> 2) * 8 + (l16 & 3)) * kRow;
     const int fj = SH::kHalf + (wj * FJ * 16 + l16 * FJ) * kRow;
     const int fc = (g ^ (l16 & 7)) * 16;    // sw(row) = l16 & 7 for both
+    // What the epilogue reads (the map of rows and columns is above), in units
+    // of one column run: unit u is column u % FJ of fragments 2 (u / FJ) and
+    // the next.  The first kEarly are fetched ahead of the products, the rest
+    // kRing - 1 units ahead of their use: vector memory completes in order,
+    // and a load behind stores waits for them.  Past the edges the nearest
+    // values inside are read, and dropped.
+    constexpr bool kX = EPI >= kUpdate;
+    constexpr int kUnits = FI / 2 * FJ;
+    // as many as the registers beside the largest tile's sums hold
+    constexpr int kRing =
+        EPI == kStep || (EPI == kProd && FULL) ? 3 : EPI == kProd ? 4 : 6;
+    constexpr int kMost = EPI == kGram ? 0 : kRing == 3 ? 2 : 3;
+    constexpr int kEarly = kMost < kUnits ? kMost : kUnits;
+    static_assert(kEarly < kRing, "units");
+    const f16* const xin = w.xd(a.parity) + b * w.e;
+    const f16* const pm = w.square(a.sp) + b * w.s;
+    const f16* const qm = w.square(a.sq) + b * w.s;
+    const float* const dp = w.diag(a.sp) + (int64_t)b * mp;
+    const float* const dq = w.diag(a.sq) + (int64_t)b * mp;
+    const int64_t olo = kTri ? w.S : w.E;
+    const int ld = kTri ? w.mp : w.cp, ldT = kTri ? w.mp : w.rp;
+    const int ib = i0 + wi * FI * 16 + g * 8;
+    const int jb = j0 + (wj * 16 + l16) * FJ;
+    const bool vec4 = m.C % 4 == 0;             // kStep's state by fours
+    f16x8 inh[kRing], inl[kRing], inh2[kRing], inl2[kRing];
+    f32x4 inS[kRing][2];
+    auto fetch = [&](int u) {
+        if constexpr (EPI == kGram)
+            return;
+        const int n = u % kRing, f = u / FJ * 2, jf = u % FJ;
+        const int i = ib + f * 16 < ni ? ib + f * 16 : ni - 8;
+        const int j = jb + jf < nj ? jb + jf : nj - 1;
+        const int64_t o = (int64_t)j * ld + i;
+        const f16* const in = kX ? xin : pm;
+        inh[n] = *reinterpret_cast<const f16x8*>(in + o);
+        if constexpr (FULL || kX)
+            inl[n] = *reinterpret_cast<const f16x8*>(in + olo + o);
+        if constexpr (EPI == kProd) {
+            inh2[n] = *reinterpret_cast<const f16x8*>(qm + o);
+            if constexpr (FULL)
+                inl2[n] = *reinterpret_cast<const f16x8*>(qm + olo + o);
+        }
+        if constexpr (EPI == kStep) {
+            if (vec4) {
+                const int js = j < m.R ? j : m.R - 1;
+                const int64_t r = ((int64_t)b * m.R + js) * m.C;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int is = i + 4 * h;
+                    const int64_t e = r + (is < m.C ? is : m.C - 4);
+                    inS[n][h] = *reinterpret_cast<const f32x4*>(
+                        a.st[p].state + e / kTile * 3 * kTile + e % kTile);
+                }
+            }
+        }
+    };
+    if constexpr (EPI != kGram) {
+        // the diagonals along the tile's rows and columns: in an update the
+        // one along X's shorter side counts (tall: i), the other is not read
+        for (int t = threadIdx.x; t < BT; t += SH::kThreads) {
+            const int i = i0 + t < ni ? i0 + t : ni - 1;
+            const int j = j0 + t < nj ? j0 + t : nj - 1;
+            if (!kX || tall)
+                diag[0][t] = dp[i];
+            if (!kX || !tall)
+                diag[1][t] = (kX ? dp : dq)[j];
+        }
+#pragma unroll
+        for (int u = 0; u < kEarly; ++u)
+            fetch(u);
+    }
+
     f16x8 x[FI], y[FJ];
     auto read = [&](const char* lds, int ks) {
 #pragma unroll
@@ -856,165 +953,118 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         }
     }
 
-    // Epilogue, from registers (the map of rows and columns is above).
-    const int64_t mat = (int64_t)b * rp * cp;
-    const f16* const xin = w.xd(a.parity) + mat;
-    const f16* const pm = w.square(a.sp) + (int64_t)b * mp * mp;
-    const f16* const qm = w.square(a.sq) + (int64_t)b * mp * mp;
-    const float* const dp = w.diag(a.sp) + (int64_t)b * mp;
-    const float* const dq = w.diag(a.sq) + (int64_t)b * mp;
+    // Epilogue, from registers.
     float* const dout = w.diag(a.so) + (int64_t)b * mp;
-    f16* const out = kTri ? w.square(a.so) + (int64_t)b * mp * mp
-                          : w.xd(1 - a.parity) + mat;
-    f16* const outT = kTri ? out : w.xt(1 - a.parity) + mat;
-    const int64_t olo = kTri ? w.S : w.E;
-    const int ld = kTri ? mp : cp, ldT = kTri ? mp : rp;
-    const int jb = j0 + (wj * 16 + l16) * FJ;
-    // What the epilogue reads, fetched for fragments f, f + 1 before the
-    // results of f - 2, f - 1 are stored: vector memory completes in order,
-    // and a load behind a store waits for it.  Past the edges the nearest
-    // values inside are read, and dropped.
-    constexpr bool kX = EPI >= kUpdate;
-    f16x8 inh[FJ], inl[FJ], inh2[FJ], inl2[FJ];
-    f32x4 inS[FJ][2], di0, di1;
-    float dj[FJ];
-    const bool vec4 = m.C % 4 == 0;             // kStep's state by fours
-    auto fetch = [&](int f) {
-        if constexpr (EPI == kGram)
-            return;
-        int i = i0 + wi * FI * 16 + f * 16 + g * 8;
-        i = i < ni ? i : ni - 8;
-        if (!kX || tall) {
-            di0 = *reinterpret_cast<const f32x4*>(dp + i);
-            di1 = *reinterpret_cast<const f32x4*>(dp + i + 4);
+    f16* const out =
+        kTri ? w.square(a.so) + b * w.s : w.xd(1 - a.parity) + b * w.e;
+    f16* const outT = kTri ? out : w.xt(1 - a.parity) + b * w.e;
+#pragma unroll
+    for (int u = kEarly; u < kRing - 1 && u < kUnits; ++u)
+        fetch(u);
+#pragma unroll
+    for (int f = 0; f < FI; f += 2) {
+        const int i = ib + f * 16;
+        f16x8 vh[FJ], vl[FJ];
+        f32x4 di[2] = {};
+        if constexpr (EPI != kGram) {
+            const f32x4* const d4 = reinterpret_cast<const f32x4*>(
+                &diag[0][(wi * FI + f) * 16 + g * 8]);
+            di[0] = d4[0];
+            di[1] = d4[1];
         }
 #pragma unroll
         for (int jf = 0; jf < FJ; ++jf) {
-            const int j = jb + jf < nj ? jb + jf : nj - 1;
-            const int64_t o = (int64_t)j * ld + i;
-            const f16* const in = kX ? xin : pm;
-            inh[jf] = *reinterpret_cast<const f16x8*>(in + o);
-            if constexpr (FULL || kX)
-                inl[jf] = *reinterpret_cast<const f16x8*>(in + olo + o);
-            if constexpr (EPI == kProd) {
-                inh2[jf] = *reinterpret_cast<const f16x8*>(qm + o);
-                if constexpr (FULL)
-                    inl2[jf] =
-                        *reinterpret_cast<const f16x8*>(qm + olo + o);
-            }
-            if constexpr (EPI == kStep) {
-                if (vec4) {
-                    const int js = j < m.R ? j : m.R - 1;
-                    const int64_t r = ((int64_t)b * m.R + js) * m.C;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const int is = i + 4 * h;
-                        const int64_t e = r + (is < m.C ? is : m.C - 4);
-                        inS[jf][h] = *reinterpret_cast<const f32x4*>(
-                            a.st[p].state + e / kTile * 3 * kTile +
-                            e % kTile);
-                    }
-                }
-            }
-        }
-    };
-    if constexpr (EPI != kGram)
-#pragma unroll
-        for (int jf = 0; jf < FJ; ++jf)
-            dj[jf] = (kX ? dp : dq)[jb + jf < nj ? jb + jf : nj - 1];
-    fetch(0);
-#pragma unroll
-    for (int f = 0; f < FI; f += 2) {
-        const int i = i0 + wi * FI * 16 + f * 16 + g * 8;
-        float v[FJ][8];                     // the results, times kScale
-#pragma unroll
-        for (int jf = 0; jf < FJ; ++jf)
+            const float dj =
+                EPI == kGram ? 0 : diag[1][(wj * 16 + l16) * FJ + jf];
+            const int u = f / 2 * FJ + jf, n = u % kRing, j = jb + jf;
+            if (u + kRing - 1 < kUnits)
+                fetch(u + kRing - 1);
+            float v[8];                     // the results, times kScale
 #pragma unroll
             for (int q = 0; q < 8; ++q) {
                 const float d = acc[f + q / 4][jf][q % 4] * kUnscale;
-                const float di = q < 4 ? di0[q % 4] : di1[q % 4];
+                const float dii = di[q / 4][q % 4];
                 if constexpr (EPI == kGram) {
-                    v[jf][q] = d;
+                    v[q] = d;
                 } else if constexpr (EPI == kPoly || EPI == kProd) {
                     // (R + D)(S + F) = R S + D S + R F + D F, with D and F
                     // the diagonals
-                    float r = (float)inh[jf][q];
+                    float r = (float)inh[n][q];
                     if constexpr (FULL)
-                        r = r + (float)inl[jf][q];
+                        r = r + (float)inl[n][q];
                     if constexpr (EPI == kPoly) {
-                        v[jf][q] =
-                            a.b * r + a.c * (d + (di + dj[jf]) * r);
+                        v[q] = a.b * r + a.c * (d + (dii + dj) * r);
                     } else {
-                        float t = (float)inh2[jf][q];
+                        float t = (float)inh2[n][q];
                         if constexpr (FULL)
-                            t = t + (float)inl2[jf][q];
-                        v[jf][q] = d + (di * t + r * dj[jf]);
+                            t = t + (float)inl2[n][q];
+                        v[q] = d + (dii * t + r * dj);
                     }
                 } else {
-                    v[jf][q] = (tall ? di : dj[jf]) *
-                                   ((float)inh[jf][q] + (float)inl[jf][q]) +
-                               d;
+                    v[q] = (tall ? dii : dj) *
+                               ((float)inh[n][q] + (float)inl[n][q]) + d;
                 }
             }
-        if constexpr (kTri) {
-            // the diagonal, apart
-            if (ti == tj) {
-#pragma unroll
-                for (int jf = 0; jf < FJ; ++jf)
+            if constexpr (kTri) {
+                // the diagonal, apart
+                if (ti == tj) {
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        if (i + q == jb + jf && i < ni) {
+                        if (i + q == j && i < ni) {
                             const float d =
                                 acc[f + q / 4][jf][q % 4] * kUnscale *
                                 kUnscale;
-                            const float di = q < 4 ? di0[q % 4] : di1[q % 4];
+                            const float dii = di[q / 4][q % 4];
                             const float dd =
-                                EPI == kGram ? d : d + di * dj[jf];
-                            dout[i + q] =
-                                EPI == kPoly
-                                    ? a.a + (a.b * dj[jf] + a.c * dd)
-                                    : dd;
-                            v[jf][q] = 0;
+                                EPI == kGram ? d : d + dii * dj;
+                            dout[j] = EPI == kPoly
+                                          ? a.a + (a.b * dj + a.c * dd)
+                                          : dd;
+                            v[q] = 0;
                         }
+                }
             }
-        }
-        f32x4 st[FJ][2];
-        if constexpr (EPI == kStep) {
-            if (vec4) {
-#pragma unroll
-                for (int jf = 0; jf < FJ; ++jf)
-#pragma unroll
-                    for (int q = 0; q < 8; ++q) {
-                        const float t = inS[jf][q / 4][q % 4] * a.dec;
-                        const float u = a.st[p].s * (v[jf][q] * kUnscale);
-                        st[jf][q / 4][q % 4] = t - u;
-                    }
-            }
-        }
-        if (f + 2 < FI)
-            fetch(f + 2);
-        if (i >= ni)
-            continue;
-        if constexpr (EPI <= kUpdate) {
-            f16x8 vh[FJ], vl[FJ];
-#pragma unroll
-            for (int jf = 0; jf < FJ; ++jf) {
+            if constexpr (EPI <= kUpdate) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     f16 h, l;
-                    split(v[jf][q], h, l);
+                    split(v[q], h, l);
                     vh[jf][q] = h;
                     vl[jf][q] = l;
                 }
-                if (jb + jf < nj) {
-                    const int64_t o = (int64_t)(jb + jf) * ld + i;
+                if (i < ni && j < nj) {
+                    const int64_t o = (int64_t)j * ld + i;
                     *reinterpret_cast<f16x8*>(out + o) = vh[jf];
                     if constexpr (FULL || EPI == kUpdate)
                         *reinterpret_cast<f16x8*>(out + olo + o) = vl[jf];
                 }
+            } else {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    f32x4 st;
+                    if constexpr (EPI == kStep) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const float t = inS[n][h][q] * a.dec;
+                            const float x =
+                                a.st[p].s * (v[4 * h + q] * kUnscale);
+                            st[q] = t - x;
+                        }
+                    }
+                    if (j < m.R && i + 4 * h < m.C) {
+                        if constexpr (EPI == kStep)
+                            finish_step(a, p, m, b, j, i + 4 * h, vec4,
+                                        v + 4 * h, st);
+                        else
+                            finish_out<EPI>(a.out[p], m, b, j, i + 4 * h,
+                                            v + 4 * h);
+                    }
+                }
             }
-            // the other triangle (a tile on the diagonal holds both), or X^T
-            if (jb < nj && (!kTri || ti != tj)) {
+        }
+        // the other triangle (a tile on the diagonal holds both), or X^T
+        if constexpr (EPI <= kUpdate) {
+            if (i < ni && jb < nj && (!kTri || ti != tj)) {
 #pragma unroll
                 for (int q = 0; q < 8; ++q) {
                     f16* const o = outT + (int64_t)(i + q) * ldT + jb;
@@ -1023,19 +1073,6 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                         store_cols<FJ>(o + olo, vl, q, nj - jb);
                 }
             }
-        } else {
-#pragma unroll
-            for (int jf = 0; jf < FJ; ++jf)
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    if (jb + jf < m.R && i + 4 * h < m.C) {
-                        if constexpr (EPI == kStep)
-                            finish_step(a, p, m, b, jb + jf, i + 4 * h, vec4,
-                                        v[jf] + 4 * h, st[jf][h]);
-                        else
-                            finish_out<EPI>(a.out[p], m, b, jb + jf,
-                                            i + 4 * h, v[jf] + 4 * h);
-                    }
         }
     }
 }
@@ -1269,8 +1306,8 @@ int choose_tile(const Group& g)
         }
     };
     offer(128, estimate<128, EPI>(g, 0.98, 0.6, 6, 2));
-    offer(192, estimate<192, EPI>(g, 1.0, 1.0, 9, 1));
-    offer(256, estimate<256, EPI>(g, 1.6, 1.6, 12, 1));
+    offer(192, estimate<192, EPI>(g, 1.12, 0.95, 8, 1));
+    offer(256, estimate<256, EPI>(g, 1.5, 1.4, 12, 1));
     return tile;
 }
 

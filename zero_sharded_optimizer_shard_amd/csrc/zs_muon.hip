@@ -491,8 +491,10 @@ struct Shape {
 typedef Shape<256, 2, 4, 2> Shape256;
 typedef Shape<192, 2, 4, 2> Shape192;
 typedef Shape<128, 2, 4, 2> Shape128;
-// Few tiles, bound by the latency of a stage: three in flight.
+// Small matrices are bound by the latency of a stage: three in flight, or
+// seven where there is a CU for every tile.
 typedef Shape<64, 2, 2, 4> Shape64;
+typedef Shape<64, 2, 2, 8> Shape64Deep;
 
 // s_waitcnt immediate: at most vm vector loads and lg LDS operations out.
 constexpr int wait_count(int vm, int lg)
@@ -659,7 +661,11 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     __shared__ __align__(1024) char lds0[2 * SH::kHalf];
     __shared__ __align__(1024) char lds1[2 * SH::kHalf];
     __shared__ __align__(1024) char lds2[ST > 2 ? 2 * SH::kHalf : 16];
-    __shared__ __align__(1024) char lds3[ST > 3 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(1024) char lds3[ST > 2 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(1024) char lds4[ST > 4 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(1024) char lds5[ST > 4 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(1024) char lds6[ST > 4 ? 2 * SH::kHalf : 16];
+    __shared__ __align__(1024) char lds7[ST > 4 ? 2 * SH::kHalf : 16];
     __shared__ __align__(16) float diag[2][BT];        // of the epilogue's squares
 
     uint32_t bid = blockIdx.x;
@@ -735,17 +741,19 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     // so out[j][i] is written 16 bytes a lane, 64 in a row, and its transpose
     // out[i][j] 2 FJ bytes a lane, 32 FJ in a row, straight from registers.
     //
-    // A stage's row is 64 k, 128 bytes, in 16-byte pieces.  Piece c of a row
-    // is stored at c ^ sw(row), with sw(row) spreading the 16 rows that a
+    // A stage's row is 128 bytes, in 16-byte pieces: 64 k, or in full
+    // precision 32 k, their high parts and then their low ones.  Piece c of a
+    // row is stored at c ^ sw(row), with sw(row) spreading the 16 rows that a
     // fragment reads at one k over all eight places.  A load instruction
     // fills 1 KiB of LDS in lane order, 8 rows, so the lane fetches the piece
     // that belongs at its place.
     const bool isP = wave < SH::kWaves / 2;
     const char* const base = reinterpret_cast<const char*>(
         isP ? P + (int64_t)i0 * nk : Q + (int64_t)j0 * nk);
+    constexpr int kStageK = FULL ? 32 : 64;
     const int64_t lo = 2 * (isP ? plo : qlo);       // bytes to the low parts
-    const int loSeg = isP ? 2 : 1;                  // and when they are read
     uint32_t voff[NL];
+    int64_t llo[NL];
 #pragma unroll
     for (int q = 0; q < NL; ++q) {
         const int u = wave * NL + q;
@@ -753,27 +761,21 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         const int lim = isP ? ni - i0 : nj - j0;
         const int r = row < lim ? row : lim - 1;
         const int sw = isP ? (row & 3) | ((row >> 1) & 4) : (row / FJ) & 7;
-        voff[q] = (uint32_t)r * nk * 2 + ((lane & 7) ^ sw) * 16;
+        const int piece = (lane & 7) ^ sw;
+        voff[q] = (uint32_t)r * nk * 2 + (FULL ? piece & 3 : piece) * 16;
+        llo[q] = piece < 4 ? 0 : lo;
     }
-    const int nkt = nk / 64;
-    const int total = FULL ? 3 * nkt : nkt;
-    int seg = 0, kseg = 0;                          // of the next stage
+    const int total = nk / kStageK;
+    int next = 0;                                   // stage to be loaded
     auto load = [&](char* lds) {
-        const char* s = base + (int64_t)kseg * kRow;
-        if constexpr (FULL) {
-            s += seg == loSeg ? lo : 0;
-            if (++kseg == nkt) {
-                kseg = 0;
-                ++seg;
-            }
-        } else {
-            ++kseg;
-        }
+        const char* const s = base + (int64_t)next * (kStageK * 2);
+        ++next;
 #pragma unroll
-        for (int q = 0; q < NL; ++q)
+        for (int q = 0; q < NL; ++q) {
+            const char* const from = FULL ? s + llo[q] + voff[q] : s + voff[q];
             __builtin_amdgcn_global_load_lds(
-                (gptr*)(s + voff[q]), (lptr*)(lds + (wave * NL + q) * 1024),
-                16, 0, 0);
+                (gptr*)from, (lptr*)(lds + (wave * NL + q) * 1024), 16, 0, 0);
+        }
     };
 
     f32x4 acc[FI][FJ];
@@ -796,8 +798,8 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     constexpr int kUnits = FI / 2 * FJ;
     // as many as the registers beside the largest tile's sums hold
     constexpr int kRing =
-        EPI == kStep || (EPI == kProd && FULL) ? 3 : EPI == kProd ? 4 : 6;
-    constexpr int kMost = EPI == kGram ? 0 : kRing == 3 ? 2 : 3;
+        EPI == kStep || FULL ? 3 : EPI == kProd ? 4 : 6;
+    constexpr int kMost = EPI == kGram ? 0 : FULL ? 1 : kRing == 3 ? 2 : 3;
     constexpr int kEarly = kMost < kUnits ? kMost : kUnits;
     static_assert(kEarly < kRing, "units");
     const f16* const xin = w.xd(a.parity) + b * w.e;
@@ -858,53 +860,66 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
             fetch(u);
     }
 
-    f16x8 x[FI], y[FJ];
-    auto read = [&](const char* lds, int ks) {
-#pragma unroll
-        for (int j = 0; j < FJ; ++j)
-            y[j] = *reinterpret_cast<const f16x8*>(lds + fj + j * kRow +
-                                                   (fc ^ (ks * 64)));
+    // Fragments: half h of a stage's rows (k 0..31 and 32..63, or the high and
+    // the low parts).
+    f16x8 x[FI], y[FULL ? 2 : 1][FJ];
+    auto readx = [&](const char* lds, int h) {
 #pragma unroll
         for (int i = 0; i < FI; ++i)
             x[i] = *reinterpret_cast<const f16x8*>(
-                lds + fi + (i / 2 * 32 + i % 2 * 4) * kRow + (fc ^ (ks * 64)));
+                lds + fi + (i / 2 * 32 + i % 2 * 4) * kRow + (fc ^ (h * 64)));
     };
-    auto multiply = [&]() {
+    auto ready = [&](const char* lds, int h) {
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+            y[FULL ? h : 0][j] = *reinterpret_cast<const f16x8*>(
+                lds + fj + j * kRow + (fc ^ (h * 64)));
+    };
+    auto multiply = [&](int h) {
 #pragma unroll
         for (int i = 0; i < FI; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    x[i], y[j], acc[i][j], 0, 0, 0);
+                    x[i], y[h][j], acc[i][j], 0, 0, 0);
     };
+    // A stage's products, each after its reads: k 0..31 and 32..63, or in
+    // full precision high x high, high x low and low x high.
+    constexpr int kParts = FULL ? 3 : 2;
+    auto read = [&](const char* lds, int part) {
+        if (!FULL || part < 2)
+            ready(lds, part);
+        if (!FULL || part != 1)
+            readx(lds, part != 0);
+    };
+    auto product = [&](int part) { multiply(FULL && part == 1); };
 
     if constexpr (SH::kWaves == 8) {
         // The waves of a SIMD (w and w + 4) run one slot apart: while one
         // multiplies, the other reads its fragments and issues loads.  A
-        // stage takes a wave four slots: read, multiply (k 0..31), read,
-        // multiply (k 32..63), each ended by a barrier.  The loads for the
-        // next stage go out in the first; they have landed for every wave
-        // when it waits for its own before the barrier that ends the third,
-        // the later half one slot before the earlier half reads them.  They
+        // part of a stage takes a wave two slots, read and multiply, each
+        // ended by a barrier.  The loads for the next stage go out in the
+        // stage's first slot; they have landed for every wave when it waits
+        // for its own before the barrier that ends the last part's reads,
+        // the later half's one slot before the earlier half reads them.  They
         // overwrite what was read two slots earlier or before, and each read
         // has returned before the barrier that ends its slot.
-        auto stage = [&](const char* cur, char* next, int kt) {
+        auto stage = [&](const char* cur, char* other, int kt) {
             if (kt + 1 < total)
-                load(next);
-            read(cur, 0);
-            __builtin_amdgcn_s_waitcnt(wait_count(63, 0));
-            slot_barrier();
-            __builtin_amdgcn_s_setprio(1);
-            multiply();
-            __builtin_amdgcn_s_setprio(0);
-            slot_barrier();
-            read(cur, 1);
-            __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
-            slot_barrier();
-            __builtin_amdgcn_s_setprio(1);
-            multiply();
-            __builtin_amdgcn_s_setprio(0);
-            slot_barrier();
+                load(other);
+#pragma unroll
+            for (int part = 0; part < kParts; ++part) {
+                read(cur, part);
+                if (part + 1 < kParts)
+                    __builtin_amdgcn_s_waitcnt(wait_count(63, 0));
+                else
+                    __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+                slot_barrier();
+                __builtin_amdgcn_s_setprio(1);
+                product(part);
+                __builtin_amdgcn_s_setprio(0);
+                slot_barrier();
+            }
         };
         load(lds0);
         __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
@@ -922,34 +937,31 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         // ST - 1 stages in flight: stage kt is whole when at most the loads
         // of the ST - 2 younger ones are out, and the barrier, which every
         // wave reaches with its reads returned, also frees the stage before.
-        auto stage = [&](const char* cur, char* next, int kt) {
-            if (kt + ST - 2 < total)
-                __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 0));
-            else
-                __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
-            slot_barrier();
-            if (kt + ST - 1 < total)
-                load(next);
+        static_assert(SH::kWaves == 8 || ST == 4 || ST == 8, "stages");
+        char* const bufs[8] = {lds0, lds1, lds2, lds3,
+                               lds4, lds5, lds6, lds7};
 #pragma unroll
-            for (int ks = 0; ks < 2; ++ks) {
-                read(cur, ks);
-                multiply();
+        for (int k = 0; k < ST - 1; ++k)
+            if (k < total)
+                load(bufs[k]);
+        for (int kt = 0; kt < total; kt += ST) {
+#pragma unroll
+            for (int k = 0; k < ST; ++k) {
+                if (kt + k >= total)
+                    break;
+                if (kt + k + ST - 2 < total)
+                    __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 0));
+                else
+                    __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+                slot_barrier();
+                if (kt + k + ST - 1 < total)
+                    load(bufs[(k + ST - 1) % ST]);
+#pragma unroll
+                for (int part = 0; part < kParts; ++part) {
+                    read(bufs[k], part);
+                    product(part);
+                }
             }
-        };
-        static_assert(SH::kWaves == 8 || ST == 4, "four stages");
-        load(lds0);
-        if (total > 1)
-            load(lds1);
-        if (total > 2)
-            load(lds2);
-        for (int kt = 0; kt < total; kt += 4) {
-            stage(lds0, lds3, kt);
-            if (kt + 1 < total)
-                stage(lds1, lds0, kt + 1);
-            if (kt + 2 < total)
-                stage(lds2, lds1, kt + 2);
-            if (kt + 3 < total)
-                stage(lds3, lds2, kt + 3);
         }
     }
 
@@ -1294,20 +1306,24 @@ double estimate(const Group& g, double stage, double alone, double fixed,
 }
 
 // The tile for a product on these stacks, by estimated time.
-template <int EPI>
+template <int EPI, bool FULL>
 int choose_tile(const Group& g)
 {
-    double best = estimate<64, EPI>(g, 0.36, 0.25, 3, 2);
-    int tile = 64;
+    int64_t n = 0;
+    for (int p = 0; p < g.count; ++p)
+        n += (int64_t)g.m[p].batch * d_tiles<64, EPI>(g.m[p]);
+    const double c = FULL ? 2.6 : 1;            // three products for one
+    double best = estimate<64, EPI>(g, 0.36 * c, 0.25 * c, 3, 2);
+    int tile = n <= 256 ? 65 : 64;              // 65: seven stages in flight
     auto offer = [&](int t, double us) {
         if (us < best) {
             best = us;
             tile = t;
         }
     };
-    offer(128, estimate<128, EPI>(g, 0.98, 0.6, 6, 2));
-    offer(192, estimate<192, EPI>(g, 1.12, 0.95, 8, 1));
-    offer(256, estimate<256, EPI>(g, 1.5, 1.4, 12, 1));
+    offer(128, estimate<128, EPI>(g, 0.98 * c, 0.6 * c, 6, 2));
+    offer(192, estimate<192, EPI>(g, 1.12 * c, 0.95 * c, 8, 1));
+    offer(256, estimate<256, EPI>(g, 1.5 * c, 1.4 * c, 12, 1));
     return tile;
 }
 
@@ -1316,6 +1332,7 @@ int launch_product(GemmArgs& a, int tile, hipStream_t s)
 {
     switch (tile) {
     case 64: return launch_gemm<Shape64, EPI, FULL>(a, s);
+    case 65: return launch_gemm<Shape64Deep, EPI, FULL>(a, s);
     case 128: return launch_gemm<Shape128, EPI, FULL>(a, s);
     case 192: return launch_gemm<Shape192, EPI, FULL>(a, s);
     default: return launch_gemm<Shape256, EPI, FULL>(a, s);
@@ -1353,8 +1370,9 @@ template <int LAST, bool FULL>
 int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
 {
     const bool pairs = in_pairs(a.g);
-    const int tGram = choose_tile<kGram>(a.g), tPoly = choose_tile<kPoly>(a.g),
-              tUpdate = choose_tile<kUpdate>(a.g);
+    const int tGram = choose_tile<kGram, FULL>(a.g),
+              tPoly = choose_tile<kPoly, FULL>(a.g),
+              tUpdate = choose_tile<kUpdate, FULL>(a.g);
     a.parity = 0;
     int rc = ZS_OK;
     auto poly = [&](int k, Square out) {

@@ -77,8 +77,10 @@ typedef struct {
  * at k*batch_stride + i*row_stride + j, strides in elements.  x: inputs,
  * o: outputs.  row_stride >= cols; outputs of a stack must not overlap
  * (o_batch_stride >= (rows - 1)*o_row_stride + cols when batch > 1), inputs
- * may (x_batch_stride >= 0).  An output may share memory with any input of
- * the same call: all inputs are read before an output is written. */
+ * may (x_batch_stride >= 0).  A matrix's output may be the matrix itself; an
+ * output that shares elements with another matrix of the call is an error
+ * that is not detected (the order in which matrices are read and written is
+ * not defined). */
 typedef struct {
     const void* x;
     void* o;

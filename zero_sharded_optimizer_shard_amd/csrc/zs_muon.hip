@@ -119,8 +119,11 @@ struct Region {
     {
         return (float*)(ws + d_off() + 4 * k * D);
     }
-    __device__ double* parts() const { return (double*)(ws + parts_off()); }
-    __device__ float* u() const { return (float*)xd(1); }
+    __host__ __device__ double* parts() const
+    {
+        return (double*)(ws + parts_off());
+    }
+    __host__ float* u() const { return (float*)(ws + 4 * E); }  // xd(1)
 };
 
 struct Group {
@@ -250,6 +253,9 @@ __global__ __launch_bounds__(kNT) void ns_norm_kernel(NormArgs a)
 struct MomSrc {
     const uint16_t* grads;
     float* state;                       // the tensor's first tile
+    float* u;                           // where U goes
+    double* parts;                      // and its partial sums of squares,
+                                        // NULL where nobody reads them
 };
 
 struct MomArgs {
@@ -265,7 +271,7 @@ struct MomArgs {
 // of U's squares.  2W + 8 bytes read and written in the state and gradients
 // and 4 for U, per element; bound by HBM.  VEC: four elements a thread
 // (every row of four stays inside a tile, tiles being multiples of four).
-template <bool TILED, bool VEC, bool FULL>
+template <bool TILED, bool VEC>
 __device__ __forceinline__ void momentum_part(const MomArgs& a, const Mat& m,
                                               const MomSrc& s, uint32_t bid)
 {
@@ -274,8 +280,7 @@ __device__ __forceinline__ void momentum_part(const MomArgs& a, const Mat& m,
     const uint32_t n = (uint32_t)m.R * m.C;
     const uint32_t e0 = part * m.chunk;
     const uint32_t e1 = n - e0 < (uint32_t)m.chunk ? n : e0 + m.chunk;
-    const Region<FULL> w(m.ws, m.R, m.C, m.batch);
-    float* const u = w.u();
+    float* const u = s.u;
     double sum = 0;
     for (uint32_t e = e0 + V * threadIdx.x; e < e1; e += V * kNT) {
         const int64_t ge = (int64_t)b * n + e;
@@ -324,21 +329,23 @@ __device__ __forceinline__ void momentum_part(const MomArgs& a, const Mat& m,
             u[ge] = up.x;
         }
     }
+    if (!s.parts)
+        return;
     sum = block_sum(sum);
     if (threadIdx.x == 0)
-        w.parts()[(int64_t)b * m.nparts + part] = sum;
+        s.parts[(int64_t)b * m.nparts + part] = sum;
 }
 
-template <bool TILED, bool FULL>
+template <bool TILED>
 __global__ __launch_bounds__(kNT) void muon_momentum_kernel(MomArgs a)
 {
     uint32_t bid = blockIdx.x;
     const int p = find(a.g, bid);
     const Mat& m = a.g.m[p];
     if (((uint32_t)m.R * m.C) % 4 == 0)
-        momentum_part<TILED, true, FULL>(a, m, a.src[p], bid);
+        momentum_part<TILED, true>(a, m, a.src[p], bid);
     else
-        momentum_part<TILED, false, FULL>(a, m, a.src[p], bid);
+        momentum_part<TILED, false>(a, m, a.src[p], bid);
 }
 
 // ---- X = U / (|U| + eps) into the workspace ---------------------------------------
@@ -356,8 +363,8 @@ __device__ __forceinline__ void split(float x, f16& hi, f16& lo)
 }
 
 // Workgroup = one 64 x 64 tile of one padded matrix: read U, scale, write Xd
-// (hi, lo) and, through LDS, Xt.  SRC: 0 bf16, 1 fp32, 2 the workspace's U.
-template <int SRC, bool FULL>
+// (hi, lo) and, through LDS, Xt.
+template <bool BF16, bool FULL>
 __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
 {
     __shared__ f16 t[FULL ? 2 : 1][64][64 + 4];
@@ -380,23 +387,20 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
     const double inv =
         norm < HUGE_VAL ? (double)kScale / (norm + (double)a.eps) : NAN;
     const Source& s = a.src[p];
-    const void* const x = SRC == 2 ? (const void*)w.u() : s.x;
-    const int64_t xr = SRC == 2 ? m.C : s.row;
-    const int64_t xb = SRC == 2 ? (int64_t)m.R * m.C : s.batch;
     const int tx = threadIdx.x % 16 * 4, ty = threadIdx.x / 16;
 #pragma unroll
     for (int k = 0; k < 4; ++k) {
         const int r = r0 + ty + 16 * k, c = c0 + tx;
         f32x4 v = {0, 0, 0, 0};
         if (r < m.R && c < m.C) {
-            const int64_t i = b * xb + r * xr + c;
+            const int64_t i = b * s.batch + r * s.row + c;
             if (s.vec) {
-                v = load4<SRC == 0>(x, i);
+                v = load4<BF16>(s.x, i);
             } else {
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
                     if (c + q < m.C)
-                        v[q] = load1<SRC == 0>(x, i + q);
+                        v[q] = load1<BF16>(s.x, i + q);
             }
         }
         f16x4 hi, lo;
@@ -1089,6 +1093,299 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     }
 }
 
+// ---- small matrices, whole in one workgroup ---------------------------------------
+
+// A matrix whose shorter side is at most TM and whose longer one at most TN
+// stays in one CU for all steps: one launch instead of three a step, each of
+// which would cost its latency and little else (64 x 64, five steps: SMALL_A us
+// against SMALL_B us).  Below, X is m x n with m the shorter side, transposed on
+// the way in and out where the matrix is tall.  X itself is held by the
+// threads in fp32, laid out as the update's sums; LDS holds the operands of
+// the products: X by rows and by columns and the square A, then C.  The
+// arithmetic is the large kernels', with X kept in fp32.
+template <int TM_, int TN_, int NW_, int GI_, int UI_>
+struct Small {
+    static constexpr int TM = TM_, TN = TN_, NW = NW_;
+    // waves along i and j: of the squares (m x m), of the update (i along n)
+    static constexpr int GI = GI_, GJ = NW / GI, UI = UI_, UJ = NW / UI;
+    static constexpr int kThreads = 64 * NW;
+};
+
+struct SmallArgs {
+    Group g;
+    Source src[kMaxMats];
+    union {
+        OutMat out[kMaxMats];
+        StepMat st[kMaxMats];
+    };
+    int32_t bf16;                       // the source's type
+    int32_t epi;                        // kOutBf16, kOutF32 or kStep
+    int32_t steps;
+    float eps, dec;
+    float coef[ZS_NS_MAX_STEPS][3];
+};
+static_assert(sizeof(SmallArgs) <= 4096, "kernel arguments");
+
+// Byte offset of element (row, col) of an fp16 matrix of L columns in LDS:
+// 16-byte pieces permuted within each 128 bytes by the row.
+template <int L>
+__device__ __forceinline__ int lds_at(int row, int col)
+{
+    return row * (2 * L) + (col >> 6) * 128 +
+           ((((col >> 3) & 7) ^ (row & 7)) << 4) + (col & 7) * 2;
+}
+
+// acc[i][j] += sum over K columns of P's rows p0 + 16 i .. and Q's rows
+// q0 + 16 j ..; FULL: high and low parts, the low ones LP and LQ bytes on.
+template <int FI, int FJ, int K, bool FULL>
+__device__ __forceinline__ void lds_product(f32x4 (&acc)[FI][FJ],
+                                            const char* P, int LP, int p0,
+                                            const char* Q, int LQ, int q0)
+{
+    const int l16 = threadIdx.x & 15, g = (threadIdx.x >> 4) & 3;
+#pragma unroll
+    for (int i = 0; i < FI; ++i)
+#pragma unroll
+        for (int j = 0; j < FJ; ++j)
+            acc[i][j] = f32x4{0, 0, 0, 0};
+#pragma unroll 2
+    for (int k = 0; k < K; k += 32) {
+#pragma unroll
+        for (int part = 0; part < (FULL ? 3 : 1); ++part) {
+            f16x8 x[FI], y[FJ];
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+                x[i] = *reinterpret_cast<const f16x8*>(
+                    P + (part == 2 ? LP : 0) +
+                    lds_at<K>(p0 + 16 * i + l16, k + 8 * g));
+#pragma unroll
+            for (int j = 0; j < FJ; ++j)
+                y[j] = *reinterpret_cast<const f16x8*>(
+                    Q + (part == 1 ? LQ : 0) +
+                    lds_at<K>(q0 + 16 * j + l16, k + 8 * g));
+#pragma unroll
+            for (int i = 0; i < FI; ++i)
+#pragma unroll
+                for (int j = 0; j < FJ; ++j)
+                    acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
+                        x[i], y[j], acc[i][j], 0, 0, 0);
+        }
+    }
+}
+
+template <class SM, bool FULL>
+__global__ __launch_bounds__(SM::kThreads) void ns_small_kernel(SmallArgs a)
+{
+    constexpr int TM = SM::TM, TN = SM::TN, F = FULL ? 2 : 1;
+    constexpr int GFI = TM / SM::GI / 16, GFJ = TM / SM::GJ / 16;
+    constexpr int UFI = TN / SM::UI / 16, UFJ = TM / SM::UJ / 16;
+    constexpr int LX = TM * TN * 2, LS = TM * TM * 2;
+    __shared__ __align__(1024) char xm[LX * F];     // X  [m][n]
+    __shared__ __align__(1024) char xt[LX * F];     // X^T [n][m]
+    __shared__ __align__(1024) char sq[LS * F];     // A, then C
+    __shared__ float dg[TM];                        // its diagonal
+    __shared__ double red[SM::NW];
+
+    uint32_t b = blockIdx.x;
+    const int p = find(a.g, b);
+    const Mat& m = a.g.m[p];
+    const Source& s = a.src[p];
+    const bool tall = m.R > m.C;
+    const int M = tall ? m.C : m.R, N = tall ? m.R : m.C;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int l16 = lane & 15, g = lane >> 4;
+    const int gi = wave / SM::GJ * GFI * 16, gj = wave % SM::GJ * GFJ * 16;
+    const int ui = wave / SM::UJ * UFI * 16, uj = wave % SM::UJ * UFJ * 16;
+
+    // X, this thread's elements: n index ui + 16 i + 4 g + q, m index
+    // uj + 16 j + l16
+    f32x4 x[UFI][UFJ];
+    double sum = 0;
+    const int64_t sn = tall ? s.row : 1, sm = tall ? 1 : s.row;
+#pragma unroll
+    for (int i = 0; i < UFI; ++i)
+#pragma unroll
+        for (int j = 0; j < UFJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = ui + 16 * i + 4 * g + q, r = uj + 16 * j + l16;
+                float v = 0;
+                if (n < N && r < M) {
+                    const int64_t at = b * s.batch + r * sm + n * sn;
+                    v = a.bf16 ? load1<true>(s.x, at) : load1<false>(s.x, at);
+                }
+                x[i][j][q] = v;
+                sum += (double)v * v;
+            }
+    for (int d = 32; d; d >>= 1)
+        sum += __shfl_down(sum, d, 64);
+    if (lane == 0)
+        red[wave] = sum;
+    __syncthreads();
+    sum = 0;
+    for (int w = 0; w < SM::NW; ++w)
+        sum += red[w];
+    const double norm = sqrt(sum);
+    // a matrix with a NaN or an infinity is NaN everywhere
+    const double inv =
+        norm < HUGE_VAL ? (double)kScale / (norm + (double)a.eps) : NAN;
+#pragma unroll
+    for (int i = 0; i < UFI; ++i)
+#pragma unroll
+        for (int j = 0; j < UFJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                x[i][j][q] = (float)((double)x[i][j][q] * inv);
+
+    for (int step = 0; step < a.steps; ++step) {
+        const float ca = a.coef[step][0], cb = a.coef[step][1],
+                    cc = a.coef[step][2];
+        // X's operands
+#pragma unroll
+        for (int i = 0; i < UFI; ++i)
+#pragma unroll
+            for (int j = 0; j < UFJ; ++j) {
+                const int n = ui + 16 * i + 4 * g, r = uj + 16 * j + l16;
+                f16x4 hi, lo;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    f16 h, l;
+                    split(x[i][j][q], h, l);
+                    hi[q] = h;
+                    lo[q] = l;
+                    *reinterpret_cast<f16*>(xt + lds_at<TM>(n + q, r)) = h;
+                    if constexpr (FULL)
+                        *reinterpret_cast<f16*>(xt + LX +
+                                                lds_at<TM>(n + q, r)) = l;
+                }
+                *reinterpret_cast<f16x4*>(xm + lds_at<TN>(r, n)) = hi;
+                if constexpr (FULL)
+                    *reinterpret_cast<f16x4*>(xm + LX + lds_at<TN>(r, n)) =
+                        lo;
+            }
+        __syncthreads();
+        // A = X X^T, its diagonal apart
+        f32x4 A[GFI][GFJ], S[GFI][GFJ];
+        auto store = [&](const f32x4 (&v)[GFI][GFJ]) {
+#pragma unroll
+            for (int i = 0; i < GFI; ++i)
+#pragma unroll
+                for (int j = 0; j < GFJ; ++j) {
+                    const int at = lds_at<TM>(gj + 16 * j + l16,
+                                              gi + 16 * i + 4 * g);
+                    f16x4 hi, lo;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        f16 h, l;
+                        split(v[i][j][q], h, l);
+                        hi[q] = h;
+                        lo[q] = l;
+                    }
+                    *reinterpret_cast<f16x4*>(sq + at) = hi;
+                    if constexpr (FULL)
+                        *reinterpret_cast<f16x4*>(sq + LS + at) = lo;
+                }
+        };
+        lds_product<GFI, GFJ, TN, FULL>(A, xm, LX, gi, xm, LX, gj);
+#pragma unroll
+        for (int i = 0; i < GFI; ++i)
+#pragma unroll
+            for (int j = 0; j < GFJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    A[i][j][q] = A[i][j][q] * kUnscale;
+                    if (gi + 16 * i + 4 * g + q == gj + 16 * j + l16) {
+                        dg[gj + 16 * j + l16] = A[i][j][q] * kUnscale;
+                        A[i][j][q] = 0;
+                    }
+                }
+        store(A);
+        __syncthreads();
+        // C = a + b A + c A A
+        lds_product<GFI, GFJ, TM, FULL>(S, sq, LS, gi, sq, LS, gj);
+        float dc[GFI][GFJ];
+#pragma unroll
+        for (int i = 0; i < GFI; ++i)
+#pragma unroll
+            for (int j = 0; j < GFJ; ++j) {
+                const float dj = dg[gj + 16 * j + l16];
+                dc[i][j] = 0;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    const int t = gi + 16 * i + 4 * g + q;
+                    const float d = S[i][j][q] * kUnscale;
+                    const float r = A[i][j][q];
+                    S[i][j][q] = cb * r + cc * (d + (dg[t] + dj) * r);
+                    if (t == gj + 16 * j + l16) {
+                        dc[i][j] = ca + (cb * dj +
+                                         cc * (d * kUnscale + dj * dj));
+                        S[i][j][q] = 0;
+                    }
+                }
+            }
+        __syncthreads();                // A and its diagonal have been read
+#pragma unroll
+        for (int i = 0; i < GFI; ++i)
+#pragma unroll
+            for (int j = 0; j < GFJ; ++j)
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    if (gi + 16 * i + 4 * g + q == gj + 16 * j + l16)
+                        dg[gj + 16 * j + l16] = dc[i][j];
+        store(S);
+        __syncthreads();
+        // X <- C X
+        f32x4 U[UFI][UFJ];
+        lds_product<UFI, UFJ, TM, FULL>(U, xt, LX, ui, sq, LS, uj);
+#pragma unroll
+        for (int i = 0; i < UFI; ++i)
+#pragma unroll
+            for (int j = 0; j < UFJ; ++j) {
+                const float dj = dg[uj + 16 * j + l16];
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+                    x[i][j][q] = dj * x[i][j][q] + U[i][j][q] * kUnscale;
+            }
+        __syncthreads();                // the operands have been read
+    }
+
+#pragma unroll
+    for (int i = 0; i < UFI; ++i)
+#pragma unroll
+        for (int j = 0; j < UFJ; ++j)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int n = ui + 16 * i + 4 * g + q, r = uj + 16 * j + l16;
+                if (n >= N || r >= M)
+                    continue;
+                const float v = x[i][j][q] * kUnscale;
+                const int64_t row = tall ? n : r, col = tall ? r : n;
+                if (a.epi == kStep) {
+                    const StepMat& o = a.st[p];
+                    const int64_t e = (b * (int64_t)m.R + row) * m.C + col;
+                    float* const s1 =
+                        o.state + e / kTile * 3 * kTile + e % kTile;
+                    const float t = *s1 * a.dec;
+                    const float u = o.s * v;
+                    const float w = t - u;
+                    *s1 = w;
+                    const uint16_t h = (uint16_t)to_bf16(w);
+                    if (o.pshard)
+                        o.pshard[e] = h;
+                    if (o.flat)
+                        o.flat[e] = h;
+                } else {
+                    const OutMat& o = a.out[p];
+                    const int64_t at = b * o.batch + row * o.row + col;
+                    if (a.epi == kOutBf16)
+                        static_cast<uint16_t*>(o.o)[at] =
+                            (uint16_t)to_bf16(v);
+                    else
+                        static_cast<float*>(o.o)[at] = v;
+                }
+            }
+}
+
 // ---- host ---------------------------------------------------------------------------
 
 int check_launch(const char* what)
@@ -1172,9 +1469,30 @@ void set_parts(Mat& m)
     m.nparts = (int32_t)((n + m.chunk - 1) / m.chunk);
 }
 
+typedef Small<64, 64, 4, 2, 2> Small64;
+typedef Small<64, 256, 8, 2, 8> Small256;
+typedef Small<64, 512, 8, 2, 8> Small512;
+typedef Small<128, 128, 8, 2, 2> Small128;
+
+// Which of the small kernels takes a matrix: 1 .. kSmalls, 0 for none.  Full
+// precision's pairs leave LDS for the first two.
+constexpr int kSmalls = 4;
+int small_kind(int32_t R, int32_t C, bool full)
+{
+    const int32_t rp = padded(R), cp = padded(C);
+    const int32_t m = rp < cp ? rp : cp, n = rp < cp ? cp : rp;
+    if (m == 64 && n <= 64) return 1;
+    if (m == 64 && n <= 256) return 2;
+    if (full) return 0;
+    if (m == 64 && n <= 512) return 3;
+    return m == 128 && n == 128 ? 4 : 0;
+}
+
 // A stack's bytes of workspace.
 int64_t mat_bytes(const Mat& m, bool full)
 {
+    if (small_kind(m.R, m.C, full))     // U alone
+        return (4 * (int64_t)m.batch * m.R * m.C + 255) / 256 * 256;
     const int64_t parts = 8 * (int64_t)m.batch * m.nparts;
     const int64_t off =
         full ? Region<true>(nullptr, m.R, m.C, m.batch).parts_off()
@@ -1419,7 +1737,7 @@ uint32_t init_tiles(const Mat& m)
     return (uint32_t)(padded(m.R) / 64) * (uint32_t)(padded(m.C) / 64);
 }
 
-template <int SRC, bool FULL>
+template <bool BF16, bool FULL>
 int launch_init(const Group& g, const Source* src, float eps, hipStream_t s)
 {
     InitArgs a;
@@ -1428,33 +1746,129 @@ int launch_init(const Group& g, const Source* src, float eps, hipStream_t s)
         a.src[i] = src[i];
     a.eps = eps;
     const uint32_t n = set_starts(a.g, init_tiles);
-    hipLaunchKernelGGL((ns_init_kernel<SRC, FULL>), dim3(n), dim3(kNT), 0, s,
+    hipLaunchKernelGGL((ns_init_kernel<BF16, FULL>), dim3(n), dim3(kNT), 0, s,
                        a);
     return check_launch("Newton-Schulz start");
 }
 
-template <bool BF16, bool FULL>
-int orthogonalize(const Group& g, const Source* src, const OutMat* out,
-                  int32_t o_type, const zs_newton_schulz& ns, hipStream_t s)
+template <class SM, bool FULL>
+int launch_small(SmallArgs& a, hipStream_t s)
 {
-    NormArgs na;
-    na.g = g;
+    const uint32_t n = set_starts(a.g, [](const Mat&) { return 1; });
+    hipLaunchKernelGGL((ns_small_kernel<SM, FULL>), dim3(n),
+                       dim3(SM::kThreads), 0, s, a);
+    return check_launch("Newton-Schulz steps");
+}
+
+// What a call does with the stacks of a group: src where they come from, out
+// or st where they go.
+struct Work {
+    const Group* g;
+    const Source* src;
+    int32_t x_type;
+    int epi;                            // kOutBf16, kOutF32 or kStep
+    const OutMat* out;
+    const StepMat* st;
+    float dec;
+    const zs_newton_schulz* ns;
+};
+
+// The small stacks of each kind, and the rest into `g` (with its members'
+// places in the whole group in `at`).
+template <bool FULL>
+int run_small(const Work& w, Group& g, int* at, hipStream_t s)
+{
+    g.count = 0;
+    for (int kind = 0; kind <= kSmalls; ++kind) {
+        SmallArgs a;
+        a.g.count = 0;
+        for (int i = 0; i < w.g->count; ++i) {
+            const Mat& m = w.g->m[i];
+            if (small_kind(m.R, m.C, FULL) != kind)
+                continue;
+            if (kind == 0) {
+                at[g.count] = i;
+                g.m[g.count++] = m;
+                continue;
+            }
+            const int n = a.g.count++;
+            a.g.m[n] = m;
+            a.src[n] = w.src[i];
+            if (w.epi == kStep)
+                a.st[n] = w.st[i];
+            else
+                a.out[n] = w.out[i];
+        }
+        if (kind == 0 || a.g.count == 0)
+            continue;
+        a.bf16 = w.x_type == ZS_BF16;
+        a.epi = w.epi;
+        a.steps = w.ns->steps;
+        a.eps = w.ns->eps;
+        a.dec = w.dec;
+        for (int k = 0; k < ZS_NS_MAX_STEPS; ++k)
+            for (int q = 0; q < 3; ++q)
+                a.coef[k][q] = k < a.steps ? w.ns->coef[k][q] : 0;
+        int rc;
+        if (kind == 1) {
+            rc = launch_small<Small64, FULL>(a, s);
+        } else if (kind == 2) {
+            rc = launch_small<Small256, FULL>(a, s);
+        } else if constexpr (FULL) {
+            rc = ZS_OK;
+        } else {
+            rc = kind == 3 ? launch_small<Small512, FULL>(a, s)
+                           : launch_small<Small128, FULL>(a, s);
+        }
+        if (rc) return rc;
+    }
+    return ZS_OK;
+}
+
+// The large stacks, whose partial sums of squares are in the workspace.
+template <bool FULL>
+int run_large(const Work& w, const Group& g, const int* at, hipStream_t s)
+{
+    Source src[kMaxMats];
     for (int i = 0; i < g.count; ++i)
-        na.src[i] = src[i];
-    const uint32_t n =
-        set_starts(na.g, [](const Mat& m) { return m.nparts; });
-    hipLaunchKernelGGL((ns_norm_kernel<BF16, FULL>), dim3(n), dim3(kNT), 0,
-                       s, na);
-    int rc = check_launch("norm kernel");
-    if (!rc) rc = launch_init<BF16 ? 0 : 1, FULL>(g, src, ns.eps, s);
+        src[i] = w.src[at[i]];
+    const int rc = w.x_type == ZS_BF16
+                       ? launch_init<true, FULL>(g, src, w.ns->eps, s)
+                       : launch_init<false, FULL>(g, src, w.ns->eps, s);
     if (rc) return rc;
     GemmArgs a;
     a.g = g;
+    a.dec = w.dec;
     for (int i = 0; i < g.count; ++i)
-        a.out[i] = out[i];
-    a.dec = 1;
-    return o_type == ZS_BF16 ? run_steps<kOutBf16, FULL>(a, ns, s)
-                             : run_steps<kOutF32, FULL>(a, ns, s);
+        if (w.epi == kStep)
+            a.st[i] = w.st[at[i]];
+        else
+            a.out[i] = w.out[at[i]];
+    return w.epi == kOutBf16  ? run_steps<kOutBf16, FULL>(a, *w.ns, s)
+           : w.epi == kOutF32 ? run_steps<kOutF32, FULL>(a, *w.ns, s)
+                              : run_steps<kStep, FULL>(a, *w.ns, s);
+}
+
+template <bool FULL>
+int orthogonalize(const Work& w, hipStream_t s)
+{
+    NormArgs na;
+    int at[kMaxMats];
+    if (const int rc = run_small<FULL>(w, na.g, at, s)) return rc;
+    if (na.g.count == 0) return ZS_OK;
+    const Group g = na.g;
+    for (int i = 0; i < g.count; ++i)
+        na.src[i] = w.src[at[i]];
+    const uint32_t n =
+        set_starts(na.g, [](const Mat& m) { return m.nparts; });
+    if (w.x_type == ZS_BF16)
+        hipLaunchKernelGGL((ns_norm_kernel<true, FULL>), dim3(n), dim3(kNT),
+                           0, s, na);
+    else
+        hipLaunchKernelGGL((ns_norm_kernel<false, FULL>), dim3(n), dim3(kNT),
+                           0, s, na);
+    if (const int rc = check_launch("norm kernel")) return rc;
+    return run_large<FULL>(w, g, at, s);
 }
 
 }  // namespace
@@ -1560,11 +1974,9 @@ extern "C" int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
         return fail(ZS_ERANGE, "workspace of %lld bytes, %lld needed",
                     (long long)workspace_bytes, (long long)used);
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    if (x_type == ZS_BF16)
-        return full ? orthogonalize<true, true>(g, src, out, o_type, *ns, s)
-                    : orthogonalize<true, false>(g, src, out, o_type, *ns, s);
-    return full ? orthogonalize<false, true>(g, src, out, o_type, *ns, s)
-                : orthogonalize<false, false>(g, src, out, o_type, *ns, s);
+    const Work w = {&g, src, x_type, o_type == ZS_BF16 ? kOutBf16 : kOutF32,
+                    out, nullptr, 1.f, ns};
+    return full ? orthogonalize<true>(w, s) : orthogonalize<false>(w, s);
 }
 
 namespace {
@@ -1620,25 +2032,34 @@ int muon_step(const Group& g, MomArgs& ma, const StepMat* st, bool tiled,
               const zs_muon& hp, hipStream_t s)
 {
     ma.g = g;
+    Source src[kMaxMats] = {};
+    for (int i = 0; i < g.count; ++i) {
+        const Mat& m = g.m[i];
+        const bool small = small_kind(m.R, m.C, FULL) != 0;
+        const Region<FULL> r(m.ws, m.R, m.C, m.batch);
+        ma.src[i].u = small ? (float*)m.ws : r.u();
+        ma.src[i].parts = small ? nullptr : r.parts();
+        src[i].x = ma.src[i].u;
+        src[i].row = m.C;
+        src[i].batch = (int64_t)m.R * m.C;
+        src[i].vec = m.C % 4 == 0;
+    }
     const uint32_t n =
         set_starts(ma.g, [](const Mat& m) { return m.nparts; });
     if (tiled)
-        hipLaunchKernelGGL((muon_momentum_kernel<true, FULL>), dim3(n),
-                           dim3(kNT), 0, s, ma);
+        hipLaunchKernelGGL(muon_momentum_kernel<true>, dim3(n), dim3(kNT), 0,
+                           s, ma);
     else
-        hipLaunchKernelGGL((muon_momentum_kernel<false, FULL>), dim3(n),
-                           dim3(kNT), 0, s, ma);
+        hipLaunchKernelGGL(muon_momentum_kernel<false>, dim3(n), dim3(kNT),
+                           0, s, ma);
     if (const int rc = check_launch("momentum kernel")) return rc;
-    Source src[kMaxMats] = {};
-    for (int i = 0; i < g.count; ++i)
-        src[i].vec = g.m[i].C % 4 == 0;
-    if (const int rc = launch_init<2, FULL>(g, src, hp.ns.eps, s)) return rc;
-    GemmArgs a;
-    a.g = g;
-    for (int i = 0; i < g.count; ++i)
-        a.st[i] = st[i];
-    a.dec = (float)(1.0 - (double)hp.lr * (double)hp.weight_decay);
-    return run_steps<kStep, FULL>(a, hp.ns, s);
+    const Work w = {&g, src, ZS_F32, kStep, nullptr, st,
+                    (float)(1.0 - (double)hp.lr * (double)hp.weight_decay),
+                    &hp.ns};
+    Group large;
+    int at[kMaxMats];
+    if (const int rc = run_small<FULL>(w, large, at, s)) return rc;
+    return large.count ? run_large<FULL>(w, large, at, s) : ZS_OK;
 }
 
 }  // namespace

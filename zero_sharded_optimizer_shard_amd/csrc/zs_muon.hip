@@ -479,6 +479,7 @@ template <int BT_, int WI_, int WJ_, int ST_>
 struct Shape {
     static constexpr int BT = BT_, WI = WI_, WJ = WJ_, ST = ST_;
     static constexpr int kWaves = WI * WJ, kThreads = 64 * kWaves;
+    static constexpr bool kTurns = kWaves == 8;     // see the kernel
     static constexpr int FI = BT / WI / 16, FJ = BT / WJ / 16;
     static constexpr int kRow = 128;                // bytes of a stage's row
     static constexpr int kHalf = BT * kRow;         // bytes per operand
@@ -495,8 +496,8 @@ struct Shape {
 typedef Shape<256, 2, 4, 2> Shape256;
 typedef Shape<192, 2, 4, 2> Shape192;
 typedef Shape<128, 2, 4, 2> Shape128;
-// Small matrices are bound by the latency of a stage: three in flight, or
-// seven where there is a CU for every tile.
+// Small matrices are bound by the latency of a stage: four in LDS, or eight
+// where there is a CU for every tile.
 typedef Shape<64, 2, 2, 4> Shape64;
 typedef Shape<64, 2, 2, 8> Shape64Deep;
 
@@ -866,39 +867,38 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
 
     // Fragments: half h of a stage's rows (k 0..31 and 32..63, or the high and
     // the low parts).
-    f16x8 x[FI], y[FULL ? 2 : 1][FJ];
-    auto readx = [&](const char* lds, int h) {
+    auto readx = [&](const char* lds, int h, f16x8 (&x)[FI]) {
 #pragma unroll
         for (int i = 0; i < FI; ++i)
             x[i] = *reinterpret_cast<const f16x8*>(
                 lds + fi + (i / 2 * 32 + i % 2 * 4) * kRow + (fc ^ (h * 64)));
     };
-    auto ready = [&](const char* lds, int h) {
+    auto ready = [&](const char* lds, int h, f16x8 (&y)[FJ]) {
 #pragma unroll
         for (int j = 0; j < FJ; ++j)
-            y[FULL ? h : 0][j] = *reinterpret_cast<const f16x8*>(
-                lds + fj + j * kRow + (fc ^ (h * 64)));
+            y[j] = *reinterpret_cast<const f16x8*>(lds + fj + j * kRow +
+                                                   (fc ^ (h * 64)));
     };
-    auto multiply = [&](int h) {
+    auto multiply = [&](const f16x8 (&x)[FI], const f16x8 (&y)[FJ]) {
 #pragma unroll
         for (int i = 0; i < FI; ++i)
 #pragma unroll
             for (int j = 0; j < FJ; ++j)
                 acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_f16(
-                    x[i], y[h][j], acc[i][j], 0, 0, 0);
+                    x[i], y[j], acc[i][j], 0, 0, 0);
     };
-    // A stage's products, each after its reads: k 0..31 and 32..63, or in
-    // full precision high x high, high x low and low x high.
-    constexpr int kParts = FULL ? 3 : 2;
-    auto read = [&](const char* lds, int part) {
-        if (!FULL || part < 2)
-            ready(lds, part);
-        if (!FULL || part != 1)
-            readx(lds, part != 0);
-    };
-    auto product = [&](int part) { multiply(FULL && part == 1); };
-
-    if constexpr (SH::kWaves == 8) {
+    if constexpr (SH::kTurns) {
+        // A stage's products, each after its reads: k 0..31 and 32..63, or in
+        // full precision high x high, high x low and low x high.
+        constexpr int kParts = FULL ? 3 : 2;
+        f16x8 x[FI], y[FULL ? 2 : 1][FJ];
+        auto read = [&](const char* lds, int part) {
+            if (!FULL || part < 2)
+                ready(lds, part, y[FULL ? part : 0]);
+            if (!FULL || part != 1)
+                readx(lds, part != 0, x);
+        };
+        auto product = [&](int part) { multiply(x, y[FULL && part == 1]); };
         // The waves of a SIMD (w and w + 4) run one slot apart: while one
         // multiplies, the other reads its fragments and issues loads.  A
         // part of a stage takes a wave two slots, read and multiply, each
@@ -938,33 +938,57 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         if (wave < 4)
             slot_barrier();
     } else {
-        // ST - 1 stages in flight: stage kt is whole when at most the loads
-        // of the ST - 2 younger ones are out, and the barrier, which every
-        // wave reaches with its reads returned, also frees the stage before.
-        static_assert(SH::kWaves == 8 || ST == 4 || ST == 8, "stages");
+        // ST stages in LDS, fragments in two register sets: while the products
+        // of stage k run, stage k + 1 is read.  At the top of turn k stage
+        // k + 1 is whole when at most the loads of the ST - 2 younger ones
+        // are out, and this wave's reads of stage k have returned; after the
+        // barrier that holds for every wave, and stage k's place is free.
+        static_assert(SH::kTurns || ST == 4 || ST == 8, "stages");
         char* const bufs[8] = {lds0, lds1, lds2, lds3,
                                lds4, lds5, lds6, lds7};
+        f16x8 fx[2][2][FI], fy[2][2][FJ];       // [set][half]
+        auto readAll = [&](const char* lds, int set) {
 #pragma unroll
-        for (int k = 0; k < ST - 1; ++k)
+            for (int h = 0; h < 2; ++h) {
+                readx(lds, h, fx[set][h]);
+                ready(lds, h, fy[set][h]);
+            }
+        };
+        auto mulAll = [&](int set) {
+            multiply(fx[set][0], fy[set][0]);
+            if constexpr (FULL) {
+                multiply(fx[set][0], fy[set][1]);
+                multiply(fx[set][1], fy[set][0]);
+            } else {
+                multiply(fx[set][1], fy[set][1]);
+            }
+        };
+#pragma unroll
+        for (int k = 0; k < ST; ++k)
             if (k < total)
                 load(bufs[k]);
+        if (total >= ST)
+            __builtin_amdgcn_s_waitcnt(wait_count((ST - 1) * NL, 0));
+        else
+            __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+        slot_barrier();
+        readAll(bufs[0], 0);
         for (int kt = 0; kt < total; kt += ST) {
 #pragma unroll
             for (int k = 0; k < ST; ++k) {
                 if (kt + k >= total)
                     break;
-                if (kt + k + ST - 2 < total)
+                if (kt + k + ST - 1 < total)
                     __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 0));
                 else
                     __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
                 slot_barrier();
-                if (kt + k + ST - 1 < total)
-                    load(bufs[(k + ST - 1) % ST]);
-#pragma unroll
-                for (int part = 0; part < kParts; ++part) {
-                    read(bufs[k], part);
-                    product(part);
-                }
+                if (kt + k + ST < total)
+                    load(bufs[k]);
+                if (kt + k + 1 < total)
+                    readAll(bufs[(k + 1) % ST], (k + 1) % 2);
+                __builtin_amdgcn_sched_barrier(0);
+                mulAll(k % 2);
             }
         }
     }
@@ -1632,7 +1656,7 @@ int choose_tile(const Group& g)
         n += (int64_t)g.m[p].batch * d_tiles<64, EPI>(g.m[p]);
     const double c = FULL ? 2.6 : 1;            // three products for one
     double best = estimate<64, EPI>(g, 0.36 * c, 0.25 * c, 3, 2);
-    int tile = n <= 256 ? 65 : 64;              // 65: seven stages in flight
+    int tile = n <= 256 ? 65 : 64;              // 65: eight stages in LDS
     auto offer = [&](int t, double us) {
         if (us < best) {
             best = us;

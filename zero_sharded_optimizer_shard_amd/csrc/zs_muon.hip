@@ -973,7 +973,20 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
             __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
         slot_barrier();
         readAll(bufs[0], 0);
-        for (int kt = 0; kt < total; kt += ST) {
+        int kt = 0;
+        for (; kt + 2 * ST <= total; kt += ST) {    // no stage is missing
+#pragma unroll
+            for (int k = 0; k < ST; ++k) {
+                __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 0));
+                slot_barrier();
+                load(bufs[k]);
+                readAll(bufs[(k + 1) % ST], (k + 1) % 2);
+                __builtin_amdgcn_sched_barrier(0);
+                mulAll(k % 2);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+        for (; kt < total; kt += ST) {
 #pragma unroll
             for (int k = 0; k < ST; ++k) {
                 if (kt + k >= total)

@@ -128,17 +128,25 @@ struct Region {
 
 struct Group {
     int32_t count;
-    uint32_t start[kMaxMats + 1];       // first workgroup of each stack
+    uint32_t start[kMaxMats];           // first workgroup of each stack; past
+                                        // the last one 2^32 - 1
     Mat m[kMaxMats];
 };
 
-// The stack of workgroup `bid`, and the workgroup's index within it.
+// The stack of workgroup `bid`, and the workgroup's index within it.  All
+// starts are read at once: kernel arguments are far away, and a search would
+// wait for each in turn.
 __device__ __forceinline__ int find(const Group& g, uint32_t& bid)
 {
     int p = 0;
-    while (p + 1 < g.count && bid >= g.start[p + 1])
-        ++p;
-    bid -= g.start[p];
+    uint32_t s = 0;
+#pragma unroll
+    for (int k = 1; k < kMaxMats; ++k) {
+        const uint32_t t = g.start[k];
+        p = bid >= t ? k : p;
+        s = bid >= t ? t : s;
+    }
+    bid -= s;
     return p;
 }
 
@@ -1590,7 +1598,8 @@ uint32_t set_starts(Group& g, Fn fn, uint32_t align = 1)
         g.m[i].tiles = (uint32_t)g.m[i].batch * (uint32_t)fn(g.m[i]);
         n += (g.m[i].tiles + align - 1) / align * align;
     }
-    g.start[g.count] = n;
+    for (int i = g.count; i < kMaxMats; ++i)
+        g.start[i] = UINT32_MAX;
     return n;
 }
 

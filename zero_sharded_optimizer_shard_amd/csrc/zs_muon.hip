@@ -64,7 +64,6 @@ struct Mat {
     int32_t R, C;           // rows, cols
     int32_t batch;
     int32_t nparts;         // partial sums of squares per matrix
-    int32_t chunk;          // elements behind each of them
     uint32_t tiles;         // workgroups of the present launch
 };
 
@@ -166,6 +165,11 @@ __device__ __forceinline__ uint32_t to_bf16(float f)
 // ---- sums of squares ---------------------------------------------------------
 
 constexpr int kNT = 256;                // threads of the elementwise kernels
+// Elements behind one partial sum: a workgroup takes them at once, all loads
+// before the arithmetic.
+constexpr int kNormChunk = 8192, kMomChunk = 2048;
+constexpr int32_t kMaxParts = 2048;     // more are summed by a launch of their
+                                        // own
 
 // Sum over the workgroup in a fixed order; valid in thread 0.
 __device__ __forceinline__ double block_sum(double v)
@@ -234,14 +238,24 @@ __global__ __launch_bounds__(kNT) void ns_norm_kernel(NormArgs a)
     const Source& s = a.src[p];
     const uint32_t b = bid / m.nparts, part = bid % m.nparts;
     const uint32_t n = (uint32_t)m.R * m.C;
-    const uint32_t e0 = part * m.chunk;
-    const uint32_t e1 = n - e0 < (uint32_t)m.chunk ? n : e0 + m.chunk;
+    const uint32_t e0 = part * kNormChunk;
+    const uint32_t e1 = n - e0 < (uint32_t)kNormChunk ? n : e0 + kNormChunk;
     double sum = 0;
     if (s.vec) {
-        for (uint32_t e = e0 + 4 * threadIdx.x; e < e1; e += 4 * kNT) {
-            const uint32_t r = e / m.C, c = e % m.C;
-            sum += sq4(load4<BF16>(s.x, b * s.batch + r * s.row + c));
+        constexpr int U = kNormChunk / (4 * kNT);
+        f32x4 x[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const uint32_t e = e0 + 4 * (u * kNT + threadIdx.x);
+            x[u] = f32x4{0, 0, 0, 0};
+            if (e < e1) {
+                const uint32_t r = e / m.C, c = e % m.C;
+                x[u] = load4<BF16>(s.x, b * s.batch + r * s.row + c);
+            }
         }
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            sum += sq4(x[u]);
     } else {
         for (uint32_t e = e0 + threadIdx.x; e < e1; e += kNT) {
             const uint32_t r = e / m.C, c = e % m.C;
@@ -279,62 +293,96 @@ struct MomArgs {
 // of U's squares.  2W + 8 bytes read and written in the state and gradients
 // and 4 for U, per element; bound by HBM.  VEC: four elements a thread
 // (every row of four stays inside a tile, tiles being multiples of four).
-template <bool TILED, bool VEC>
+template <int WT, bool TILED, bool VEC>
 __device__ __forceinline__ void momentum_part(const MomArgs& a, const Mat& m,
                                               const MomSrc& s, uint32_t bid)
 {
-    constexpr int V = VEC ? 4 : 1;
+    constexpr int V = VEC ? 4 : 1, U = kMomChunk / (V * kNT);
+    constexpr int NB = WT ? WT : 8;     // slices loaded at a time
+    constexpr int UB = VEC ? U : 2;     // and elements (V each)
     const uint32_t b = bid / m.nparts, part = bid % m.nparts;
     const uint32_t n = (uint32_t)m.R * m.C;
-    const uint32_t e0 = part * m.chunk;
-    const uint32_t e1 = n - e0 < (uint32_t)m.chunk ? n : e0 + m.chunk;
-    float* const u = s.u;
+    const uint32_t e0 = part * kMomChunk;
+    const uint32_t e1 = n - e0 < (uint32_t)kMomChunk ? n : e0 + kMomChunk;
+    const int W = WT ? WT : a.W;
     double sum = 0;
-    for (uint32_t e = e0 + V * threadIdx.x; e < e1; e += V * kNT) {
-        const int64_t ge = (int64_t)b * n + e;
-        const int64_t tile = ge / kTile, pos = ge % kTile;
-        const uint16_t* const gp =
-            TILED ? s.grads + tile * a.W * kTile + pos : s.grads + ge;
+#pragma unroll
+    for (int u0 = 0; u0 < U; u0 += UB) {
+        f32x4 mom[UB], acc[UB];         // V of each four in use
+        float* mp[UB];
+        const uint16_t* gp[UB];
+        int64_t ge[UB];
+        bool in[UB];
         const int64_t gs = TILED ? kTile : a.gstride;
-        float* const mp = s.state + (tile * 3 + 1) * kTile + pos;
-        f32x4 mom, acc, up;             // V of the four in use
-        if constexpr (VEC)
-            mom = *reinterpret_cast<const f32x4*>(mp);
-        else
-            mom.x = *mp;
-        for (int s0 = 0; s0 < a.W; s0 += 8) {
-            f32x4 x[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (s0 + i < a.W) {
-                    if constexpr (VEC)
-                        x[i] = load4<true>(gp, (s0 + i) * gs);
-                    else
-                        x[i].x = load1<true>(gp, (s0 + i) * gs);
-                }
+        for (int u = 0; u < UB; ++u) {
+            const uint32_t e = e0 + V * ((u0 + u) * kNT + threadIdx.x);
+            in[u] = e < e1;
+            ge[u] = (int64_t)b * n + e;
+            const int64_t tile = ge[u] / kTile, pos = ge[u] % kTile;
+            gp[u] = TILED ? s.grads + tile * W * kTile + pos : s.grads + ge[u];
+            mp[u] = s.state + (tile * 3 + 1) * kTile + pos;
+            if (in[u]) {
+                if constexpr (VEC)
+                    mom[u] = __builtin_nontemporal_load(
+                        reinterpret_cast<const f32x4*>(mp[u]));
+                else
+                    mom[u].x = *mp[u];
+            }
+        }
+        for (int s0 = 0; s0 < W; s0 += NB) {
+            u32x2 x[UB][NB];
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (s0 + i < a.W) {
+            for (int u = 0; u < UB; ++u)
 #pragma unroll
-                    for (int k = 0; k < V; ++k)
-                        acc[k] = s0 + i == 0 ? x[i][k] : acc[k] + x[i][k];
-                }
+                for (int i = 0; i < NB; ++i)
+                    if (in[u] && (WT || s0 + i < W)) {
+                        const uint16_t* const g = gp[u] + (s0 + i) * gs;
+                        if constexpr (VEC)
+                            x[u][i] = __builtin_nontemporal_load(
+                                reinterpret_cast<const u32x2*>(g));
+                        else
+                            x[u][i].x = *g;
+                    }
+#pragma unroll
+            for (int u = 0; u < UB; ++u)
+#pragma unroll
+                for (int i = 0; i < NB; ++i)
+                    if (WT || s0 + i < W) {
+                        const f32x4 v = {
+                            bf16_to_f32(x[u][i].x),
+                            __uint_as_float(x[u][i].x & 0xffff0000u),
+                            bf16_to_f32(x[u][i].y),
+                            __uint_as_float(x[u][i].y & 0xffff0000u)};
+#pragma unroll
+                        for (int k = 0; k < V; ++k)
+                            acc[u][k] =
+                                s0 + i == 0 ? v[k] : acc[u][k] + v[k];
+                    }
         }
 #pragma unroll
-        for (int k = 0; k < V; ++k) {
-            const float g = a.pow2 ? acc[k] * a.invw : acc[k] / a.fw;
-            const float t = a.mu * mom[k];
-            mom[k] = t + g;
-            const float t2 = a.mu * mom[k];
-            up[k] = a.nesterov ? g + t2 : mom[k];
-            sum += (double)up[k] * up[k];
-        }
-        if constexpr (VEC) {
-            *reinterpret_cast<f32x4*>(mp) = mom;
-            *reinterpret_cast<f32x4*>(u + ge) = up;
-        } else {
-            *mp = mom.x;
-            u[ge] = up.x;
+        for (int u = 0; u < UB; ++u) {
+            if (!in[u])
+                continue;
+            f32x4 up;
+#pragma unroll
+            for (int k = 0; k < V; ++k) {
+                const float g =
+                    a.pow2 ? acc[u][k] * a.invw : acc[u][k] / a.fw;
+                const float t = a.mu * mom[u][k];
+                mom[u][k] = t + g;
+                const float t2 = a.mu * mom[u][k];
+                up[k] = a.nesterov ? g + t2 : mom[u][k];
+                sum += (double)up[k] * up[k];
+            }
+            if constexpr (VEC) {
+                __builtin_nontemporal_store(mom[u],
+                                            reinterpret_cast<f32x4*>(mp[u]));
+                *reinterpret_cast<f32x4*>(s.u + ge[u]) = up;
+            } else {
+                *mp[u] = mom[u].x;
+                s.u[ge[u]] = up.x;
+            }
         }
     }
     if (!s.parts)
@@ -344,16 +392,32 @@ __device__ __forceinline__ void momentum_part(const MomArgs& a, const Mat& m,
         s.parts[(int64_t)b * m.nparts + part] = sum;
 }
 
-template <bool TILED>
+template <int WT, bool TILED>
 __global__ __launch_bounds__(kNT) void muon_momentum_kernel(MomArgs a)
 {
     uint32_t bid = blockIdx.x;
     const int p = find(a.g, bid);
     const Mat& m = a.g.m[p];
     if (((uint32_t)m.R * m.C) % 4 == 0)
-        momentum_part<TILED, true>(a, m, a.src[p], bid);
+        momentum_part<WT, TILED, true>(a, m, a.src[p], bid);
     else
-        momentum_part<TILED, false>(a, m, a.src[p], bid);
+        momentum_part<WT, TILED, false>(a, m, a.src[p], bid);
+}
+
+// A matrix's many partial sums into the first of them: workgroup = one matrix.
+template <bool FULL>
+__global__ __launch_bounds__(kNT) void ns_sum_kernel(Group g)
+{
+    uint32_t b = blockIdx.x;
+    const Mat& m = g.m[find(g, b)];
+    double* const parts = Region<FULL>(m.ws, m.R, m.C, m.batch).parts() +
+                          (int64_t)b * m.nparts;
+    double sum = 0;
+    for (int i = threadIdx.x; i < m.nparts; i += kNT)
+        sum += parts[i];
+    sum = block_sum(sum);               // every thread has read its own
+    if (threadIdx.x == 0)
+        parts[0] = sum;
 }
 
 // ---- X = U / (|U| + eps) into the workspace ---------------------------------------
@@ -362,6 +426,7 @@ struct InitArgs {
     Group g;
     Source src[kMaxMats];
     float eps;
+    int32_t summed;                     // the first partial sum is the sum
 };
 
 __device__ __forceinline__ void split(float x, f16& hi, f16& lo)
@@ -387,7 +452,8 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
     // the matrix's sum of squares, every workgroup in the same order
     double sum = 0;
     const double* const parts = w.parts() + (int64_t)b * m.nparts;
-    for (int i = threadIdx.x; i < m.nparts; i += kNT)
+    const int nparts = a.summed ? 1 : m.nparts;
+    for (int i = threadIdx.x; i < nparts; i += kNT)
         sum += parts[i];
     sum = block_sum(sum);
     const double norm = sqrt(sum);
@@ -1445,8 +1511,6 @@ constexpr int64_t kMaxSide = 32768;             // of the smaller side
 constexpr int64_t kMaxLong = (int64_t)1 << 22;  // of the larger: a tile's rows
                                                 // span less than 4 GiB
 constexpr int64_t kMaxTiles = (int64_t)1 << 23; // 64 x 64 tiles of a call
-constexpr int32_t kMaxParts = 1024;             // partial sums per matrix
-constexpr int32_t kMinChunk = 2048;
 
 // One member's sizes, checked; tiles: 64 x 64 tiles of X or of A.
 int check_sizes(int32_t i, int64_t batch, int64_t rows, int64_t cols,
@@ -1468,7 +1532,7 @@ int check_sizes(int32_t i, int64_t batch, int64_t rows, int64_t cols,
                     (long long)rows, (long long)cols, (long long)kMaxSide,
                     (long long)kMaxLong);
     const int64_t per = ((rows + 63) / 64) * ((cols + 63) / 64);
-    const int64_t parts = rows * cols / kMinChunk + 1;
+    const int64_t parts = rows * cols / kMomChunk + 1;
     const int64_t most = per > parts ? per : parts;
     if (batch > kMaxTiles / most || (tiles += batch * most) > kMaxTiles)
         return fail(ZS_ERANGE, "more than %lld matrix tiles in one call",
@@ -1503,15 +1567,6 @@ int check_ns(const zs_newton_schulz* ns)
 bool aligned(const void* p, uintptr_t n)
 {
     return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
-}
-
-void set_parts(Mat& m)
-{
-    const int64_t n = (int64_t)m.R * m.C;
-    int64_t chunk = (n + kMaxParts - 1) / kMaxParts;
-    chunk = (chunk + 4 * kNT - 1) / (4 * kNT) * (4 * kNT);
-    m.chunk = (int32_t)(chunk < kMinChunk ? kMinChunk : chunk);
-    m.nparts = (int32_t)((n + m.chunk - 1) / m.chunk);
 }
 
 typedef Small<64, 64, 4, 2, 2> Small64;
@@ -1567,14 +1622,14 @@ void sort_members(int32_t* order, int32_t count, Sides sides)
 }
 
 // Appends a stack to the group, with its part of the workspace.
-void add_mat(Group& g, int64_t batch, int64_t rows, int64_t cols, bool full,
-             char* ws, int64_t& used)
+void add_mat(Group& g, int64_t batch, int64_t rows, int64_t cols, int chunk,
+             bool full, char* ws, int64_t& used)
 {
     Mat& m = g.m[g.count++];
     m.R = (int32_t)rows;
     m.C = (int32_t)cols;
     m.batch = (int32_t)batch;
-    set_parts(m);
+    m.nparts = (int32_t)((rows * cols + chunk - 1) / chunk);
     m.ws = ws + used;
     used += mat_bytes(m, full);
 }
@@ -1791,6 +1846,15 @@ int launch_init(const Group& g, const Source* src, float eps, hipStream_t s)
     for (int i = 0; i < g.count; ++i)
         a.src[i] = src[i];
     a.eps = eps;
+    a.summed = 0;
+    for (int i = 0; i < g.count; ++i)
+        a.summed |= g.m[i].nparts > kMaxParts;
+    if (a.summed) {
+        const uint32_t n = set_starts(a.g, [](const Mat&) { return 1; });
+        hipLaunchKernelGGL(ns_sum_kernel<FULL>, dim3(n), dim3(kNT), 0, s,
+                           a.g);
+        if (const int rc = check_launch("norm sums")) return rc;
+    }
     const uint32_t n = set_starts(a.g, init_tiles);
     hipLaunchKernelGGL((ns_init_kernel<BF16, FULL>), dim3(n), dim3(kNT), 0, s,
                        a);
@@ -1937,7 +2001,8 @@ extern "C" int zs_orthogonalize_workspace(int32_t count,
         const int rc = check_sizes(i, m.batch, m.rows, m.cols, tiles);
         if (rc) return rc;
         if (m.batch && m.rows && m.cols)
-            add_mat(g, m.batch, m.rows, m.cols, precision == ZS_NS_FULL,
+            add_mat(g, m.batch, m.rows, m.cols, kNormChunk,
+                    precision == ZS_NS_FULL,
                     nullptr, used);
     }
     *bytes = group_bytes(g, precision == ZS_NS_FULL);
@@ -2009,7 +2074,7 @@ extern "C" int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
         o.row = m.o_row_stride;
         o.vec = m.cols % 4 == 0 && o.row % 4 == 0 &&
                 (m.batch == 1 || o.batch % 4 == 0) && aligned(m.o, 4 * oe);
-        add_mat(g, m.batch, m.rows, m.cols, full,
+        add_mat(g, m.batch, m.rows, m.cols, kNormChunk, full,
                 static_cast<char*>(workspace), used);
     }
     if (g.count == 0) return ZS_OK;
@@ -2068,9 +2133,20 @@ int muon_group(const zs_layout* L, int32_t count, const zs_muon_tensor* t,
     });
     for (int32_t n = 0; n < count; ++n) {
         const zs_muon_tensor& m = t[order[n]];
-        add_mat(g, m.batch, m.rows, m.cols, full, ws, used);
+        add_mat(g, m.batch, m.rows, m.cols, kMomChunk, full, ws, used);
     }
     return ZS_OK;
+}
+
+template <int WT>
+void launch_momentum(const MomArgs& a, bool tiled, uint32_t n, hipStream_t s)
+{
+    if (tiled)
+        hipLaunchKernelGGL((muon_momentum_kernel<WT, true>), dim3(n),
+                           dim3(kNT), 0, s, a);
+    else
+        hipLaunchKernelGGL((muon_momentum_kernel<WT, false>), dim3(n),
+                           dim3(kNT), 0, s, a);
 }
 
 template <bool FULL>
@@ -2092,12 +2168,13 @@ int muon_step(const Group& g, MomArgs& ma, const StepMat* st, bool tiled,
     }
     const uint32_t n =
         set_starts(ma.g, [](const Mat& m) { return m.nparts; });
-    if (tiled)
-        hipLaunchKernelGGL(muon_momentum_kernel<true>, dim3(n), dim3(kNT), 0,
-                           s, ma);
-    else
-        hipLaunchKernelGGL(muon_momentum_kernel<false>, dim3(n), dim3(kNT),
-                           0, s, ma);
+    switch (ma.W) {
+    case 1: launch_momentum<1>(ma, tiled, n, s); break;
+    case 2: launch_momentum<2>(ma, tiled, n, s); break;
+    case 4: launch_momentum<4>(ma, tiled, n, s); break;
+    case 8: launch_momentum<8>(ma, tiled, n, s); break;
+    default: launch_momentum<0>(ma, tiled, n, s); break;
+    }
     if (const int rc = check_launch("momentum kernel")) return rc;
     const Work w = {&g, src, ZS_F32, kStep, nullptr, st,
                     (float)(1.0 - (double)hp.lr * (double)hp.weight_decay),

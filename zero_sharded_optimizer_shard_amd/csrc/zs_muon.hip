@@ -172,16 +172,17 @@ constexpr int32_t kMaxParts = 2048;     // more are summed by a launch of their
                                         // own
 
 // Sum over the workgroup in a fixed order; valid in thread 0.
+template <int NT = kNT>
 __device__ __forceinline__ double block_sum(double v)
 {
-    __shared__ double s[kNT / 64];
+    __shared__ double s[NT / 64];
     for (int d = 32; d; d >>= 1)
         v += __shfl_down(v, d, 64);
     if ((threadIdx.x & 63) == 0)
         s[threadIdx.x >> 6] = v;
     __syncthreads();
     double t = 0;
-    for (int w = 0; w < kNT / 64; ++w)
+    for (int w = 0; w < NT / 64; ++w)
         t += s[w];
     return t;
 }
@@ -405,17 +406,28 @@ __global__ __launch_bounds__(kNT) void muon_momentum_kernel(MomArgs a)
 }
 
 // A matrix's many partial sums into the first of them: workgroup = one matrix.
+constexpr int kSumNT = 1024;
+
 template <bool FULL>
-__global__ __launch_bounds__(kNT) void ns_sum_kernel(Group g)
+__global__ __launch_bounds__(kSumNT) void ns_sum_kernel(Group g)
 {
     uint32_t b = blockIdx.x;
     const Mat& m = g.m[find(g, b)];
     double* const parts = Region<FULL>(m.ws, m.R, m.C, m.batch).parts() +
                           (int64_t)b * m.nparts;
     double sum = 0;
-    for (int i = threadIdx.x; i < m.nparts; i += kNT)
-        sum += parts[i];
-    sum = block_sum(sum);               // every thread has read its own
+    for (int i = threadIdx.x; i < m.nparts; i += 8 * kSumNT) {
+        double x[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+            const int n = i + k * kSumNT;
+            x[k] = n < m.nparts ? parts[n] : 0;
+        }
+#pragma unroll
+        for (int k = 0; k < 8; ++k)
+            sum += x[k];
+    }
+    sum = block_sum<kSumNT>(sum);       // every thread has read its own
     if (threadIdx.x == 0)
         parts[0] = sum;
 }
@@ -1725,25 +1737,30 @@ double estimate(const Group& g, double stage, double alone, double fixed,
 }
 
 // The tile for a product on these stacks, by estimated time.
+struct Choice {
+    int tile;                           // 65: the 64 tile with a deep ring
+    double us;
+};
+
 template <int EPI, bool FULL>
-int choose_tile(const Group& g)
+Choice choose_tile(const Group& g)
 {
     int64_t n = 0;
     for (int p = 0; p < g.count; ++p)
         n += (int64_t)g.m[p].batch * d_tiles<64, EPI>(g.m[p]);
-    const double c = FULL ? 2.6 : 1;            // three products for one
-    double best = estimate<64, EPI>(g, 0.36 * c, 0.25 * c, 3, 2);
-    int tile = n <= 256 ? 65 : 64;              // 65: eight stages in LDS
+    const double c = FULL ? 2.7 : 1;    // three products for one
+    // beside the products: a launch, the first loads, and the epilogue, which
+    // moves ten bytes an element in an update and four in a square
+    const bool sq = symmetric(EPI);
+    Choice best = {n <= 256 ? 65 : 64,
+                   estimate<64, EPI>(g, 0.36 * c, 0.18 * c, sq ? 5 : 7, 2)};
     auto offer = [&](int t, double us) {
-        if (us < best) {
-            best = us;
-            tile = t;
-        }
+        if (us < best.us) best = {t, us};
     };
-    offer(128, estimate<128, EPI>(g, 0.98 * c, 0.6 * c, 6, 2));
-    offer(192, estimate<192, EPI>(g, 1.12 * c, 0.95 * c, 8, 1));
-    offer(256, estimate<256, EPI>(g, 1.5 * c, 1.4 * c, 12, 1));
-    return tile;
+    offer(128, estimate<128, EPI>(g, 0.98 * c, 0.6 * c, sq ? 7 : 13, 2));
+    offer(192, estimate<192, EPI>(g, 1.12 * c, 0.95 * c, sq ? 9 : 20, 1));
+    offer(256, estimate<256, EPI>(g, 1.5 * c, 1.4 * c, sq ? 10 : 22, 1));
+    return best;
 }
 
 template <int EPI, bool FULL>
@@ -1758,8 +1775,8 @@ int launch_product(GemmArgs& a, int tile, hipStream_t s)
     }
 }
 
-// Whether two steps taken on the m x m side cost less than one by one.  In
-// units of m^3 flops with r = n/m, a symmetric product being 1:
+// Two steps taken together on the m x m side.  In units of m^3 flops with
+// r = n/m, a symmetric product being 1:
 //   one by one   A = X X^T (r), C = a + b A + c A A (1), X <- C X (2 r),
 //                twice: 6 r + 2
 //   together     A (r), C (1), T = C A (1), A' = T C (1), C' from A' (1),
@@ -1769,18 +1786,28 @@ int launch_product(GemmArgs& a, int tile, hipStream_t s)
 // but only into C', where they count for a^2 b 2^-12; X itself stays exact.  A
 // third step in the same way would multiply that by a^2 = 12 again (a matrix
 // of 1024 x 3584 with singular values 1/k: 2.2e-4 one by one, 1e-3 in twos,
-// 5e-3 in threes), so it is at most two.
-bool in_pairs(const Group& g)
+// 5e-3 in threes), so it is at most two.  An odd number of steps: the second
+// turn is the single one.
+//
+// Whether step k goes together with the next, where twos are taken at all.  E
+// is about a a' where A is small and has to stay in fp16's range.
+bool together(const zs_newton_schulz& ns, int k)
 {
-    double pairs = 0, singles = 0;
-    for (int p = 0; p < g.count; ++p) {
-        const Mat& m = g.m[p];
-        const double rp = padded(m.R), cp = padded(m.C);
-        const double s = rp < cp ? rp : cp, r = (rp < cp ? cp : rp) / s;
-        pairs += m.batch * s * s * s * (3 * r + 5);
-        singles += m.batch * s * s * s * (6 * r + 2);
+    return k + 1 < ns.steps && !(ns.steps % 2 && k == 2) &&
+           std::fabs(ns.coef[k][0] * ns.coef[k + 1][0]) < 24;
+}
+
+// Whether twos take less time, by the estimates of the launches.
+bool in_pairs(const zs_newton_schulz& ns, double gram, double square,
+              double update)
+{
+    double pairs = 0;
+    for (int k = 0; k < ns.steps;) {
+        const bool two = together(ns, k);
+        pairs += gram + (two ? 5.2 : 1) * square + update;
+        k += two ? 2 : 1;
     }
-    return pairs < 0.8 * singles;
+    return pairs < 0.97 * ns.steps * (gram + square + update);
 }
 
 // The steps on a group whose X[0] is in the workspace; LAST: the epilogue of
@@ -1788,10 +1815,10 @@ bool in_pairs(const Group& g)
 template <int LAST, bool FULL>
 int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
 {
-    const bool pairs = in_pairs(a.g);
-    const int tGram = choose_tile<kGram, FULL>(a.g),
-              tPoly = choose_tile<kPoly, FULL>(a.g),
-              tUpdate = choose_tile<kUpdate, FULL>(a.g);
+    const Choice gram = choose_tile<kGram, FULL>(a.g),
+                 square = choose_tile<kPoly, FULL>(a.g),
+                 update = choose_tile<kUpdate, FULL>(a.g);
+    const bool pairs = in_pairs(ns, gram.us, square.us, update.us);
     a.parity = 0;
     int rc = ZS_OK;
     auto poly = [&](int k, Square out) {
@@ -1800,22 +1827,18 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         a.c = ns.coef[k][2];
         a.sp = a.sq = kA;
         a.so = out;
-        if (!rc) rc = launch_product<kPoly, FULL>(a, tPoly, s);
+        if (!rc) rc = launch_product<kPoly, FULL>(a, square.tile, s);
     };
     auto prod = [&](Square p, Square q, Square out) {
         a.sp = p;
         a.sq = q;
         a.so = out;
-        if (!rc) rc = launch_product<kProd, FULL>(a, tPoly, s);
+        if (!rc) rc = launch_product<kProd, FULL>(a, square.tile, s);
     };
     for (int k = 0; k < ns.steps && !rc;) {
-        // an odd number of steps: the second by itself, or the only one.  E
-        // is about a a' where A is small and has to stay in fp16's range.
-        const bool two = pairs && k + 1 < ns.steps &&
-                         !(ns.steps % 2 && k == 2) &&
-                         std::fabs(ns.coef[k][0] * ns.coef[k + 1][0]) < 24;
+        const bool two = pairs && together(ns, k);
         a.so = kA;
-        rc = launch_product<kGram, FULL>(a, tGram, s);
+        rc = launch_product<kGram, FULL>(a, gram.tile, s);
         poly(k, kC);
         if (two) {
             prod(kC, kA, kT);
@@ -1826,8 +1849,8 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         k += two ? 2 : 1;
         a.sp = two ? kT : kC;
         if (!rc)
-            rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, tUpdate, s)
-                              : launch_product<LAST, FULL>(a, tUpdate, s);
+            rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, update.tile, s)
+                              : launch_product<LAST, FULL>(a, update.tile, s);
         a.parity ^= 1;
     }
     return rc;
@@ -1851,7 +1874,7 @@ int launch_init(const Group& g, const Source* src, float eps, hipStream_t s)
         a.summed |= g.m[i].nparts > kMaxParts;
     if (a.summed) {
         const uint32_t n = set_starts(a.g, [](const Mat&) { return 1; });
-        hipLaunchKernelGGL(ns_sum_kernel<FULL>, dim3(n), dim3(kNT), 0, s,
+        hipLaunchKernelGGL(ns_sum_kernel<FULL>, dim3(n), dim3(kSumNT), 0, s,
                            a.g);
         if (const int rc = check_launch("norm sums")) return rc;
     }

@@ -582,10 +582,9 @@ struct Shape {
 typedef Shape<256, 2, 4, 2> Shape256;
 typedef Shape<192, 2, 4, 2> Shape192;
 typedef Shape<128, 2, 4, 2> Shape128;
-// Small matrices are bound by the latency of a stage: four in LDS, or eight
-// where there is a CU for every tile.
+// Small matrices are bound by the latency of a launch and of a stage: four
+// stages in LDS (eight in a longer loop cost 3 to 7 % more a call).
 typedef Shape<64, 2, 2, 4> Shape64;
-typedef Shape<64, 2, 2, 8> Shape64Deep;
 
 // s_waitcnt immediate: at most vm vector loads and lg LDS operations out.
 constexpr int wait_count(int vm, int lg)
@@ -753,10 +752,6 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     __shared__ __align__(1024) char lds1[2 * SH::kHalf];
     __shared__ __align__(1024) char lds2[ST > 2 ? 2 * SH::kHalf : 16];
     __shared__ __align__(1024) char lds3[ST > 2 ? 2 * SH::kHalf : 16];
-    __shared__ __align__(1024) char lds4[ST > 4 ? 2 * SH::kHalf : 16];
-    __shared__ __align__(1024) char lds5[ST > 4 ? 2 * SH::kHalf : 16];
-    __shared__ __align__(1024) char lds6[ST > 4 ? 2 * SH::kHalf : 16];
-    __shared__ __align__(1024) char lds7[ST > 4 ? 2 * SH::kHalf : 16];
     __shared__ __align__(16) float diag[2][BT];        // of the epilogue's squares
 
     uint32_t bid = blockIdx.x;
@@ -1029,9 +1024,8 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         // k + 1 is whole when at most the loads of the ST - 2 younger ones
         // are out, and this wave's reads of stage k have returned; after the
         // barrier that holds for every wave, and stage k's place is free.
-        static_assert(SH::kTurns || ST == 4 || ST == 8, "stages");
-        char* const bufs[8] = {lds0, lds1, lds2, lds3,
-                               lds4, lds5, lds6, lds7};
+        static_assert(SH::kTurns || ST == 4, "stages");
+        char* const bufs[4] = {lds0, lds1, lds2, lds3};
         f16x8 fx[2][2][FI], fy[2][2][FJ];       // [set][half]
         auto readAll = [&](const char* lds, int set) {
 #pragma unroll
@@ -1077,17 +1071,20 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
             for (int k = 0; k < ST; ++k) {
                 if (kt + k >= total)
                     break;
+                // (apart from the loads', so that every path has it)
+                __builtin_amdgcn_s_waitcnt(wait_count(63, 0));
                 if (kt + k + ST - 1 < total)
-                    __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 0));
+                    __builtin_amdgcn_s_waitcnt(wait_count((ST - 2) * NL, 15));
                 else
-                    __builtin_amdgcn_s_waitcnt(wait_count(0, 0));
+                    __builtin_amdgcn_s_waitcnt(wait_count(0, 15));
                 slot_barrier();
                 if (kt + k + ST < total)
                     load(bufs[k]);
-                if (kt + k + 1 < total)
-                    readAll(bufs[(k + 1) % ST], (k + 1) % 2);
+                // past the last stage: what lies there, for nobody
+                readAll(bufs[(k + 1) % ST], (k + 1) % 2);
                 __builtin_amdgcn_sched_barrier(0);
                 mulAll(k % 2);
+                __builtin_amdgcn_sched_barrier(0);
             }
         }
     }
@@ -1738,21 +1735,18 @@ double estimate(const Group& g, double stage, double alone, double fixed,
 
 // The tile for a product on these stacks, by estimated time.
 struct Choice {
-    int tile;                           // 65: the 64 tile with a deep ring
+    int tile;
     double us;
 };
 
 template <int EPI, bool FULL>
 Choice choose_tile(const Group& g)
 {
-    int64_t n = 0;
-    for (int p = 0; p < g.count; ++p)
-        n += (int64_t)g.m[p].batch * d_tiles<64, EPI>(g.m[p]);
     const double c = FULL ? 2.7 : 1;    // three products for one
     // beside the products: a launch, the first loads, and the epilogue, which
     // moves ten bytes an element in an update and four in a square
     const bool sq = symmetric(EPI);
-    Choice best = {n <= 256 ? 65 : 64,
+    Choice best = {64,
                    estimate<64, EPI>(g, 0.36 * c, 0.18 * c, sq ? 5 : 7, 2)};
     auto offer = [&](int t, double us) {
         if (us < best.us) best = {t, us};
@@ -1768,7 +1762,6 @@ int launch_product(GemmArgs& a, int tile, hipStream_t s)
 {
     switch (tile) {
     case 64: return launch_gemm<Shape64, EPI, FULL>(a, s);
-    case 65: return launch_gemm<Shape64Deep, EPI, FULL>(a, s);
     case 128: return launch_gemm<Shape128, EPI, FULL>(a, s);
     case 192: return launch_gemm<Shape192, EPI, FULL>(a, s);
     default: return launch_gemm<Shape256, EPI, FULL>(a, s);

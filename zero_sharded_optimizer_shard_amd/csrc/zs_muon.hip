@@ -1744,16 +1744,19 @@ Choice choose_tile(const Group& g)
 {
     const double c = FULL ? 2.7 : 1;    // three products for one
     // beside the products: a launch, the first loads, and the epilogue, which
-    // moves ten bytes an element in an update and four in a square
-    const bool sq = symmetric(EPI);
+    // moves four bytes an element in a square, ten in an update, and in the
+    // step fourteen to sixteen with the tiles of a round all at once
+    const int k = symmetric(EPI) ? 0 : EPI == kStep ? 2 : 1;
+    constexpr double fixed[3][4] = {
+        {5, 7, 9, 10}, {7, 13, 20, 22}, {8, 20, 35, 55}};
     Choice best = {64,
-                   estimate<64, EPI>(g, 0.36 * c, 0.18 * c, sq ? 5 : 7, 2)};
+                   estimate<64, EPI>(g, 0.36 * c, 0.18 * c, fixed[k][0], 2)};
     auto offer = [&](int t, double us) {
         if (us < best.us) best = {t, us};
     };
-    offer(128, estimate<128, EPI>(g, 0.98 * c, 0.6 * c, sq ? 7 : 13, 2));
-    offer(192, estimate<192, EPI>(g, 1.12 * c, 0.95 * c, sq ? 9 : 20, 1));
-    offer(256, estimate<256, EPI>(g, 1.5 * c, 1.4 * c, sq ? 10 : 22, 1));
+    offer(128, estimate<128, EPI>(g, 0.98 * c, 0.6 * c, fixed[k][1], 2));
+    offer(192, estimate<192, EPI>(g, 1.12 * c, 0.95 * c, fixed[k][2], 1));
+    offer(256, estimate<256, EPI>(g, 1.5 * c, 1.4 * c, fixed[k][3], 1));
     return best;
 }
 
@@ -1810,7 +1813,8 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
 {
     const Choice gram = choose_tile<kGram, FULL>(a.g),
                  square = choose_tile<kPoly, FULL>(a.g),
-                 update = choose_tile<kUpdate, FULL>(a.g);
+                 update = choose_tile<kUpdate, FULL>(a.g),
+                 last = choose_tile<LAST, FULL>(a.g);
     const bool pairs = in_pairs(ns, gram.us, square.us, update.us);
     a.parity = 0;
     int rc = ZS_OK;
@@ -1843,7 +1847,7 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         a.sp = two ? kT : kC;
         if (!rc)
             rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, update.tile, s)
-                              : launch_product<LAST, FULL>(a, update.tile, s);
+                              : launch_product<LAST, FULL>(a, last.tile, s);
         a.parity ^= 1;
     }
     return rc;

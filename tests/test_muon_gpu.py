@@ -91,7 +91,8 @@ def check(U, O, precision="fast", steps=5, coef=OM.COEF, eps=1e-7):
 SHAPES = [(1, 1), (1, 7), (7, 1), (3, 5), (64, 64), (63, 65), (65, 63),
           (64, 128), (127, 129), (128, 128), (129, 257), (257, 129),
           (192, 448), (300, 1000), (1000, 300), (1, 4099), (4099, 1),
-          (515, 513), (768, 320)]
+          (515, 513), (768, 320), (50, 500), (500, 50), (100, 128),
+          (128, 97), (33, 250), (250, 33)]
 
 
 @pytest.mark.parametrize("precision", ["fast", "full"])
@@ -260,6 +261,37 @@ def test_same_bits_every_time():
     a = run([x], [torch.empty_like(x)], poison=False)[0]
     for k in range(3):
         assert torch.equal(run([x], [torch.empty_like(x)])[0], a)
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each: the results of one after the other."""
+    xs = [torch.from_numpy(matrix(gen(40 + k), 900, 1100)).cuda()
+          for k in range(2)]
+    want = [run([x], [torch.empty_like(x)])[0] for x in xs]
+    ws = [torch.empty(zs.zs_orthogonalize_workspace([x]), dtype=torch.uint8,
+                      device="cuda") for x in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for x, o, w, st in zip(xs, outs, ws, streams):
+            zs.zs_orthogonalize([x], [o], workspace=w, stream=st)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+def test_stack_of_many_small_matrices():
+    """More workgroups than the chip holds, of every small kind."""
+    for shape in ((700, 40, 60), (400, 64, 256), (300, 300, 64),
+                  (300, 128, 120)):
+        x = torch.randn(shape, device="cuda",
+                        generator=torch.Generator("cuda").manual_seed(1))
+        o = run([x], [torch.empty_like(x)])[0]
+        for k in (0, 1, shape[0] // 2, shape[0] - 1):
+            check(x[k].cpu().numpy(), o[k])
+        one = run([x[5]], [torch.empty_like(x[5])])[0]
+        assert torch.equal(one, o[5])
 
 
 def test_another_stream_and_a_captured_graph():
@@ -441,6 +473,17 @@ def test_step(shapes, W, layout):
     scale = {1: "none", 2: "shape"}.get(W, "rms")
     c.step(d, nesterov=nesterov, scale=scale)
     c.check(d, nesterov=nesterov, scale=scale)
+
+
+@pytest.mark.parametrize("shapes", [[(2111, 2052)], [(1501, 1503)],
+                                    [(9, 640, 700), (64, 64)]], ids=str)
+def test_step_of_large_matrices(shapes):
+    """Large tiles, and more partial sums of squares than a workgroup adds on
+    its way."""
+    c = Case(shapes, 2, "tiled", seed=35)
+    d = c.device()
+    c.step(d, steps=2)
+    c.check(d, steps=2)
 
 
 @pytest.mark.parametrize("precision", ["fast", "full"])

@@ -3,9 +3,9 @@
 //
 // With X = U / (|U|_F + eps) and m <= n its sides, one step is
 //   gram     A = X X^T            symmetric: one triangle of tiles, m^2 n flops
-//   poly     B = b A + c A A      symmetric: one triangle of tiles, m^3
-//   update   X <- a X + B X       2 m^2 n
-// (X^T X and X B for a matrix with more rows than columns), on the matrix
+//   poly     C = a + b A + c A A  symmetric: one triangle of tiles, m^3
+//   update   X <- C X             2 m^2 n
+// (X^T X and X C for a matrix with more rows than columns), on the matrix
 // cores: D[i][j] = sum_k P[i][k] Q[j][k] with both operands contiguous along
 // k.  gram multiplies the rows of X's shorter side, update needs the rows of
 // its longer side, so X is kept in both orientations: Xd [rows][cols] as the
@@ -17,13 +17,22 @@
 // is not:
 //  - X is a pair (hi, lo), 22 bits; products use hi, the term a X uses both.
 //    Rounded to fp16 alone, the rounding of each step would enter the null
-//    directions of a matrix of low rank and grow by a = 3.4 a step.
-//  - The diagonals of A and B are fp32 vectors, and zero in the fp16
+//    directions of a matrix of low rank and grow by a = 3.4 a step (rank 8 of
+//    1024: 4e-2 of the result's norm against 3e-4).
+//  - The diagonals of A and C are fp32 vectors, and zero in the fp16
 //    matrices: near the end A is close to the identity, and the rounding of
 //    its diagonal would be most of the error.  (R + D)(R + D) = R R + D R +
 //    R D + D D, the last three element by element.
-//  - In full precision (FULL) A, B and X^T are pairs too and every product
-//    is three: hi hi + hi lo + lo hi.
+//  - In full precision (FULL) the squares and X^T are pairs too and every
+//    product is three: hi hi + hi lo + lo hi.
+//
+// Launches: the norm (or the momentum, which leaves U and its norm), X_0, and
+// three products a step, for all matrices of a call at once; small matrices
+// take all steps in one launch.  What bounds them on MI355X: from 4096 a side
+// on the matrix cores, which are busy 57-65 % of the cycles of a square's
+// launch and 50 % of an update's, whose epilogue moves ten bytes an element
+// with nothing beside it; up to about 1024 a side the launches themselves,
+// each 5-7 us plus 0.18 us for 64 k (0.5 us in full precision).
 //
 // Padding.  Every matrix is stored with its sides rounded up to 64 and zeros
 // behind, which the products preserve, so the k loop has no edge; rows past
@@ -35,14 +44,12 @@
 #include <cmath>
 #include <cstdint>
 
-#include "zs_device.h"
 #include "zs_internal.h"
 #include "zs_muon.h"
 
 namespace {
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
-typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef _Float16 f16;
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
@@ -162,7 +169,7 @@ __device__ __forceinline__ uint32_t to_bf16(float f)
     return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
 }
 
-// ---- sums of squares ---------------------------------------------------------
+// ---- sums of squares -------------------------------------------------------
 
 constexpr int kNT = 256;                // threads of the elementwise kernels
 // Elements behind one partial sum: a workgroup takes them at once, all loads
@@ -171,7 +178,7 @@ constexpr int kNormChunk = 8192, kMomChunk = 2048;
 constexpr int32_t kMaxParts = 2048;     // more are summed by a launch of their
                                         // own
 
-// Sum over the workgroup in a fixed order; valid in thread 0.
+// Sum over the workgroup in a fixed order, for every thread.
 template <int NT = kNT>
 __device__ __forceinline__ double block_sum(double v)
 {
@@ -271,7 +278,7 @@ __global__ __launch_bounds__(kNT) void ns_norm_kernel(NormArgs a)
             .parts()[(int64_t)b * m.nparts + part] = sum;
 }
 
-// ---- the step's momentum --------------------------------------------------------
+// ---- the step's momentum ---------------------------------------------------
 
 struct MomSrc {
     const uint16_t* grads;
@@ -432,7 +439,7 @@ __global__ __launch_bounds__(kSumNT) void ns_sum_kernel(Group g)
         parts[0] = sum;
 }
 
-// ---- X = U / (|U| + eps) into the workspace ---------------------------------------
+// ---- X = U / (|U| + eps) into the workspace --------------------------------
 
 struct InitArgs {
     Group g;
@@ -517,7 +524,7 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
     }
 }
 
-// ---- the products ------------------------------------------------------------------
+// ---- the products ----------------------------------------------------------
 
 // What a product's epilogue makes of D, and which operands it has:
 //   kGram     A = X X^T
@@ -752,7 +759,8 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     __shared__ __align__(1024) char lds1[2 * SH::kHalf];
     __shared__ __align__(1024) char lds2[ST > 2 ? 2 * SH::kHalf : 16];
     __shared__ __align__(1024) char lds3[ST > 2 ? 2 * SH::kHalf : 16];
-    __shared__ __align__(16) float diag[2][BT];        // of the epilogue's squares
+    // the diagonals of the epilogue's squares along i and j
+    __shared__ __align__(16) float diag[2][BT];
 
     uint32_t bid = blockIdx.x;
     const int p = find(a.g, bid);
@@ -830,9 +838,12 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     // A stage's row is 128 bytes, in 16-byte pieces: 64 k, or in full
     // precision 32 k, their high parts and then their low ones.  Piece c of a
     // row is stored at c ^ sw(row), with sw(row) spreading the 16 rows that a
-    // fragment reads at one k over all eight places.  A load instruction
-    // fills 1 KiB of LDS in lane order, 8 rows, so the lane fetches the piece
-    // that belongs at its place.
+    // fragment reads at one k over all eight places.  (Q's rows of one read
+    // are then all even or all odd where FJ is 2 or 4, and use half of the
+    // banks: a quarter of the LDS cycles, measured to cost no time, since the
+    // products take three times as many.)  A load instruction fills 1 KiB of
+    // LDS in lane order, 8 rows, so the lane fetches the piece that belongs at
+    // its place.
     const bool isP = wave < SH::kWaves / 2;
     const char* const base = reinterpret_cast<const char*>(
         isP ? P + (int64_t)i0 * nk : Q + (int64_t)j0 * nk);
@@ -1213,16 +1224,17 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     }
 }
 
-// ---- small matrices, whole in one workgroup ---------------------------------------
+// ---- small matrices, whole in one workgroup --------------------------------
 
 // A matrix whose shorter side is at most TM and whose longer one at most TN
 // stays in one CU for all steps: one launch instead of three a step, each of
-// which would cost its latency and little else (64 x 64, five steps: SMALL_A us
-// against SMALL_B us).  Below, X is m x n with m the shorter side, transposed on
-// the way in and out where the matrix is tall.  X itself is held by the
+// which would cost its latency and little else (64 x 64, five steps: 16 us a
+// call against 72 us).  Below, X is m x n with m the shorter side, transposed
+// on the way in and out where the matrix is tall.  X itself is held by the
 // threads in fp32, laid out as the update's sums; LDS holds the operands of
 // the products: X by rows and by columns and the square A, then C.  The
-// arithmetic is the large kernels', with X kept in fp32.
+// arithmetic is the large kernels', with X kept in fp32.  A step is three
+// products of 64 or 128 k and five barriers, bound by their latency.
 template <int TM_, int TN_, int NW_, int GI_, int UI_>
 struct Small {
     static constexpr int TM = TM_, TN = TN_, NW = NW_;
@@ -1506,7 +1518,7 @@ __global__ __launch_bounds__(SM::kThreads) void ns_small_kernel(SmallArgs a)
             }
 }
 
-// ---- host ---------------------------------------------------------------------------
+// ---- host ------------------------------------------------------------------
 
 int check_launch(const char* what)
 {

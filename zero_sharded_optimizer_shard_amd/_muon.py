@@ -85,29 +85,37 @@ def _precision(precision) -> int:
         else int(precision)
 
 
+_Coef = ctypes.c_float * 3
+
+
 def _newton_schulz(steps: int, coef, eps: float, precision):
     """coef: one (a, b, c) for every step, or one per step."""
     ns = zs_newton_schulz(steps, _precision(precision), eps)
-    rows = [coef] * steps if not isinstance(coef[0], (tuple, list)) \
-        else list(coef)
+    if isinstance(coef[0], (tuple, list)):
+        rows = [_Coef(*row) for row in coef]
+    else:
+        rows = [_Coef(*coef)] * steps
     if len(rows) != steps:
         raise ValueError(f"coef: {len(rows)} rows for {steps} steps")
     for k, row in enumerate(rows[:ZS_NS_MAX_STEPS]):
-        ns.coef[k] = (ctypes.c_float * 3)(*row)
+        ns.coef[k] = row
     return ns
 
 
 def _device(*tensors):
     """The library works on the current device: refuse tensors of another."""
     import torch
+    current = None
     for t in tensors:
         if t is None:
             continue
         if not t.is_cuda:
             raise ValueError("expected a device tensor")
-        if t.device.index != torch.cuda.current_device():
+        if current is None:
+            current = torch.cuda.current_device()
+        if t.device.index != current:
             raise ValueError(f"tensor on {t.device}, the current device is "
-                             f"cuda:{torch.cuda.current_device()}")
+                             f"cuda:{current}")
 
 
 def _on_stream(stream):

@@ -253,7 +253,7 @@ def test_binding_refuses_before_the_library():
                         weight_decay=0., **kw)
 
 
-# ---- the oracle ------------------------------------------------------------------
+# ---- the oracle -------------------------------------------------------------
 
 @pytest.mark.parametrize("shape", [(20, 33), (33, 20), (24, 24), (1, 9)])
 def test_oracle_maps_singular_values(shape):

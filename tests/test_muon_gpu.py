@@ -321,7 +321,7 @@ def test_another_stream_and_a_captured_graph():
             assert torch.equal(o, want)
 
 
-# ---- the step ------------------------------------------------------------------
+# ---- the step ---------------------------------------------------------------
 
 LR, MU, WD = 3e-4, 0.95, 0.1
 TILE = zs.ZS_TILE

@@ -29,10 +29,11 @@
 // Launches: the norm (or the momentum, which leaves U and its norm), X_0, and
 // three products a step, for all matrices of a call at once; small matrices
 // take all steps in one launch.  What bounds them on MI355X: from 4096 a side
-// on the matrix cores, which are busy 57-65 % of the cycles of a square's
-// launch and 50 % of an update's, whose epilogue moves ten bytes an element
-// with nothing beside it; up to about 1024 a side the launches themselves,
-// each 5-7 us plus 0.18 us for 64 k (0.5 us in full precision).
+// on the matrix cores, which are busy 52-64 % of the cycles of a square's
+// launch and 42-57 % of an update's, whose epilogue moves ten bytes an element
+// (more with the master) with nothing beside it; up to about 1024 a side the
+// launches themselves, each 5-7 us plus 0.18 us for 64 k (0.5 us in full
+// precision).
 //
 // Padding.  Every matrix is stored with its sides rounded up to 64 and zeros
 // behind, which the products preserve, so the k loop has no edge; rows past

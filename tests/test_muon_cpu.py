@@ -253,6 +253,14 @@ def test_binding_refuses_before_the_library():
                         weight_decay=0., **kw)
 
 
+@pytest.mark.parametrize("coef", [(), (3.4, -4.8), (1., 2., 3., 4.),
+                                  [(1., 2., 3.), (1., 2.)]],
+                         ids=["none", "two", "four", "short row"])
+def test_binding_refuses_coefficients(coef):
+    with pytest.raises(ValueError):
+        zm._newton_schulz(2, coef, 1e-7, "fast")
+
+
 # ---- the oracle -------------------------------------------------------------
 
 @pytest.mark.parametrize("shape", [(20, 33), (33, 20), (24, 24), (1, 9)])

@@ -91,12 +91,14 @@ _Coef = ctypes.c_float * 3
 def _newton_schulz(steps: int, coef, eps: float, precision):
     """coef: one (a, b, c) for every step, or one per step."""
     ns = zs_newton_schulz(steps, _precision(precision), eps)
-    if isinstance(coef[0], (tuple, list)):
-        rows = [_Coef(*row) for row in coef]
-    else:
-        rows = [_Coef(*coef)] * steps
-    if len(rows) != steps:
-        raise ValueError(f"coef: {len(rows)} rows for {steps} steps")
+    per_step = len(coef) > 0 and isinstance(coef[0], (tuple, list))
+    for row in coef if per_step else [coef]:
+        if len(row) != 3:
+            raise ValueError(f"coef: {len(row)} coefficients, not 3")
+    if per_step and len(coef) != steps:
+        raise ValueError(f"coef: {len(coef)} rows for {steps} steps")
+    rows = [_Coef(*row) for row in coef] if per_step \
+        else [_Coef(*coef)] * steps
     for k, row in enumerate(rows[:ZS_NS_MAX_STEPS]):
         ns.coef[k] = row
     return ns

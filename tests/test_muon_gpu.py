@@ -228,6 +228,43 @@ def test_group_of_shapes_equals_single_calls():
     assert run(xs[4:6], [torch.empty_like(x) for x in xs[4:6]]) is not None
 
 
+def strong(rng, r, c):
+    """One direction six times as strong as the others."""
+    u, v = rng.standard_normal((r, 1)), rng.standard_normal((1, c))
+    w = rng.standard_normal((r, c)) / max(r, c) ** 0.5
+    return (6 * (u / np.linalg.norm(u)) @ (v / np.linalg.norm(v)) + w).astype(
+        np.float32)
+
+
+def check_singly(U, O):
+    """As exact as steps one by one: of few rows, twos are ten times less."""
+    exact = OM.orthogonalize(U)
+    t = 2 * rel(OM.rounded(U, pairs=False), exact) + 2.0 ** -18
+    got = rel(O.cpu().numpy(), exact)
+    assert got <= t, (got, t)
+
+
+THIN = [(8, 6000), (6000, 3), (16, 9000), (2, 7001)]
+
+
+@pytest.mark.parametrize("shape", THIN, ids=lambda s: "%dx%d" % s)
+def test_few_rows(shape):
+    U = strong(gen(sum(shape)), *shape)
+    x = torch.from_numpy(U).cuda()
+    check_singly(U, run([x], [torch.empty_like(x)])[0])
+
+
+def test_few_rows_beside_others():
+    rng = gen(12)
+    us = [strong(rng, *s) for s in THIN[:2] + [(256, 8000), (1, 9000)]]
+    xs = [torch.from_numpy(u).cuda() for u in us]
+    a = run(xs, [torch.empty_like(x) for x in xs])
+    for u, o in zip(us[:2], a):
+        check_singly(u, o)
+    for u, o in zip(us, a):
+        check(u, o)
+
+
 @pytest.mark.parametrize("shape", [(48, 80), (140, 150)],
                          ids=lambda s: "%dx%d" % s)
 @pytest.mark.parametrize("precision", ["fast", "full"])
@@ -484,6 +521,13 @@ def test_step_of_large_matrices(shapes):
     d = c.device()
     c.step(d, steps=2)
     c.check(d, steps=2)
+
+
+def test_step_of_few_rows_beside_others():
+    c = Case([(5, 6000), (256, 8000), (9001, 2)], 2, "tiled", seed=36)
+    d = c.device()
+    c.step(d)
+    c.check(d)
 
 
 @pytest.mark.parametrize("precision", ["fast", "full"])

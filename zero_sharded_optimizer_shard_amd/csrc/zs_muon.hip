@@ -1825,16 +1825,24 @@ bool in_pairs(const zs_newton_schulz& ns, double gram, double square,
     return pairs < 0.97 * ns.steps * (gram + square + update);
 }
 
-// The steps on a group whose X[0] is in the workspace; LAST: the epilogue of
-// the last update.
+// The tiles of a group's products; LAST: the epilogue of the last update.
+struct Tiles {
+    Choice gram, square, update, last;
+};
+
 template <int LAST, bool FULL>
-int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
+Tiles choose_tiles(const Group& g)
 {
-    const Choice gram = choose_tile<kGram, FULL>(a.g),
-                 square = choose_tile<kPoly, FULL>(a.g),
-                 update = choose_tile<kUpdate, FULL>(a.g),
-                 last = choose_tile<LAST, FULL>(a.g);
-    const bool pairs = in_pairs(ns, gram.us, square.us, update.us);
+    return {choose_tile<kGram, FULL>(g), choose_tile<kPoly, FULL>(g),
+            choose_tile<kUpdate, FULL>(g), choose_tile<LAST, FULL>(g)};
+}
+
+template <int LAST, bool FULL>
+int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Tiles& t,
+                 bool pairs, hipStream_t s)
+{
+    const Choice &gram = t.gram, &square = t.square, &update = t.update,
+                 &last = t.last;
     a.parity = 0;
     int rc = ZS_OK;
     auto poly = [&](int k, Square out) {
@@ -1870,6 +1878,51 @@ int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
         a.parity ^= 1;
     }
     return rc;
+}
+
+// In fast precision twos are not for matrices of few rows: a strong
+// direction's part of A off the diagonal is then spread over few elements,
+// and its rounding does not average out (roundings modelled in 64 bits, one
+// direction six times the others:
+// 8 x 1200 5.8e-4 one by one and 8.7e-3 in twos, 32 x 1200 2.3e-4 and 5.9e-4,
+// 64 x 1200 2.3e-4 and 3.6e-4).  A single row has nothing off the diagonal.
+bool thin(const Mat& m)
+{
+    const int32_t side = m.R < m.C ? m.R : m.C;
+    return side > 1 && side < 64;
+}
+
+// The steps on a group whose X[0] is in the workspace.
+template <int LAST, bool FULL>
+int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
+{
+    const Tiles t = choose_tiles<LAST, FULL>(a.g);
+    const bool pairs =
+        in_pairs(ns, t.gram.us, t.square.us, t.update.us);
+    int n = 0;
+    for (int i = 0; i < a.g.count && !FULL && pairs; ++i)
+        n += thin(a.g.m[i]);
+    if (n == 0)
+        return run_products<LAST, FULL>(a, ns, t, pairs, s);
+    if (n == a.g.count)
+        return run_products<LAST, FULL>(a, ns, t, false, s);
+    // the thin ones by themselves, then the others
+    for (const bool now : {true, false}) {
+        GemmArgs b = a;
+        b.g.count = 0;
+        for (int i = 0; i < a.g.count; ++i) {
+            if (thin(a.g.m[i]) != now)
+                continue;
+            const int k = b.g.count++;
+            b.g.m[k] = a.g.m[i];
+            if (LAST == kStep)
+                b.st[k] = a.st[i];
+            else
+                b.out[k] = a.out[i];
+        }
+        if (const int rc = run_steps<LAST, FULL>(b, ns, s)) return rc;
+    }
+    return ZS_OK;
 }
 
 uint32_t init_tiles(const Mat& m)

@@ -48,14 +48,18 @@ def _f16(x):
         return (x * 1024).astype(np.float16).astype(np.float64) / 1024
 
 
-def chain_of(steps, pairs):
-    """Steps taken together: twos, an odd count's single one second."""
-    if not pairs:
+def chain_of(steps, pairs, full=False):
+    """Steps taken together: in full precision twos, an odd count's single one
+    second; else the first two, and of five or more the last two."""
+    if not pairs or steps < 2:
         return [1] * steps
-    out = [2] * (steps // 2)
-    if steps % 2:
-        out.insert(1, 1)
-    return out
+    if full:
+        out = [2] * (steps // 2)
+        if steps % 2:
+            out.insert(1, 1)
+        return out
+    last = [2] if steps >= 5 else []
+    return [2] + [1] * (steps - 2 - 2 * len(last)) + last
 
 
 def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):
@@ -93,7 +97,7 @@ def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):
     X = start(U, eps)
     rows = rows_of(coef, steps)
     k = 0
-    for many in chain_of(steps, pairs):
+    for many in chain_of(steps, pairs, full):
         x = pair(X)
         A = square(times(x, (x[0].T, x[1].T)))
         E = None

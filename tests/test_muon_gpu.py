@@ -228,6 +228,20 @@ def test_group_of_shapes_equals_single_calls():
     assert run(xs[4:6], [torch.empty_like(x) for x in xs[4:6]]) is not None
 
 
+@pytest.mark.parametrize("steps", [2, 3, 4, 6, 8])
+def test_steps_of_a_stack(steps):
+    """A dozen directions some twenty times as strong as the others, in a
+    stack that takes steps in twos."""
+    rng = gen(13)
+    U = (rng.standard_normal((384, 12)) @ rng.standard_normal((12, 1500)) +
+         rng.standard_normal((384, 1500))).astype(np.float32)
+    x = torch.from_numpy(U).cuda().expand(24, 384, 1500)
+    o = torch.empty(24, 384, 1500, device="cuda")
+    run([x], [o], steps=steps)
+    check(U, o[0], steps=steps)
+    assert torch.equal(o[23], o[0])
+
+
 def strong(rng, r, c):
     """One direction six times as strong as the others."""
     u, v = rng.standard_normal((r, 1)), rng.standard_normal((1, c))

@@ -109,7 +109,8 @@ int zs_orthogonalize_workspace(int32_t count, const zs_ns_matrices* mats,
  * ZS_EALIGN (a pointer not aligned to its element, the workspace to 256);
  * ZS_ERANGE (workspace_bytes too small; rows*cols >= 2^31, the smaller
  * side above 32768, the larger above 2^22, strides that reach past 2^46
- * elements, or a call of more than 2^23 tiles of 64 x 64); ZS_EDEVICE. */
+ * elements, or a call of 2^23 pieces or more, a matrix counting as its tiles
+ * of 64 x 64 or as rows*cols/2048 + 1, whichever is more); ZS_EDEVICE. */
 int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
                      int32_t x_type, int32_t o_type,
                      const zs_newton_schulz* ns, void* workspace,

@@ -151,6 +151,27 @@ def test_workspace_sizes():
     assert orth(m=mats(), nbytes=need(0, (2, 8, 16)) - 1) == ERANGE
 
 
+@pytest.mark.parametrize("precision", [0, 1])
+def test_largest_call(precision):
+    """A launch has fewer than 2^32 threads, and a matrix of one tile up to
+    512: 2^23 of them are refused by the call and by its workspace, one less
+    is not."""
+    a = mats(batch=1 << 23, rows=1, cols=1, x_batch_stride=1,
+             o_batch_stride=1, x_row_stride=1, o_row_stride=1)
+    b = ctypes.c_int64()
+    assert orth(m=a, s=ns(precision=precision)) == ERANGE
+    size = zm._lib().zs_orthogonalize_workspace
+    assert size(1, a, precision, ctypes.byref(b)) == ERANGE
+    a[0].batch -= 1
+    assert size(1, a, precision, ctypes.byref(b)) == 0
+    # the same over two stacks
+    two = mats(2, batch=1 << 22, rows=1, cols=1)
+    assert size(2, two, precision, ctypes.byref(b)) == ERANGE
+    lay = zs.zs_layout_build_tensors([1 << 23], 1, 0)
+    assert step(lay=lay, t=((0, 1 << 23, 1, 1),),
+                hp=muon(ns=ns(precision=precision))) == ERANGE
+
+
 def layout():
     return zs.zs_layout_build_tensors([64 * 48, 300, 5 * 7], 1, 0)
 

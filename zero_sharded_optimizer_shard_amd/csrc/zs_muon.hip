@@ -1535,9 +1535,12 @@ int check_launch(const char* what)
 constexpr int64_t kMaxSide = 32768;             // of the smaller side
 constexpr int64_t kMaxLong = (int64_t)1 << 22;  // of the larger: a tile's rows
                                                 // span less than 4 GiB
-constexpr int64_t kMaxTiles = (int64_t)1 << 23; // 64 x 64 tiles of a call
+// Workgroups of a call's widest launch, at least: HIP allows fewer than 2^32
+// threads, and the small kernel has 512 for a matrix of one tile.
+constexpr int64_t kMaxTiles = ((int64_t)1 << 23) - 1;
 
-// One member's sizes, checked; tiles: 64 x 64 tiles of X or of A.
+// One member's sizes, checked; tiles: a matrix's 64 x 64 tiles or its pieces
+// of the momentum, whichever are more.
 int check_sizes(int32_t i, int64_t batch, int64_t rows, int64_t cols,
                 int64_t& tiles)
 {
@@ -1601,6 +1604,11 @@ using Small64 = Small<64, 64, FULL ? 8 : 4, 2, 2>;
 typedef Small<64, 256, 8, 2, 8> Small256;
 typedef Small<64, 512, 8, 2, 8> Small512;
 typedef Small<128, 128, 8, 2, 2> Small128;
+// A matrix counts for one tile in the first of these, for two and more in the
+// others, and for four and more where sums have a launch of their own.
+static_assert(kMaxTiles * Small64<true>::kThreads < (int64_t)1 << 32 &&
+              kMaxTiles / 2 * 512 < (int64_t)1 << 32 &&
+              kMaxTiles / 4 * kSumNT < (int64_t)1 << 32, "threads of a launch");
 
 // Which of the small kernels takes a matrix: 1 .. kSmalls, 0 for none.  Full
 // precision's pairs leave LDS for the first two.

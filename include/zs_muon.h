@@ -79,9 +79,11 @@ typedef struct {
 
 /* A stack of `batch` matrices of one shape.  Element (i, j) of matrix k is
  * at k*batch_stride + i*row_stride + j, strides in elements.  x: inputs,
- * o: outputs.  row_stride >= cols; outputs of a stack must not overlap
- * (o_batch_stride >= (rows - 1)*o_row_stride + cols when batch > 1), inputs
- * may (x_batch_stride >= 0).  A matrix's output may be the matrix itself; an
+ * o: outputs.  row_stride >= cols; outputs of a stack must not overlap, inputs
+ * may (x_batch_stride >= 0).  With batch > 1 they lie one behind the other
+ * (o_batch_stride >= (rows - 1)*o_row_stride + cols) or side by side, as the
+ * heads of one matrix do (o_batch_stride >= cols and
+ * o_row_stride >= (batch - 1)*o_batch_stride + cols).  A matrix's output may be the matrix itself; an
  * output that shares elements with another matrix of the call is an error
  * that is not detected (the order in which matrices are read and written is
  * not defined). */

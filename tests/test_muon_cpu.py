@@ -151,6 +151,16 @@ def test_workspace_sizes():
     assert orth(m=mats(), nbytes=need(0, (2, 8, 16)) - 1) == ERANGE
 
 
+def test_outputs_side_by_side():
+    """Two matrices of 8 x 16 in rows of their own, or overlapping by one
+    element; past the strides the first lacks its workspace."""
+    for batch, row, code in ((16, 32, ERANGE), (16, 31, EINVAL),
+                             (15, 32, EINVAL), (20, 36, ERANGE),
+                             (20, 35, EINVAL)):
+        m = mats(o_batch_stride=batch, o_row_stride=row)
+        assert orth(m=m, nbytes=0) == code
+
+
 @pytest.mark.parametrize("precision", [0, 1])
 def test_largest_call(precision):
     """A launch has fewer than 2^32 threads, and a matrix of one tile up to

@@ -196,6 +196,27 @@ def test_large_tiles(shape, precision):
         assert r <= t, (r, t)
 
 
+@pytest.mark.parametrize("shape", [(4, 66, 72), (3, 150, 70), (3, 40, 31)],
+                         ids=lambda s: "%dx%dx%d" % s)
+def test_outputs_side_by_side(shape):
+    """Heads of one matrix: the stack's members share its rows, in place too."""
+    h, r, c = shape
+    rng = gen(14)
+    U = np.stack([matrix(rng, r, c) for _ in range(h)])
+    for dtype in (torch.float32, torch.bfloat16):
+        buf = torch.full((r, h * c + 5), 3.0, device="cuda", dtype=dtype)
+        o = buf[:, :h * c].view(r, h, c).transpose(0, 1)
+        x = torch.from_numpy(U).cuda().to(dtype)
+        run([x], [o])
+        for k in range(h):
+            check(x[k].float().cpu().numpy(), o[k])
+        assert torch.all(buf[:, h * c:] == 3)
+        want = o.clone()
+        o.copy_(x)
+        run([o], [o])
+        assert torch.equal(o, want)
+
+
 def test_in_place_and_broadcast_input():
     U = matrix(gen(7), 130, 70)
     x = torch.from_numpy(U).cuda()

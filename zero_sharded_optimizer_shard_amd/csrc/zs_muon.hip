@@ -2166,8 +2166,14 @@ extern "C" int zs_orthogonalize(int32_t count, const zs_ns_matrices* mats,
             m.x_batch_stride > kFar / m.batch ||
             m.o_batch_stride > kFar / m.batch)
             return fail(ZS_ERANGE, "matrices %d: strides too large", i);
-        if (m.batch > 1 &&
-            m.o_batch_stride < (m.rows - 1) * m.o_row_stride + m.cols)
+        // a stack's outputs: one behind the other, or side by side in rows
+        // of their own
+        const bool behind =
+            m.o_batch_stride >= (m.rows - 1) * m.o_row_stride + m.cols;
+        const bool beside =
+            m.o_batch_stride >= m.cols &&
+            m.o_row_stride >= (m.batch - 1) * m.o_batch_stride + m.cols;
+        if (m.batch > 1 && !behind && !beside)
             return fail(ZS_EINVAL, "matrices %d: outputs overlap", i);
         Source& s = src[g.count];
         s.x = m.x;

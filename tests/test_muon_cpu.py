@@ -292,6 +292,27 @@ def test_binding_refuses_coefficients(coef):
         zm._newton_schulz(2, coef, 1e-7, "fast")
 
 
+def test_binding_refuses_integers_that_do_not_fit():
+    """2^32 is 0 to a 32-bit field: another tensor, another precision."""
+    big = 1 << 32
+    for t in ((big, 64, 48), (0, (1 << 64) + 64, 48), (-big, 1, 64, 48)):
+        with pytest.raises(ValueError):
+            zs.zs_muon_workspace(layout(), [t])
+    with pytest.raises(ValueError):
+        zs.zs_muon_workspace(layout(), [(0, 64, 48)], precision=big)
+    for steps in (big + 5, -big + 5, 1 << 70):
+        with pytest.raises(ValueError):
+            zm._newton_schulz(steps, OM.COEF, 1e-7, "fast")
+    with pytest.raises(ValueError):
+        zm._newton_schulz(5, OM.COEF, 1e-7, big + 1)
+    with pytest.raises(TypeError):
+        zm._newton_schulz(5.0, OM.COEF, 1e-7, "fast")
+    # in 32 bits, and the library's to refuse
+    assert zm._newton_schulz(1 << 30, OM.COEF, 1e-7, "fast").steps == 1 << 30
+    assert zm._newton_schulz(np.int64(3), OM.COEF, 1e-7, "full").steps == 3
+    assert zs.zs_muon_workspace(layout(), [(np.int64(0), 64, 48)]) > 0
+
+
 # ---- the oracle -------------------------------------------------------------
 
 @pytest.mark.parametrize("shape", [(20, 33), (33, 20), (24, 24), (1, 9)])

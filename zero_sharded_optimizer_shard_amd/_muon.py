@@ -6,6 +6,7 @@ _zs.py; the caller hands over the workspace, as it does every other buffer.
 from __future__ import annotations
 
 import ctypes
+import operator
 from typing import Sequence
 
 from ._zs import (ZS_GRADS_TILED, ZS_TILE, Layout, _bf16, _check, _f32,
@@ -79,10 +80,19 @@ def _lib():
     return L
 
 
+def _int(v, name: str, bits: int = 32) -> int:
+    """v, if it has a place in the library's integer (ctypes would drop its
+    upper bits without a word)."""
+    v = operator.index(v)
+    if not -(1 << (bits - 1)) <= v < 1 << (bits - 1):
+        raise ValueError(f"{name}: {v} does not fit {bits} bits")
+    return v
+
+
 def _precision(precision) -> int:
     # unknown codes go through unchanged so the library reports them
     return _PRECISION[precision] if precision in _PRECISION \
-        else int(precision)
+        else _int(int(precision), "precision")
 
 
 _Coef = ctypes.c_float * 3
@@ -90,6 +100,7 @@ _Coef = ctypes.c_float * 3
 
 def _newton_schulz(steps: int, coef, eps: float, precision):
     """coef: one (a, b, c) for every step, or one per step."""
+    steps = _int(steps, "steps")
     ns = zs_newton_schulz(steps, _precision(precision), eps)
     per_step = len(coef) > 0 and isinstance(coef[0], (tuple, list))
     for row in coef if per_step else [coef]:
@@ -97,8 +108,9 @@ def _newton_schulz(steps: int, coef, eps: float, precision):
             raise ValueError(f"coef: {len(row)} coefficients, not 3")
     if per_step and len(coef) != steps:
         raise ValueError(f"coef: {len(coef)} rows for {steps} steps")
+    # a number of steps past the last place is the library's to refuse
     rows = [_Coef(*row) for row in coef] if per_step \
-        else [_Coef(*coef)] * steps
+        else [_Coef(*coef)] * min(steps, ZS_NS_MAX_STEPS)
     for k, row in enumerate(rows[:ZS_NS_MAX_STEPS]):
         ns.coef[k] = row
     return ns
@@ -216,8 +228,9 @@ def _tensors(tensors):
         if len(t) not in (3, 4):
             raise ValueError("tensors: need (bucket_id, rows, cols) or "
                              "(bucket_id, batch, rows, cols)")
-        arr[i] = zs_muon_tensor(t[0], *((1,) + tuple(t[1:]) if len(t) == 3
-                                        else t[1:]))
+        sizes = (1,) + tuple(t[1:]) if len(t) == 3 else t[1:]
+        arr[i] = zs_muon_tensor(_int(t[0], "bucket_id"),
+                                *[_int(v, "tensors", 64) for v in sizes])
     return arr
 
 
@@ -246,7 +259,8 @@ def zs_muon_step(layout: Layout, tensors: Sequence, grads: Sequence, state,
     if len(grads) != n:
         raise ValueError("one gradient tensor per matrix tensor")
     _device(*grads, state, param_shard, full_flat, workspace)
-    code = _layout_code(grad_layout)
+    code = _int(_layout_code(grad_layout), "grad_layout")
+    grad_stride = _int(grad_stride, "grad_stride", 64)
     _, _, _, W, buckets = layout.sizes()
     arr = _tensors(tensors)
     for t, g in zip(arr, grads):
@@ -261,7 +275,8 @@ def zs_muon_step(layout: Layout, tensors: Sequence, grads: Sequence, state,
                full_flat)
     ptrs = (ctypes.c_void_p * max(n, 1))(*[_bf16(g, "grads") for g in grads])
     hp = zs_muon(lr, momentum, weight_decay, int(bool(nesterov)),
-                 _SCALE[scale] if scale in _SCALE else int(scale),
+                 _SCALE[scale] if scale in _SCALE
+                 else _int(int(scale), "scale"),
                  _newton_schulz(steps, coef, eps, precision))
     ws, nbytes = _workspace(workspace)
     _check(_lib().zs_muon_step(layout.handle, n, arr, ptrs, code,

@@ -175,8 +175,9 @@ int zs_muon_workspace(const zs_layout* layout, int32_t count,
  * occur: such tensors own no bucket.
  * Errors, all before any launch: as zs_buckets_step and zs_orthogonalize,
  * and ZS_EINVAL for a layout that is not whole-tensor, batch, rows or cols
- * that do not multiply to the tensor's element count, lr, momentum or
- * weight_decay not finite, an unknown scale. */
+ * that do not multiply to the tensor's element count, lr, momentum,
+ * weight_decay, lr*s or 1 - lr*weight_decay not finite in fp32, an unknown
+ * scale. */
 int zs_muon_step(const zs_layout* layout, int32_t count,
                  const zs_muon_tensor* tensors, const uint16_t* const* grads,
                  int32_t grad_layout, int64_t grad_stride, float* state,

@@ -235,6 +235,16 @@ def test_step_refusals(code, kw):
     assert zs.zs_last_error()
 
 
+@pytest.mark.parametrize("hp", [
+    dict(lr=3e38), dict(lr=-3e38), dict(lr=1e30, weight_decay=1e10, scale=0),
+    dict(lr=1e30, weight_decay=-1e10, scale=0)])
+def test_step_refuses_factors_that_overflow(hp):
+    """lr is finite, lr * 0.2 * sqrt(64) and 1 - lr * weight_decay are not:
+    they would make NaN of a weight whose update is zero."""
+    assert step(hp=muon(**hp)) == EINVAL
+    assert "finite" in zs.zs_last_error()
+
+
 def test_step_needs_a_whole_tensor_layout():
     lay = zs.zs_layout_build([64 * 48], 1, 0)
     assert step(lay=lay) == EINVAL

@@ -2264,7 +2264,7 @@ void launch_momentum(const MomArgs& a, bool tiled, uint32_t n, hipStream_t s)
 
 template <bool FULL>
 int muon_step(const Group& g, MomArgs& ma, const StepMat* st, bool tiled,
-              const zs_muon& hp, hipStream_t s)
+              float dec, const zs_newton_schulz& ns, hipStream_t s)
 {
     ma.g = g;
     Source src[kMaxMats] = {};
@@ -2289,9 +2289,7 @@ int muon_step(const Group& g, MomArgs& ma, const StepMat* st, bool tiled,
     default: launch_momentum<0>(ma, tiled, n, s); break;
     }
     if (const int rc = check_launch("momentum kernel")) return rc;
-    const Work w = {&g, src, ZS_F32, kStep, nullptr, st,
-                    (float)(1.0 - (double)hp.lr * (double)hp.weight_decay),
-                    &hp.ns};
+    const Work w = {&g, src, ZS_F32, kStep, nullptr, st, dec, &ns};
     Group large;
     int at[kMaxMats];
     if (const int rc = run_small<FULL>(w, large, at, s)) return rc;
@@ -2334,6 +2332,10 @@ extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
     if (hp->scale != ZS_MUON_SCALE_NONE && hp->scale != ZS_MUON_SCALE_SHAPE &&
         hp->scale != ZS_MUON_SCALE_RMS)
         return fail(ZS_EINVAL, "unknown scale %d", hp->scale);
+    const float dec =
+        (float)(1.0 - (double)hp->lr * (double)hp->weight_decay);
+    if (!std::isfinite(dec))
+        return fail(ZS_EINVAL, "1 - lr*weight_decay is not finite");
     const bool full = hp->ns.precision == ZS_NS_FULL;
     Group g;
     int64_t used;
@@ -2385,6 +2387,9 @@ extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
                 ? 0.2 * std::sqrt(r > c ? r : c)
                 : 1.0;
         st[n].s = (float)((double)hp->lr * scale);
+        if (!std::isfinite(st[n].s))
+            return fail(ZS_EINVAL, "tensors[%d]: lr times its scale is not "
+                        "finite", i);
     }
     if (workspace_bytes < used)
         return fail(ZS_ERANGE, "workspace of %lld bytes, %lld needed",
@@ -2397,6 +2402,6 @@ extern "C" int zs_muon_step(const zs_layout* L, int32_t count,
     ma.invw = 1.f / (float)L->world;
     ma.pow2 = (L->world & (L->world - 1)) == 0;
     const hipStream_t s = static_cast<hipStream_t>(hip_stream);
-    return full ? muon_step<true>(g, ma, st, tiled, *hp, s)
-                : muon_step<false>(g, ma, st, tiled, *hp, s);
+    return full ? muon_step<true>(g, ma, st, tiled, dec, hp->ns, s)
+                : muon_step<false>(g, ma, st, tiled, dec, hp->ns, s);
 }

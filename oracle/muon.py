@@ -50,7 +50,7 @@ def _f16(x):
 
 def chain_of(steps, pairs, full=False):
     """Steps taken together: in full precision twos, an odd count's single one
-    second; else the first two, and of five or more the last two."""
+    second; else the first two."""
     if not pairs or steps < 2:
         return [1] * steps
     if full:
@@ -58,8 +58,7 @@ def chain_of(steps, pairs, full=False):
         if steps % 2:
             out.insert(1, 1)
         return out
-    last = [2] if steps >= 5 else []
-    return [2] + [1] * (steps - 2 - 2 * len(last)) + last
+    return [2] + [1] * (steps - 2)
 
 
 def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):

@@ -338,6 +338,29 @@ def test_oracle_maps_singular_values(shape):
                        rtol=0, atol=1e-11)
 
 
+def directions(kind, rng, m, n):
+    """`kind` 8: eight directions 100 times the others; k: singular values
+    1/k."""
+    def q(a, b):
+        return np.linalg.qr(rng.standard_normal((a, b)))[0]
+    if kind == "k":
+        return (q(m, m) / np.arange(1, m + 1.)) @ q(n, m).T
+    w = rng.standard_normal((m, n))
+    return w / np.linalg.norm(w, 2) + 100 * q(m, 8) @ q(n, 8).T
+
+
+@pytest.mark.parametrize("steps", [5, 6, 10])
+@pytest.mark.parametrize("kind", ["8", "k"])
+def test_steps_together_cost_no_accuracy(kind, steps):
+    """In fast precision: another draw of roundings as large, so at most
+    twice those of steps one by one."""
+    U = directions(kind, np.random.default_rng(3), 256, 1061)
+    e = OM.orthogonalize(U, steps)
+    one, two = (np.linalg.norm(OM.rounded(U, steps, pairs=p) - e)
+                for p in (False, True))
+    assert two <= 2 * one
+
+
 @pytest.mark.parametrize("full,u", [(False, 2.0 ** -11), (True, 2.0 ** -22)])
 @pytest.mark.parametrize("shape", [(40, 90), (90, 40), (64, 64)])
 def test_rounded_oracle_of_one_step(shape, full, u):

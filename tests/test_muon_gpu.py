@@ -263,6 +263,28 @@ def test_steps_of_a_stack(steps):
     assert torch.equal(o[23], o[0])
 
 
+@pytest.mark.parametrize("kind,steps", [("8", 5), ("8", 6), ("k", 5)])
+def test_stack_of_strong_directions(kind, steps):
+    """Eight directions a hundred times the others, or singular values 1/k,
+    in a stack that takes steps in twos: as exact as one by one."""
+    rng = gen(15)
+    q = lambda a, b: np.linalg.qr(rng.standard_normal((a, b)))[0]  # noqa
+    if kind == "k":
+        U = (q(256, 256) / np.arange(1, 257)) @ q(3000, 256).T
+    else:
+        U = rng.standard_normal((256, 3000))
+        U = U / np.linalg.norm(U, 2) + 100 * q(256, 8) @ q(3000, 8).T
+    U = U.astype(np.float32)
+    x = torch.from_numpy(U).cuda().expand(24, 256, 3000)
+    o = torch.empty(24, 256, 3000, device="cuda")
+    run([x], [o], steps=steps)
+    exact = OM.orthogonalize(U, steps)
+    t = 2 * rel(OM.rounded(U, steps, pairs=False), exact) + 2.0 ** -18
+    got = rel(o[0].cpu().numpy(), exact)
+    assert got <= t, (got, t)
+    assert torch.equal(o[23], o[0])
+
+
 def strong(rng, r, c):
     """One direction six times as strong as the others."""
     u, v = rng.standard_normal((r, 1)), rng.standard_normal((1, c))

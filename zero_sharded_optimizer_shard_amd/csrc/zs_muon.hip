@@ -1810,11 +1810,12 @@ int launch_product(GemmArgs& a, int tile, hipStream_t s)
 // third step in the same way would multiply that by a^2 = 12 again (a matrix
 // of 1024 x 3584 with singular values 1/k: 2.2e-4 one by one, 1e-3 in twos,
 // 5e-3 in threes), so it is at most two.  In fast precision twos are the first
-// two steps, where no direction is near one yet, and from five steps on the
-// last two, after which nothing grows; between them are single ones (384 x
-// 1500, twelve strong directions over noise, six steps: 5.3e-4 one by one,
-// 2.2e-3 in twos, 5.8e-4 as two, one, one, two).  In full precision all are
-// twos; of an odd number the second turn is the single one.
+// two steps alone, where no direction is near one yet (256 x 3000, eight
+// directions 100 times the others, five steps: 1.7e-4 one by one, 2.2e-4 so,
+// 8.7e-4 with the last two together as well; singular values 1/k: 3.2e-4,
+// 3.5e-4, 1.2e-3): the rounding of a gram is seen and corrected by the next
+// one, which a later two leaves out.  In full precision all are twos; of an odd number the
+// second turn is the single one.
 //
 // Whether step k goes together with the next, where twos are taken at all.  E
 // is about a a' where A is small and has to stay in fp16's range.
@@ -1822,7 +1823,7 @@ bool together(const zs_newton_schulz& ns, int k)
 {
     const bool may = ns.precision == ZS_NS_FULL
                          ? !(ns.steps % 2 && k == 2)
-                         : k == 0 || (k == ns.steps - 2 && k >= 3);
+                         : k == 0;
     return may && k + 1 < ns.steps &&
            std::fabs(ns.coef[k][0] * ns.coef[k + 1][0]) < 24;
 }

@@ -61,21 +61,28 @@ def chain_of(steps, pairs, full=False):
     return [2] + [1] * (steps - 2)
 
 
-def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):
+def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False,
+            drop=None):
     """One matrix, with the library's fp16 roundings and exact sums; `pairs`:
     two steps taken together on the smaller side, as the library does where
-    that is less work."""
+    that is less work.  `drop`: a mistake, for tests of tolerances: which
+    product ("gram", "poly", "prod" or "update") of full precision lacks its
+    high x low ("hl") or low x high ("lh") part."""
     U = np.asarray(U, np.float64)
     if U.shape[0] > U.shape[1]:
-        return rounded(U.T, steps, coef, eps, full, pairs).T
+        return rounded(U.T, steps, coef, eps, full, pairs, drop).T
 
     def pair(x):
         hi = _f16(x)
         return hi, _f16(x - hi)
 
-    def times(p, q):
+    def times(p, q, what):
         s = p[0] @ q[0]
-        return s + p[0] @ q[1] + p[1] @ q[0] if full else s
+        if full and drop != (what, "hl"):
+            s = s + p[0] @ q[1]
+        if full and drop != (what, "lh"):
+            s = s + p[1] @ q[0]
+        return s
 
     def square(M):
         """fp16 without the diagonal (a pair if full), and the diagonal; one
@@ -88,9 +95,9 @@ def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):
     def whole(M):
         return M[0][0] + M[0][1] + np.diag(M[1])
 
-    def product(M, N):
+    def product(M, N, what="prod"):
         (R, d), (S, f) = M, N
-        return (times(R, S) + d[:, None] * (S[0] + S[1]) +
+        return (times(R, S, what) + d[:, None] * (S[0] + S[1]) +
                 (R[0] + R[1]) * f[None] + np.diag(d * f))
 
     X = start(U, eps)
@@ -98,17 +105,17 @@ def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False):
     k = 0
     for many in chain_of(steps, pairs, full):
         x = pair(X)
-        A = square(times(x, (x[0].T, x[1].T)))
+        A = square(times(x, (x[0].T, x[1].T), "gram"))
         E = None
         for q in range(many):
             a, b, c = rows[k]
             k += 1
-            M = b * whole(A) + c * product(A, A)
+            M = b * whole(A) + c * product(A, A, "poly")
             C = square(M + a * np.eye(len(M)))
             E = C if E is None else square(product(C, E))
             if q + 1 < many:
                 A = square(product(square(product(C, A)), C))
-        X = E[1][:, None] * (x[0] + x[1]) + times(E[0], x)
+        X = E[1][:, None] * (x[0] + x[1]) + times(E[0], x, "update")
     return X
 
 

@@ -50,8 +50,11 @@
 
 #include "zs_internal.h"
 #include "zs_muon.h"
+#include "zs_muon_plan.h"
 
 namespace {
+
+using namespace zs::muon;
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
@@ -59,24 +62,8 @@ typedef _Float16 f16;
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr int kMaxMats = ZS_MAX_GROUP;
-constexpr int kPad = 64;                 // sides are stored rounded up to this
 constexpr float kScale = 1024.f, kUnscale = 1.f / 1024.f;
 constexpr int64_t kTile = ZS_TILE;
-
-__host__ __device__ inline int32_t padded(int32_t n)
-{
-    return (n + kPad - 1) / kPad * kPad;
-}
-
-// One stack of matrices in the workspace.
-struct Mat {
-    char* ws;
-    int32_t R, C;           // rows, cols
-    int32_t batch;
-    int32_t nparts;         // partial sums of squares per matrix
-    uint32_t tiles;         // workgroups of the present launch
-};
 
 // Where its parts lie: E elements of X, S of a square, D of a diagonal, over
 // the whole stack, and in one matrix e, s and mp.
@@ -134,13 +121,6 @@ struct Region {
         return (double*)(ws + parts_off());
     }
     __host__ float* u() const { return (float*)(ws + 4 * E); }  // xd(1)
-};
-
-struct Group {
-    int32_t count;
-    uint32_t start[kMaxMats];           // first workgroup of each stack; past
-                                        // the last one 2^32 - 1
-    Mat m[kMaxMats];
 };
 
 // The stack of workgroup `bid`, and the workgroup's index within it.  All
@@ -530,16 +510,6 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
 
 // ---- the products ----------------------------------------------------------
 
-// What a product's epilogue makes of D, and which operands it has:
-//   kGram     A = X X^T
-//   kPoly     C = a + b A + c A A
-//   kProd     the product of two of the squares, which commute
-//   kUpdate   X <- C X; the last one goes to the caller instead: kOutBf16,
-//             kOutF32, or kStep, which steps the weights by it
-enum Epi { kGram, kPoly, kProd, kUpdate, kOutBf16, kOutF32, kStep };
-
-__host__ __device__ constexpr bool symmetric(int epi) { return epi <= kProd; }
-
 struct OutMat {
     void* o;
     int64_t batch, row;
@@ -608,14 +578,6 @@ __device__ __forceinline__ void slot_barrier()
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
-}
-
-// Tiles of one matrix's D.
-template <int BT>
-__host__ __device__ inline uint32_t tri_tiles(int32_t mp)
-{
-    const uint32_t t = (mp + BT - 1) / BT;
-    return t * (t + 1) / 2;
 }
 
 // Workgroups go to the 8 XCDs in turn; give each XCD a run of neighbouring
@@ -1610,20 +1572,6 @@ static_assert(kMaxTiles * Small64<true>::kThreads < (int64_t)1 << 32 &&
               kMaxTiles / 2 * 512 < (int64_t)1 << 32 &&
               kMaxTiles / 4 * kSumNT < (int64_t)1 << 32, "threads of a launch");
 
-// Which of the small kernels takes a matrix: 1 .. kSmalls, 0 for none.  Full
-// precision's pairs leave LDS for the first two.
-constexpr int kSmalls = 4;
-int small_kind(int32_t R, int32_t C, bool full)
-{
-    const int32_t rp = padded(R), cp = padded(C);
-    const int32_t m = rp < cp ? rp : cp, n = rp < cp ? cp : rp;
-    if (m == 64 && n <= 64) return 1;
-    if (m == 64 && n <= 256) return 2;
-    if (full) return 0;
-    if (m == 64 && n <= 512) return 3;
-    return m == 128 && n == 128 ? 4 : 0;
-}
-
 // A stack's bytes of workspace.
 int64_t mat_bytes(const Mat& m, bool full)
 {
@@ -1634,27 +1582,6 @@ int64_t mat_bytes(const Mat& m, bool full)
         full ? Region<true>(nullptr, m.R, m.C, m.batch).parts_off()
              : Region<false>(nullptr, m.R, m.C, m.batch).parts_off();
     return (off + parts + 255) / 256 * 256;
-}
-
-// The order in which the members enter the group: by the larger side, then
-// the smaller, so that the tiles with the longest sums start first.
-template <class Sides>
-void sort_members(int32_t* order, int32_t count, Sides sides)
-{
-    for (int32_t i = 0; i < count; ++i) {
-        int64_t r, c;
-        sides(i, r, c);
-        int32_t k = i;
-        for (; k > 0; --k) {
-            int64_t qr, qc;
-            sides(order[k - 1], qr, qc);
-            const int64_t hi = r > c ? r : c, lo = r > c ? c : r;
-            const int64_t qh = qr > qc ? qr : qc, ql = qr > qc ? qc : qr;
-            if (qh > hi || (qh == hi && ql >= lo)) break;
-            order[k] = order[k - 1];
-        }
-        order[k] = i;
-    }
 }
 
 // Appends a stack to the group, with its part of the workspace.
@@ -1678,32 +1605,6 @@ int64_t group_bytes(const Group& g, bool full)
     return n;
 }
 
-// Workgroup prefix sums: fn(mat) workgroups per matrix of the stack, each
-// stack's from a multiple of `align` on.
-template <class Fn>
-uint32_t set_starts(Group& g, Fn fn, uint32_t align = 1)
-{
-    uint32_t n = 0;
-    for (int i = 0; i < g.count; ++i) {
-        g.start[i] = n;
-        g.m[i].tiles = (uint32_t)g.m[i].batch * (uint32_t)fn(g.m[i]);
-        n += (g.m[i].tiles + align - 1) / align * align;
-    }
-    for (int i = g.count; i < kMaxMats; ++i)
-        g.start[i] = UINT32_MAX;
-    return n;
-}
-
-// Tiles of one matrix's D in a product.
-template <int BT, int EPI>
-uint32_t d_tiles(const Mat& m)
-{
-    const int32_t rp = padded(m.R), cp = padded(m.C);
-    if (symmetric(EPI))
-        return tri_tiles<BT>(rp < cp ? rp : cp);
-    return ((rp + BT - 1) / BT) * ((cp + BT - 1) / BT);
-}
-
 template <class SH, int EPI, bool FULL>
 int launch_gemm(GemmArgs& a, hipStream_t s)
 {
@@ -1711,80 +1612,6 @@ int launch_gemm(GemmArgs& a, hipStream_t s)
     hipLaunchKernelGGL((ns_gemm_kernel<SH, EPI, FULL>), dim3(n),
                        dim3(SH::kThreads), 0, s, a);
     return check_launch("Newton-Schulz product");
-}
-
-// Time of a launch in tiles of one size, in us: `stage` per 64 k and `fixed`
-// per tile with `resident` tiles on each of the 256 CUs, or `alone` per 64 k
-// while there is at most one.  The stacks' tiles go to the free places in
-// order, longest first (the group is sorted so).
-template <int BT, int EPI>
-double estimate(const Group& g, double stage, double alone, double fixed,
-                int resident)
-{
-    struct Places {
-        double free;
-        int64_t n;
-    } at[64];
-    int64_t n = 0;
-    for (int p = 0; p < g.count; ++p)
-        n += (int64_t)g.m[p].batch * d_tiles<BT, EPI>(g.m[p]);
-    const double per = n <= 256 ? alone : stage;
-    int used = 1;
-    at[0] = {0, 256 * (int64_t)resident};
-    double end = 0;
-    for (int p = 0; p < g.count; ++p) {
-        const Mat& m = g.m[p];
-        const int32_t rp = padded(m.R), cp = padded(m.C);
-        const int nk = ((EPI == kGram) == (rp < cp) ? cp : rp) / 64;
-        const double t = nk * per + fixed;
-        int64_t left = (int64_t)m.batch * d_tiles<BT, EPI>(m);
-        // whole rounds of everything, then the rest
-        const int64_t rounds = left / (256 * resident);
-        for (int k = 0; k < used; ++k)
-            at[k].free += (double)rounds * t;
-        left -= rounds * 256 * resident;
-        while (left > 0) {
-            int k = 0;
-            for (int q = 1; q < used; ++q)
-                if (at[q].free < at[k].free) k = q;
-            if (at[k].n > left && used < 64) {
-                at[used++] = {at[k].free, at[k].n - left};
-                at[k].n = left;
-            }
-            left -= at[k].n;
-            at[k].free += t;
-        }
-    }
-    for (int k = 0; k < used; ++k)
-        end = at[k].free > end ? at[k].free : end;
-    return end;
-}
-
-// The tile for a product on these stacks, by estimated time.
-struct Choice {
-    int tile;
-    double us;
-};
-
-template <int EPI, bool FULL>
-Choice choose_tile(const Group& g)
-{
-    const double c = FULL ? 2.7 : 1;    // three products for one
-    // beside the products: a launch, the first loads, and the epilogue, which
-    // moves four bytes an element in a square, ten in an update, and in the
-    // step fourteen to sixteen with the tiles of a round all at once
-    const int k = symmetric(EPI) ? 0 : EPI == kStep ? 2 : 1;
-    constexpr double fixed[3][4] = {
-        {5, 7, 9, 10}, {7, 13, 20, 22}, {8, 20, 35, 55}};
-    Choice best = {64,
-                   estimate<64, EPI>(g, 0.36 * c, 0.18 * c, fixed[k][0], 2)};
-    auto offer = [&](int t, double us) {
-        if (us < best.us) best = {t, us};
-    };
-    offer(128, estimate<128, EPI>(g, 0.98 * c, 0.6 * c, fixed[k][1], 2));
-    offer(192, estimate<192, EPI>(g, 1.12 * c, 0.95 * c, fixed[k][2], 1));
-    offer(256, estimate<256, EPI>(g, 1.5 * c, 1.4 * c, fixed[k][3], 1));
-    return best;
 }
 
 template <int EPI, bool FULL>
@@ -1798,67 +1625,11 @@ int launch_product(GemmArgs& a, int tile, hipStream_t s)
     }
 }
 
-// Two steps taken together on the m x m side.  In units of m^3 flops with
-// r = n/m, a symmetric product being 1:
-//   one by one   A = X X^T (r), C = a + b A + c A A (1), X <- C X (2 r),
-//                twice: 6 r + 2
-//   together     A (r), C (1), T = C A (1), A' = T C (1), C' from A' (1),
-//                E = C' C (1), X <- E X (2 r): 3 r + 5
-// for A' = C A C is the next step's A: polynomials of one matrix commute.
-// The small directions of A' carry the rounding of the large ones, a^2 times,
-// but only into C', where they count for a^2 b 2^-12; X itself stays exact.  A
-// third step in the same way would multiply that by a^2 = 12 again (a matrix
-// of 1024 x 3584 with singular values 1/k: 2.2e-4 one by one, 1e-3 in twos,
-// 5e-3 in threes), so it is at most two.  In fast precision twos are the first
-// two steps alone, where no direction is near one yet (256 x 3000, eight
-// directions 100 times the others, five steps: 1.7e-4 one by one, 2.2e-4 so,
-// 8.7e-4 with the last two together as well; singular values 1/k: 3.2e-4,
-// 3.5e-4, 1.2e-3): the rounding of a gram is seen and corrected by the next
-// one, which a later two leaves out.  In full precision all are twos; of an odd number the
-// second turn is the single one.
-//
-// Whether step k goes together with the next, where twos are taken at all.  E
-// is about a a' where A is small and has to stay in fp16's range.
-bool together(const zs_newton_schulz& ns, int k)
-{
-    const bool may = ns.precision == ZS_NS_FULL
-                         ? !(ns.steps % 2 && k == 2)
-                         : k == 0;
-    return may && k + 1 < ns.steps &&
-           std::fabs(ns.coef[k][0] * ns.coef[k + 1][0]) < 24;
-}
-
-// Whether twos take less time, by the estimates of the launches.
-bool in_pairs(const zs_newton_schulz& ns, double gram, double square,
-              double update)
-{
-    double pairs = 0;
-    for (int k = 0; k < ns.steps;) {
-        const bool two = together(ns, k);
-        pairs += gram + (two ? 5.2 : 1) * square + update;
-        k += two ? 2 : 1;
-    }
-    return pairs < 0.97 * ns.steps * (gram + square + update);
-}
-
-// The tiles of a group's products; LAST: the epilogue of the last update.
-struct Tiles {
-    Choice gram, square, update, last;
-};
-
 template <int LAST, bool FULL>
-Tiles choose_tiles(const Group& g)
+int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Part& part,
+                 hipStream_t s)
 {
-    return {choose_tile<kGram, FULL>(g), choose_tile<kPoly, FULL>(g),
-            choose_tile<kUpdate, FULL>(g), choose_tile<LAST, FULL>(g)};
-}
-
-template <int LAST, bool FULL>
-int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Tiles& t,
-                 bool pairs, hipStream_t s)
-{
-    const Choice &gram = t.gram, &square = t.square, &update = t.update,
-                 &last = t.last;
+    const Tiles& t = part.tiles;
     a.parity = 0;
     int rc = ZS_OK;
     auto poly = [&](int k, Square out) {
@@ -1867,18 +1638,18 @@ int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Tiles& t,
         a.c = ns.coef[k][2];
         a.sp = a.sq = kA;
         a.so = out;
-        if (!rc) rc = launch_product<kPoly, FULL>(a, square.tile, s);
+        if (!rc) rc = launch_product<kPoly, FULL>(a, t.square.tile, s);
     };
     auto prod = [&](Square p, Square q, Square out) {
         a.sp = p;
         a.sq = q;
         a.so = out;
-        if (!rc) rc = launch_product<kProd, FULL>(a, square.tile, s);
+        if (!rc) rc = launch_product<kProd, FULL>(a, t.square.tile, s);
     };
     for (int k = 0; k < ns.steps && !rc;) {
-        const bool two = pairs && together(ns, k);
+        const bool two = part.pairs && together(ns, k);
         a.so = kA;
-        rc = launch_product<kGram, FULL>(a, gram.tile, s);
+        rc = launch_product<kGram, FULL>(a, t.gram.tile, s);
         poly(k, kC);
         if (two) {
             prod(kC, kA, kT);
@@ -1889,54 +1660,34 @@ int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Tiles& t,
         k += two ? 2 : 1;
         a.sp = two ? kT : kC;
         if (!rc)
-            rc = k < ns.steps ? launch_product<kUpdate, FULL>(a, update.tile, s)
-                              : launch_product<LAST, FULL>(a, last.tile, s);
+            rc = k < ns.steps
+                     ? launch_product<kUpdate, FULL>(a, t.update.tile, s)
+                     : launch_product<LAST, FULL>(a, t.last.tile, s);
         a.parity ^= 1;
     }
     return rc;
-}
-
-// In fast precision twos are not for matrices of few rows: a strong
-// direction's part of A off the diagonal is then spread over few elements,
-// and its rounding does not average out (roundings modelled in 64 bits, one
-// direction six times the others:
-// 8 x 1200 5.8e-4 one by one and 8.7e-3 in twos, 32 x 1200 2.3e-4 and 5.9e-4,
-// 64 x 1200 2.3e-4 and 3.6e-4).  A single row has nothing off the diagonal.
-bool thin(const Mat& m)
-{
-    const int32_t side = m.R < m.C ? m.R : m.C;
-    return side > 1 && side < 64;
 }
 
 // The steps on a group whose X[0] is in the workspace.
 template <int LAST, bool FULL>
 int run_steps(GemmArgs& a, const zs_newton_schulz& ns, hipStream_t s)
 {
-    const Tiles t = choose_tiles<LAST, FULL>(a.g);
-    const bool pairs =
-        in_pairs(ns, t.gram.us, t.square.us, t.update.us);
-    int n = 0;
-    for (int i = 0; i < a.g.count && !FULL && pairs; ++i)
-        n += thin(a.g.m[i]);
-    if (n == 0)
-        return run_products<LAST, FULL>(a, ns, t, pairs, s);
-    if (n == a.g.count)
-        return run_products<LAST, FULL>(a, ns, t, false, s);
-    // the thin ones by themselves, then the others
-    for (const bool now : {true, false}) {
+    Part parts[2];
+    const int n = plan_steps<LAST, FULL>(a.g, ns, parts);
+    if (n == 1)
+        return run_products<LAST, FULL>(a, ns, parts[0], s);
+    for (const Part& part : parts) {
         GemmArgs b = a;
-        b.g.count = 0;
-        for (int i = 0; i < a.g.count; ++i) {
-            if (thin(a.g.m[i]) != now)
-                continue;
-            const int k = b.g.count++;
+        b.g.count = part.count;
+        for (int k = 0; k < part.count; ++k) {
+            const int i = part.at[k];
             b.g.m[k] = a.g.m[i];
             if (LAST == kStep)
                 b.st[k] = a.st[i];
             else
                 b.out[k] = a.out[i];
         }
-        if (const int rc = run_steps<LAST, FULL>(b, ns, s)) return rc;
+        if (const int rc = run_products<LAST, FULL>(b, ns, part, s)) return rc;
     }
     return ZS_OK;
 }

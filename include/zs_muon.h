@@ -56,9 +56,10 @@ extern "C" {
  *   ZS_NS_FULL  three products each (high x high, high x low, low x high),
  *     22 bits throughout: about 1e-5 or less, what fp32 products give.
  * Two steps are taken together, as products of m x m matrices, where that is
- * less work (m the smaller side, in fast precision 64 at least; it goes by the shapes of all matrices of a
- * call, so a matrix's result may differ by its rounding from one call's
- * company to another's).
+ * less work: in fast precision the first two alone, and where m (the smaller
+ * side) is 1 or at least 128.  It goes by the shapes of all matrices of a call, so a
+ * matrix's result may differ by its rounding from one call's company to
+ * another's.
  * Range: the entries of X, A and b A + c A A must stay below 63 in
  * magnitude, which singular values under 2 and the usual coefficients never
  * leave; past it the result is not finite. */

@@ -51,7 +51,7 @@ COVER = {
         65), (36, 129, 931), (36, 519, 680), (36, 948, 132), (60, 72, 296),
         (60, 132, 960), (60, 145, 803), (60, 259, 73), (60, 320, 68), (60,
         391, 619), (60, 547, 129), (60, 772, 136), (60, 860, 133)],
-    ('fast', STEP): [(1, 67, 136), (1, 1771, 5880), (1, 1869, 5502), (1, 6097,
+    ('fast', STEP): [(1, 67, 136), (9, 137, 1502), (1, 1771, 5880), (1, 1869, 5502), (1, 6097,
         1675), (1, 6860, 1680), (24, 652, 84), (36, 292, 267), (36, 610, 521),
         (60, 73, 523), (60, 93, 564), (60, 148, 740), (60, 152, 726), (60,
         194, 519), (60, 432, 392), (60, 730, 153), (60, 740, 136)],

@@ -285,6 +285,21 @@ def test_stack_of_strong_directions(kind, steps):
     assert torch.equal(o[23], o[0])
 
 
+def test_stack_of_64_rows():
+    """One direction thirty times the others: as exact as one by one, where
+    twos are 2.7 times as far off."""
+    rng = gen(16)
+    u, v = rng.standard_normal((64, 1)), rng.standard_normal((1, 1200))
+    U = rng.standard_normal((64, 1200))
+    U = (U / np.linalg.norm(U, 2) + 30 * (u / np.linalg.norm(u)) @
+         (v / np.linalg.norm(v))).astype(np.float32)
+    x = torch.from_numpy(U).cuda().expand(24, 64, 1200)
+    o = torch.empty(24, 64, 1200, device="cuda")
+    run([x], [o])
+    check_singly(U, o[0])
+    assert torch.equal(o[23], o[0])
+
+
 def strong(rng, r, c):
     """One direction six times as strong as the others."""
     u, v = rng.standard_normal((r, 1)), rng.standard_normal((1, c))

@@ -70,6 +70,18 @@ def test_few_rows_by_themselves(lib):
         lib, stacks[:1], P.OUT_F32, False)]
 
 
+@pytest.mark.parametrize("rows,twos", [(1, True), (2, False), (63, False),
+                                       (64, False), (127, False),
+                                       (128, True), (192, True)])
+def test_rows_from_which_steps_go_together(lib, rows, twos):
+    """In fast precision; in full precision all of them do."""
+    for r, c in ((rows, 8000), (8000, rows)):
+        got = P.launches(lib, [(60, r, c)], P.OUT_F32, False)
+        assert (P.PROD in [e for e, _, _ in got]) == twos
+        got = P.launches(lib, [(60, r, c)], P.OUT_F32, True)
+        assert P.PROD in [e for e, _, _ in got]
+
+
 # shorter side first, where twos are likely and where they are not
 @pytest.mark.parametrize("shape", [(65, 69), (66, 275), (136, 588), (157, 1230),
                                    (204, 545), (399, 403), (333, 1001)],

@@ -246,14 +246,19 @@ Tiles choose_tiles(const Group& g)
 
 // In fast precision twos are not for matrices of few rows: a strong
 // direction's part of A off the diagonal is then spread over few elements,
-// and its rounding does not average out (roundings modelled in 64 bits, one
-// direction six times the others:
-// 8 x 1200 5.8e-4 one by one and 8.7e-3 in twos, 32 x 1200 2.3e-4 and 5.9e-4,
-// 64 x 1200 2.3e-4 and 3.6e-4).  A single row has nothing off the diagonal.
+// and its rounding does not average out.  Roundings modelled in 64 bits, n =
+// 1200 and one direction f times the others, one by one and in twos:
+//   rows      8               64              96              128
+//   f =   6   4.3e-4, 7.2e-3  2.9e-4, 5.6e-4  3.2e-4, 4.6e-4  3.4e-4, 4.0e-4
+//   f =  30   5.9e-4, 1.1e-3  2.1e-4, 5.6e-4  2.4e-4, 5.3e-4  2.6e-4, 4.7e-4
+//   f = 100   1.7e-3, 2.3e-3  2.3e-4, 5.3e-4  1.7e-4, 4.2e-4  1.9e-4, 3.8e-4
+// From 128 rows on twos are at most about twice as far off.  Below, one by one
+// costs 8 to 21 % (24 x 64 x 3000 154 -> 167 us, 60 x 120 x 8000 996 -> 1203).
+// A single row has nothing off the diagonal.
 inline bool thin(const Mat& m)
 {
     const int32_t side = m.R < m.C ? m.R : m.C;
-    return side > 1 && side < 64;
+    return side > 1 && side < 128;
 }
 
 // Members that take their steps in launches of their own, whether some of

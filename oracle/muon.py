@@ -61,6 +61,19 @@ def chain_of(steps, pairs, full=False):
     return [2] + [1] * (steps - 2)
 
 
+def exponent(U, eps):
+    """The library holds a matrix whose norm is below eps as 2^e X, with
+    2^e |X| in [1/2, 1)."""
+    n = np.sqrt(np.sum(np.asarray(U, np.float64) ** 2))
+    t = n / (n + np.float64(np.float32(eps)))
+    return max(0, -int(np.frexp(t)[1])) if t > 0 else 0
+
+
+def shift_of(a, b, c):
+    """Bits a step takes from e: it multiplies s <= 1/4 by at most 2^t."""
+    return max(0, int(np.ceil(np.log2(abs(a) + abs(b) / 16 + abs(c) / 256))))
+
+
 def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False,
             drop=None):
     """One matrix, with the library's fp16 roundings and exact sums; `pairs`:
@@ -100,7 +113,8 @@ def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False,
         return (times(R, S, what) + d[:, None] * (S[0] + S[1]) +
                 (R[0] + R[1]) * f[None] + np.diag(d * f))
 
-    X = start(U, eps)
+    e = exponent(U, eps)
+    X = start(U, eps) * 2.0 ** e
     rows = rows_of(coef, steps)
     k = 0
     for many in chain_of(steps, pairs, full):
@@ -109,6 +123,10 @@ def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False,
         E = None
         for q in range(many):
             a, b, c = rows[k]
+            e1 = max(e - shift_of(a, b, c), 0)
+            a, b, c = (a * 2.0 ** (e1 - e), b * 2.0 ** (e1 - 3 * e),
+                       c * 2.0 ** (e1 - 5 * e))
+            e = e1
             k += 1
             M = b * whole(A) + c * product(A, A, "poly")
             C = square(M + a * np.eye(len(M)))
@@ -116,7 +134,7 @@ def rounded(U, steps=5, coef=COEF, eps=1e-7, full=False, pairs=False,
             if q + 1 < many:
                 A = square(product(square(product(C, A)), C))
         X = E[1][:, None] * (x[0] + x[1]) + times(E[0], x, "update")
-    return X
+    return X * 2.0 ** -e
 
 
 def scale(mode, rows, cols):

@@ -379,3 +379,19 @@ def test_rounded_oracle_of_one_step(shape, full, u):
         d5 = [np.linalg.norm(OM.rounded(U, full=f) - OM.orthogonalize(U))
               for f in (False, True)]
         assert d5[1] < d5[0] / 2 ** 8
+
+
+@pytest.mark.parametrize("full", [False, True])
+@pytest.mark.parametrize("size", [1e-8, 1e-10, 1e-14, 1e-20])
+def test_norms_below_eps_keep_their_bits(size, full):
+    """A matrix far below eps stays as exact as its representation: the steps
+    multiply it by a and little else."""
+    U = np.random.default_rng(4).standard_normal((64, 256))
+    U *= size / np.linalg.norm(U)
+    for steps in (5, 10):
+        e = OM.orthogonalize(U, steps)
+        r = OM.rounded(U, steps, full=full)
+        off = np.linalg.norm(r - e) / np.linalg.norm(e)
+        # where singular values have come near one, roundings are fast's own
+        big = np.linalg.norm(e) > 0.1
+        assert off <= (2e-3 if big and not full else 1e-6)

@@ -28,6 +28,14 @@
 //    R D + D D, the last three element by element.
 //  - In full precision (FULL) the squares and X^T are pairs too and every
 //    product is three: hi hi + hi lo + lo hi.
+//  - fp16 ends at 2^-24, which is 2^-34 of X.  A matrix whose norm is below eps
+//    starts at |X| = |U| / (|U| + eps) << 1 and would lose its bits there, so
+//    it is held as 2^e X, with 2^e |X| in [1/2, 1).  A step that can multiply
+//    it by g takes t = ceil(log2 g) from e, by way of C alone: with
+//    e' = max(e - t, 0) and A' = 2^2e A as the gram gives it
+//      2^(e' - e) C = 2^(e' - e) (a + b 2^-2e A' + c 2^-4e A' A')
+//    (zs_muon_plan.h: shift_of).  Matrices above eps / 2 have e = 0 and
+//    powers of two round nothing.
 //
 // Launches: the norm (or the momentum, which leaves U and its norm), X_0, and
 // three products a step, for all matrices of a call at once; small matrices
@@ -62,13 +70,14 @@ typedef _Float16 f16;
 typedef f16 f16x4 __attribute__((ext_vector_type(4)));
 typedef f16 f16x8 __attribute__((ext_vector_type(8)));
 
-constexpr float kScale = 1024.f, kUnscale = 1.f / 1024.f;
+constexpr int kScaleBits = 10;
+constexpr float kScale = 1 << kScaleBits, kUnscale = 1 / kScale;
 constexpr int64_t kTile = ZS_TILE;
 
 // Where its parts lie: E elements of X, S of a square, D of a diagonal, over
 // the whole stack, and in one matrix e, s and mp.
 //   Xd[2] hi, lo | Xt[2] hi (lo) | kSquares m x m matrices, each hi (lo)
-//   | their diagonals | partial sums (double)
+//   | their diagonals | e (int32) of each matrix | partial sums (double)
 // The momentum kernel's U (fp32) lies where Xd[1] will be: it is read by the
 // normalising kernel, before the first update writes there.
 constexpr int kSquares = 4;
@@ -78,9 +87,9 @@ template <bool FULL>
 struct Region {
     char* ws;
     int32_t rp, cp, mp;                 // padded sides, the smaller one
-    int64_t e, s, E, S, D;
+    int64_t e, s, E, S, D, exps;
     __host__ __device__ Region(char* w, int32_t R, int32_t C, int32_t batch)
-        : ws(w)
+        : ws(w), exps(((int64_t)batch + 1) / 2 * 8)
     {
         rp = padded(R);
         cp = padded(C);
@@ -104,9 +113,13 @@ struct Region {
     {
         return x_bytes() + (FULL ? 4 : 2) * kSquares * S;
     }
-    __host__ __device__ int64_t parts_off() const
+    __host__ __device__ int64_t exp_off() const
     {
         return d_off() + 4 * kSquares * D;
+    }
+    __host__ __device__ int64_t parts_off() const
+    {
+        return exp_off() + exps;
     }
     __device__ f16* square(int k) const
     {
@@ -115,6 +128,10 @@ struct Region {
     __device__ float* diag(int k) const
     {
         return (float*)(ws + d_off() + 4 * k * D);
+    }
+    __device__ int32_t* exponent() const
+    {
+        return (int32_t*)(ws + exp_off());
     }
     __host__ __device__ double* parts() const
     {
@@ -438,6 +455,21 @@ __device__ __forceinline__ void split(float x, f16& hi, f16& lo)
     lo = (f16)(x - (float)hi);
 }
 
+// What a matrix of this norm is multiplied by, and its e (at the top).  One
+// with a NaN or an infinity is NaN everywhere.
+__device__ __forceinline__ double start_scale(double norm, float eps, int& e)
+{
+    e = 0;
+    if (!(norm < HUGE_VAL))
+        return NAN;
+    if (norm > 0) {
+        int x;
+        frexp(norm / (norm + (double)eps), &x);
+        e = x < 0 ? -x : 0;
+    }
+    return ldexp((double)kScale / (norm + (double)eps), e);
+}
+
 // Workgroup = one 64 x 64 tile of one padded matrix: read U, scale, write Xd
 // (hi, lo) and, through LDS, Xt.
 template <bool BF16, bool FULL>
@@ -459,10 +491,10 @@ __global__ __launch_bounds__(kNT) void ns_init_kernel(InitArgs a)
     for (int i = threadIdx.x; i < nparts; i += kNT)
         sum += parts[i];
     sum = block_sum(sum);
-    const double norm = sqrt(sum);
-    // a matrix with a NaN or an infinity is NaN everywhere
-    const double inv =
-        norm < HUGE_VAL ? (double)kScale / (norm + (double)a.eps) : NAN;
+    int ex;
+    const double inv = start_scale(sqrt(sum), a.eps, ex);
+    if (bid == 0 && threadIdx.x == 0)
+        w.exponent()[b] = ex;
     const Source& s = a.src[p];
     const int tx = threadIdx.x % 16 * 4, ty = threadIdx.x / 16;
 #pragma unroll
@@ -531,6 +563,8 @@ struct GemmArgs {
     };
     int32_t parity;                     // which of the two X is read
     int8_t sp, sq, so;                  // squares: operands and result
+    // kPoly: shifts before and after its step; the last update: all of them
+    int16_t shift, shift1;
     float a, b, c;
     float dec;                          // 1 - lr*wd
 };
@@ -609,19 +643,19 @@ __device__ __forceinline__ void store_cols(f16* o, const f16x8 (&v)[FJ],
     }
 }
 
-// The last update's results v[0..3], times kScale, at row j and columns
+// The last update's results v[0..3], times 2^-un, at row j and columns
 // i .. i+3 of matrix b (i a multiple of 4; columns past the last are not
 // there), to the caller's matrix.
 template <int EPI>
 __device__ __forceinline__ void finish_out(const OutMat& om, const Mat& m,
                                            uint32_t b, int j, int i,
-                                           const float* v)
+                                           const float* v, int un)
 {
     const int64_t o = b * om.batch + j * om.row + i;
     float x[4];
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        x[q] = v[q] * kUnscale;
+        x[q] = ldexpf(v[q], un);
     if constexpr (EPI == kOutF32) {
         float* const op = static_cast<float*>(om.o) + o;
         if (om.vec) {
@@ -652,7 +686,7 @@ __device__ __forceinline__ void finish_out(const OutMat& om, const Mat& m,
 __device__ __forceinline__ void finish_step(const GemmArgs& a, int p,
                                             const Mat& m, uint32_t b, int j,
                                             int i, bool vec4, const float* v,
-                                            f32x4 st)
+                                            int un, f32x4 st)
 {
     const StepMat& sm = a.st[p];
     const int64_t e = ((int64_t)b * m.R + j) * m.C + i;
@@ -673,7 +707,7 @@ __device__ __forceinline__ void finish_step(const GemmArgs& a, int p,
             const int64_t eq = e + q;
             float* const s1 = sm.state + eq / kTile * 3 * kTile + eq % kTile;
             const float t = *s1 * a.dec;
-            const float u = sm.s * (vv[q] * kUnscale);
+            const float u = sm.s * ldexpf(vv[q], un);
             const float x = t - u;
             *s1 = x;
             const uint16_t h = (uint16_t)to_bf16(x);
@@ -875,6 +909,8 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     const int ib = i0 + wi * FI * 16 + g * 8;
     const int jb = j0 + (wj * 16 + l16) * FJ;
     const bool vec4 = m.C % 4 == 0;             // kStep's state by fours
+    const int ex =
+        EPI == kPoly || EPI > kUpdate ? w.exponent()[b] : 0;
     f16x8 inh[kRing], inl[kRing], inh2[kRing], inl2[kRing];
     f32x4 inS[kRing][2];
     auto fetch = [&](int u) {
@@ -1067,6 +1103,10 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
     }
 
     // Epilogue, from registers.
+    const int e0 = max(ex - a.shift, 0), e1 = max(ex - a.shift1, 0);
+    const float pa = ldexpf(a.a, e1 - e0), pb = ldexpf(a.b, e1 - 3 * e0),
+                pc = ldexpf(a.c, e1 - 5 * e0);
+    const int un = -kScaleBits - e0;
     float* const dout = w.diag(a.so) + (int64_t)b * mp;
     f16* const out =
         kTri ? w.square(a.so) + b * w.s : w.xd(1 - a.parity) + b * w.e;
@@ -1106,7 +1146,7 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                     if constexpr (FULL)
                         r = r + (float)inl[n][q];
                     if constexpr (EPI == kPoly) {
-                        v[q] = a.b * r + a.c * (d + (dii + dj) * r);
+                        v[q] = pb * r + pc * (d + (dii + dj) * r);
                     } else {
                         float t = (float)inh2[n][q];
                         if constexpr (FULL)
@@ -1131,7 +1171,7 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                             const float dd =
                                 EPI == kGram ? d : d + dii * dj;
                             dout[j] = EPI == kPoly
-                                          ? a.a + (a.b * dj + a.c * dd)
+                                          ? pa + (pb * dj + pc * dd)
                                           : dd;
                             v[q] = 0;
                         }
@@ -1160,17 +1200,17 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
                         for (int q = 0; q < 4; ++q) {
                             const float t = inS[n][h][q] * a.dec;
                             const float x =
-                                a.st[p].s * (v[4 * h + q] * kUnscale);
+                                a.st[p].s * ldexpf(v[4 * h + q], un);
                             st[q] = t - x;
                         }
                     }
                     if (j < m.R && i + 4 * h < m.C) {
                         if constexpr (EPI == kStep)
                             finish_step(a, p, m, b, j, i + 4 * h, vec4,
-                                        v + 4 * h, st);
+                                        v + 4 * h, un, st);
                         else
                             finish_out<EPI>(a.out[p], m, b, j, i + 4 * h,
-                                            v + 4 * h);
+                                            v + 4 * h, un);
                     }
                 }
             }
@@ -1221,6 +1261,7 @@ struct SmallArgs {
     int32_t steps;
     float eps, dec;
     float coef[ZS_NS_MAX_STEPS][3];
+    int16_t shift[ZS_NS_MAX_STEPS];     // each step's by itself
 };
 static_assert(sizeof(SmallArgs) <= 4096, "kernel arguments");
 
@@ -1323,10 +1364,8 @@ __global__ __launch_bounds__(SM::kThreads) void ns_small_kernel(SmallArgs a)
     sum = 0;
     for (int w = 0; w < SM::NW; ++w)
         sum += red[w];
-    const double norm = sqrt(sum);
-    // a matrix with a NaN or an infinity is NaN everywhere
-    const double inv =
-        norm < HUGE_VAL ? (double)kScale / (norm + (double)a.eps) : NAN;
+    int ex;
+    const double inv = start_scale(sqrt(sum), a.eps, ex);
 #pragma unroll
     for (int i = 0; i < UFI; ++i)
 #pragma unroll
@@ -1336,8 +1375,11 @@ __global__ __launch_bounds__(SM::kThreads) void ns_small_kernel(SmallArgs a)
                 x[i][j][q] = (float)((double)x[i][j][q] * inv);
 
     for (int step = 0; step < a.steps; ++step) {
-        const float ca = a.coef[step][0], cb = a.coef[step][1],
-                    cc = a.coef[step][2];
+        const int e1 = max(ex - a.shift[step], 0);
+        const float ca = ldexpf(a.coef[step][0], e1 - ex),
+                    cb = ldexpf(a.coef[step][1], e1 - 3 * ex),
+                    cc = ldexpf(a.coef[step][2], e1 - 5 * ex);
+        ex = e1;
         // X's operands
 #pragma unroll
         for (int i = 0; i < UFI; ++i)
@@ -1456,7 +1498,7 @@ __global__ __launch_bounds__(SM::kThreads) void ns_small_kernel(SmallArgs a)
                 const int n = ui + 16 * i + 4 * g + q, r = uj + 16 * j + l16;
                 if (n >= N || r >= M)
                     continue;
-                const float v = x[i][j][q] * kUnscale;
+                const float v = ldexpf(x[i][j][q], -kScaleBits - ex);
                 const int64_t row = tall ? n : r, col = tall ? r : n;
                 if (a.epi == kStep) {
                     const StepMat& o = a.st[p];
@@ -1631,11 +1673,14 @@ int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Part& part,
 {
     const Tiles& t = part.tiles;
     a.parity = 0;
+    a.shift1 = 0;
     int rc = ZS_OK;
     auto poly = [&](int k, Square out) {
         a.a = ns.coef[k][0];
         a.b = ns.coef[k][1];
         a.c = ns.coef[k][2];
+        a.shift = a.shift1;
+        a.shift1 = (int16_t)(a.shift1 + shift_of(ns.coef[k]));
         a.sp = a.sq = kA;
         a.so = out;
         if (!rc) rc = launch_product<kPoly, FULL>(a, t.square.tile, s);
@@ -1659,6 +1704,8 @@ int run_products(GemmArgs& a, const zs_newton_schulz& ns, const Part& part,
         }
         k += two ? 2 : 1;
         a.sp = two ? kT : kC;
+        if (k == ns.steps)
+            a.shift = a.shift1;
         if (!rc)
             rc = k < ns.steps
                      ? launch_product<kUpdate, FULL>(a, t.update.tile, s)
@@ -1775,9 +1822,11 @@ int run_small(const Work& w, Group& g, int* at, hipStream_t s)
         a.steps = w.ns->steps;
         a.eps = w.ns->eps;
         a.dec = w.dec;
-        for (int k = 0; k < ZS_NS_MAX_STEPS; ++k)
+        for (int k = 0; k < ZS_NS_MAX_STEPS; ++k) {
             for (int q = 0; q < 3; ++q)
                 a.coef[k][q] = k < a.steps ? w.ns->coef[k][q] : 0;
+            a.shift[k] = (int16_t)shift_of(a.coef[k]);
+        }
         int rc;
         if (kind == 1) {
             rc = launch_small<Small64<FULL>, FULL>(a, s);

@@ -189,6 +189,23 @@ Choice choose_tile(const Group& g)
     return best;
 }
 
+// Bits that a step takes from the exponent e of a matrix held as 2^e X, so that
+// 2^e X stays below one: it multiplies a singular value s by at most
+// |a| + |b| s^2 + |c| s^4, and from e = 2 on s is below 1/4.  (Where e is 1 X
+// is within two of its usual range, whatever the step takes.)  The usual
+// coefficients take 2 and multiply by 3.4; 3 a step would leave the low parts
+// of ten steps without their bits.
+inline int shift_of(const float (&coef)[3])
+{
+    const double g = std::fabs((double)coef[0]) +
+                     std::fabs((double)coef[1]) / 16 +
+                     std::fabs((double)coef[2]) / 256;
+    int t = 0;
+    while (t < 128 && std::ldexp(1.0, t) < g)
+        ++t;
+    return t;
+}
+
 // Two steps taken together on the m x m side.  In units of m^3 flops with
 // r = n/m, a symmetric product being 1:
 //   one by one   A = X X^T (r), C = a + b A + c A A (1), X <- C X (2 r),

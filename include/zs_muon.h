@@ -41,28 +41,43 @@ extern "C" {
  *
  * Precision (zs_newton_schulz.precision).  The products run on the matrix
  * cores from fp16 operands with fp32 sums; fp16 carries 11 significant bits
- * where bf16 has 8, and a fixed scale keeps every value that the iteration
- * can hold inside its range.
- *   ZS_NS_FAST  one product each.  X itself is kept in 22 bits (a pair of
- *     fp16 values) and enters the a X term and the diagonals of A and of
- *     b A + c A A enter exactly, so that rounding does not pile up from
- *     step to step: about 1e-3 of the result's norm after five standard
- *     steps, 3e-3 at most in the matrices of 32 rows and columns or more
- *     that were tried, with directions a thousand times as strong as others
- *     and of low rank, where rounding X alone to bf16 loses a third of it.
- *     Between fewer rows that are all but parallel (one direction a hundred
- *     times the others) roundings do not average out: 5e-3, and at a
- *     thousand times 3e-2.
- *   ZS_NS_FULL  three products each (high x high, high x low, low x high),
- *     22 bits throughout: about 1e-5 or less, what fp32 products give.
+ * where bf16 has 8.
+ *   ZS_NS_FAST  one product each.  X itself is a pair of fp16 values and
+ *     enters the a X term whole, and the diagonals of A and of b A + c A A
+ *     are fp32.
+ *   ZS_NS_FULL  three products each (high x high, high x low, low x high) of
+ *     such pairs.
+ * The norm of the error over the result's, after five steps of the usual
+ * coefficients (3.4445, -4.7750, 2.0315), beside iterations by fp32 products:
+ *                                             FAST       FULL      fp32
+ *   noise; directions up to 30 times it       1e-3       2e-6      3e-6
+ *   noise of long tails                       2e-3       2e-6      3e-6
+ *   singular values 1/k and 1/k^2; directions
+ *     up to 100 times the others, 64 rows     2e-3       2e-5      2e-5
+ *     the same of 32 rows                     3e-3       1e-5      1e-5
+ *     the same of 2 rows                      5e-3       1e-5      1e-5
+ *   directions 1000 times the others, a mean
+ *     of 1000 sigma, low rank, 32 rows        7e-3       5e-5      2e-4
+ *     the same of 2 rows                      4e-2       5e-5      5e-5
+ * What a matrix does not have, or has far below its strongest direction, is
+ * roundings at first, and every step multiplies them by a, in any arithmetic.
+ * A matrix of rank 8 (64 x 256): at 6, 8 and 10 steps FAST 2e-2, 0.2 and more
+ * than the result itself, FULL 1e-4, 1e-3 and 1e-2, fp32 the same.  Matrices
+ * with a floor of noise are not of that kind (1.5e-3 at ten steps in FAST).
+ * Small values: what X holds is exact to 2^-23 of a value or to 2^-35,
+ * whichever is more.  An entry 10^6 times all others leaves them 6e-6 off in
+ * FULL (5 steps), 2e-5 (10), one 10^8 times all others 6e-6, 2e-4 (8) and 2e-3
+ * (10), where fp32 products give 2e-6 or less.  A matrix whose norm is below
+ * eps, and so |X| far below 1, is held times a power of two and loses
+ * nothing.
  * Two steps are taken together, as products of m x m matrices, where that is
  * less work: in fast precision the first two alone, and where m (the smaller
- * side) is 1 or at least 128.  It goes by the shapes of all matrices of a call, so a
- * matrix's result may differ by its rounding from one call's company to
- * another's.
- * Range: the entries of X, A and b A + c A A must stay below 63 in
- * magnitude, which singular values under 2 and the usual coefficients never
- * leave; past it the result is not finite. */
+ * side) is 1 or at least 128.  It goes by the shapes of all matrices of a
+ * call, so a matrix's result may differ by its rounding from one call's
+ * company to another's.
+ * Range: the entries of X, A and b A + c A A (off the diagonal) must stay
+ * below 63 in magnitude, which singular values under 2 and the usual
+ * coefficients never leave; past it the result is not finite. */
 #define ZS_NS_FAST 0
 #define ZS_NS_FULL 1
 #define ZS_NS_MAX_STEPS 16

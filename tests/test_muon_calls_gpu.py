@@ -11,7 +11,7 @@ import pytest
 import torch
 
 import zero_sharded_optimizer_shard_amd as zs
-from muon_bounds import full_bound, rel
+from muon_bounds import arithmetic, full_bound, rel
 from oracle import muon as OM
 
 pytestmark = pytest.mark.gpu
@@ -112,3 +112,73 @@ def test_step_of_a_momentum_below_eps(shape, precision):
                     scale="none", precision=precision, workspace=ws)
     got = -state[:, 0].reshape(-1)[:n].view(shape)
     check((m * np.float32(0.5)).reshape(shape), got, precision)
+
+
+def directions(rng, m, n, k, f):
+    """k directions f times the strongest of the noise below them."""
+    q = lambda a, b: np.linalg.qr(rng.standard_normal((a, b)))[0]  # noqa
+    w = rng.standard_normal((m, n))
+    return w / np.linalg.norm(w, 2) + f * q(m, k) @ q(n, k).T
+
+
+def decay(rng, m, n, p):
+    """Singular values k^-p."""
+    q = lambda a, b: np.linalg.qr(rng.standard_normal((a, b)))[0]  # noqa
+    return (q(m, m) * np.arange(1., m + 1) ** -p) @ q(n, m).T
+
+
+def lowrank(rng, m, n, k):
+    return rng.standard_normal((m, k)) @ rng.standard_normal((k, n))
+
+
+def entry(rng, m, n, size):
+    U = rng.standard_normal((m, n))
+    U[3, 5] = size
+    return U
+
+
+# kind, and the header's figures for five steps: fast, full
+SPECTRA = {
+    "noise": (lambda r: r.standard_normal((256, 1024)), 1e-3, 2e-6),
+    "noise 64": (lambda r: r.standard_normal((64, 128)), 1e-3, 2e-6),
+    "long tails": (lambda r: r.standard_t(2, (300, 70)), 2e-3, 2e-6),
+    "8 x 30": (lambda r: directions(r, 256, 1024, 8, 30), 1e-3, 2e-6),
+    "8 x 100": (lambda r: directions(r, 256, 3000, 8, 100), 2e-3, 2e-5),
+    "8 x 100, 64": (lambda r: directions(r, 64, 300, 8, 100), 2e-3, 2e-5),
+    "1/k": (lambda r: decay(r, 256, 3000, 1), 2e-3, 2e-5),
+    "1/k^2": (lambda r: decay(r, 64, 300, 2), 2e-3, 2e-5),
+    "8 x 100, 32": (lambda r: directions(r, 32, 1200, 8, 100), 3e-3, 1e-5),
+    "1 x 100, 2": (lambda r: directions(r, 2, 1200, 1, 100), 5e-3, 1e-5),
+    "8 x 1000, 32": (lambda r: directions(r, 32, 1200, 8, 1000), 7e-3, 5e-5),
+    "8 x 1000, 64": (lambda r: directions(r, 64, 1200, 8, 1000), 7e-3, 5e-5),
+    "mean": (lambda r: 1000 + r.standard_normal((256, 2048)), 7e-3, 5e-5),
+    "rank 8": (lambda r: lowrank(r, 64, 256, 8), 7e-3, 5e-5),
+    "rank 8, tall": (lambda r: lowrank(r, 1024, 256, 8), 7e-3, 5e-5),
+    "1 x 1000, 2": (lambda r: directions(r, 2, 1200, 1, 1000), 4e-2, 5e-5),
+    "entry 1e6": (lambda r: entry(r, 256, 1024, 1e6), 2e-3, 1e-5),
+    "entry 1e8": (lambda r: entry(r, 256, 1024, 1e8), 2e-3, 1e-5),
+}
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("kind", SPECTRA)
+def test_accuracy_by_kind_of_matrix(kind, precision):
+    """The header's figures at five steps.  At 5 to 10: twice the oracle's
+    model, and in full precision fp32 arithmetic of which the first step's
+    grows by a in each of the others where the matrix has nothing."""
+    make, fast, full = SPECTRA[kind]
+    U = make(gen(50)).astype(np.float32)
+    x = torch.from_numpy(U).cuda().expand(8, *U.shape)
+    for steps in (5, 6, 8, 10):
+        o = run([x], [torch.empty(x.shape, device="cuda")], precision,
+                steps=steps)[0]
+        e = OM.orthogonalize(U, steps)
+        t = bound(U, e, precision, F32, steps)
+        if precision == "full":
+            t += arithmetic(U.shape) * OM.COEF[0] ** (steps - 1) / \
+                np.linalg.norm(e)
+        got = rel(o[0].cpu().numpy(), e)
+        assert got <= t, (steps, got, t)
+        if steps == 5:
+            assert got <= (full if precision == "full" else fast), got
+        assert torch.equal(o[7], o[0])

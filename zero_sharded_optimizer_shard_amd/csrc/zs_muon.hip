@@ -18,7 +18,8 @@
 //  - X is a pair (hi, lo), 22 bits; products use hi, the term a X uses both.
 //    Rounded to fp16 alone, the rounding of each step would enter the null
 //    directions of a matrix of low rank and grow by a = 3.4 a step (rank 8 of
-//    1024: 4e-2 of the result's norm against 3e-4).
+//    1024: 4e-2 of the result's norm against 3e-4).  What the products round
+//    there grows all the same (zs_muon.h has what is left).
 //    What is left is mostly hi's rounding in the gram (512 x 1024: 4.6e-4 of
 //    5.7e-4; C's 2.2e-4, A's 2.1e-4, the update's 1.3e-4), which two more
 //    products would take away: a quarter of the work three times over.

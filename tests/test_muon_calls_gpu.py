@@ -13,6 +13,8 @@ import torch
 import zero_sharded_optimizer_shard_amd as zs
 from muon_bounds import arithmetic, full_bound, rel
 from oracle import muon as OM
+from test_muon_gpu import Case
+from test_muon_products_gpu import exact
 
 pytestmark = pytest.mark.gpu
 
@@ -182,3 +184,201 @@ def test_accuracy_by_kind_of_matrix(kind, precision):
         if steps == 5:
             assert got <= (full if precision == "full" else fast), got
         assert torch.equal(o[7], o[0])
+
+
+# small matrices (one launch) and others, wide and tall, columns a multiple of
+# four and not
+SHAPES = [(60, 72), (250, 33), (66, 200), (200, 72), (140, 150), (70, 333)]
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("xt,ot", [(BF16, BF16), (BF16, F32), (F32, BF16)],
+                         ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: "%dx%d" % s)
+def test_types(shape, xt, ot, precision):
+    x = torch.from_numpy(gen(3).standard_normal(shape)).cuda().to(xt)
+    o = run([x], [torch.empty(shape, dtype=ot, device="cuda")], precision)[0]
+    check(x.double().cpu().numpy(), o, precision)
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("gap", [24, 23])
+@pytest.mark.parametrize("pitch,off", [(0, 0), (5, 0), (8, 0), (3, 1), (8, 1),
+                                       (64, 4)])
+def test_strides_and_alignment(pitch, off, gap, dtype, precision):
+    """Stacks in wider buffers: every base, pitch and distance of the members
+    that decides between loads by fours and one by one, in and out apart."""
+    b = 2
+    for r, c in SHAPES[1:]:
+        U = gen(r).standard_normal((b, r, c))
+
+        def place(fill, pitch, off):
+            step = r * (c + pitch) + gap
+            buf = torch.full((off + b * step,), fill, dtype=dtype,
+                             device="cuda")
+            return buf, torch.as_strided(buf, (b, r, c),
+                                         (step, c + pitch, 1), off)
+
+        plain = place(0.0, 0, 0)[1] if gap % 4 == 0 else \
+            torch.empty(b, r, c, dtype=dtype, device="cuda")
+        for xs, os in ((True, False), (False, True), (True, True)):
+            xb, x = place(3.0, pitch, off)
+            ob, o = place(5.0, pitch, off)
+            if not xs:
+                x = torch.empty(b, r, c, dtype=dtype, device="cuda")
+            x.copy_(torch.from_numpy(U))
+            if not os:
+                o = plain
+            keep, kx = ob.clone(), x.clone()
+            run([x], [o], precision)
+            assert torch.equal(x, kx)
+            if xs and not os:           # the first of the three
+                for k in range(b):
+                    check(x[k].double().cpu().numpy(), o[k], precision)
+                want = o.clone()
+            assert torch.equal(o, want)
+            if os:
+                torch.as_strided(keep, o.shape, o.stride(), off).copy_(o)
+                assert torch.equal(ob, keep)    # nothing else was written
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("shape", [(70, 300), (300, 150), (2050, 2056)],
+                         ids=lambda s: "%dx%d" % s)
+@pytest.mark.parametrize("size", [1e-30, 1e-18, 1e15, 1e30])
+def test_any_magnitude(size, shape, precision):
+    """The norm is taken in 64 bits by the kernels of large matrices too."""
+    U = gen(4).standard_normal(shape).astype(np.float32) * np.float32(size)
+    eps = 1e-7 if size > 1 else size * 1e-3
+    x = torch.from_numpy(U).cuda()
+    o = run([x], [torch.empty_like(x)], precision, eps=eps)[0]
+    if shape[0] < 1000:
+        check(U, o, precision, eps=eps)
+        return
+    # the formulas in 64 bits on the GPU; the bound from a quarter of the
+    # sides, whose errors are the larger ones
+    V = U[:shape[0] // 4, :shape[1] // 4]
+    t = bound(V, OM.orthogonalize(V, eps=eps), precision, eps=eps)
+    e = exact(x, eps=eps)
+    assert ((o.double() - e).norm() / e.norm()).item() <= t
+
+
+def test_norm_of_many_parts():
+    """More partial sums than a workgroup adds on its way, at sizes whose
+    squares fp32 does not hold."""
+    x = torch.randn(4104, 4100, device="cuda",
+                    generator=torch.Generator("cuda").manual_seed(5))
+    want = run([x], [torch.empty_like(x)], "fast", steps=1, coef=(1., 0., 0.))
+    e = x.double() / (x.double().norm() + 1e-7)
+    t = 2.0 ** -21
+    assert (want[0].double() - e).norm() <= t * e.norm()
+    y = x * 2.0 ** 100
+    got = run([y], [torch.empty_like(y)], "fast", steps=1, coef=(1., 0., 0.))
+    assert (got[0].double() - e).norm() <= t * e.norm()
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("dtype", [BF16, F32], ids=lambda t: str(t)[6:])
+@pytest.mark.parametrize("shape", [(3, 60, 72), (3, 130, 300), (3, 400, 70),
+                                   (24, 256, 1500)],
+                         ids=lambda s: "%dx%dx%d" % s)
+def test_in_place(shape, dtype, precision):
+    x = torch.from_numpy(gen(6).standard_normal(shape)).cuda().to(dtype)
+    want = run([x], [torch.empty_like(x)], precision)[0]
+    run([x], [x], precision)
+    assert torch.equal(x, want)
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("shape", [(60, 72), (150, 200), (24, 256, 1500)],
+                         ids=str)
+def test_captured_calls(shape, precision):
+    """Replays on new inputs and a spoilt workspace, eager work between."""
+    rng = gen(7)
+    xs = [torch.from_numpy(rng.standard_normal(shape)).cuda().float()
+          for _ in range(4)]
+    want = [run([x], [torch.empty_like(x)], precision)[0] for x in xs]
+    x, o = xs[0].clone(), torch.empty_like(xs[0])
+    ws = torch.empty(zs.zs_orthogonalize_workspace([x], precision),
+                     dtype=torch.uint8, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g):
+        zs.zs_orthogonalize([x], [o], workspace=ws, precision=precision)
+    for k in (0, 1, 2, 3, 0):
+        x.copy_(xs[k])
+        ws.fill_(255)
+        o.fill_(9)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(o, want[k])
+        assert torch.equal(run([x], [torch.empty_like(x)], precision)[0], o)
+
+
+@pytest.mark.parametrize("shape", [(60, 72), (900, 1100), (24, 256, 1500)],
+                         ids=str)
+def test_two_calls_at_once(shape):
+    """Two streams, a workspace each, one call in each precision."""
+    xs = [torch.from_numpy(gen(8 + k).standard_normal(shape)).cuda().float()
+          for k in range(2)]
+    want = [run([x], [torch.empty_like(x)], p)[0]
+            for x, p in zip(xs, PRECISIONS)]
+    ws = [torch.empty(zs.zs_orthogonalize_workspace([x], p),
+                      dtype=torch.uint8, device="cuda")
+          for x, p in zip(xs, PRECISIONS)]
+    outs = [torch.empty_like(x) for x in xs]
+    streams = [torch.cuda.Stream() for _ in xs]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for x, o, w, st, p in zip(xs, outs, ws, streams, PRECISIONS):
+            zs.zs_orthogonalize([x], [o], workspace=w, stream=st, precision=p)
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o, w)
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("shape", [(256, 64), (512, 700), (24, 256, 1500)],
+                         ids=str)
+def test_same_bits_every_time(shape, precision):
+    x = torch.from_numpy(gen(9).standard_normal(shape)).cuda().float()
+    a = run([x], [torch.empty_like(x)], precision)[0]
+    for _ in range(3):
+        assert torch.equal(run([x], [torch.empty_like(x)], precision)[0], a)
+
+
+@pytest.mark.parametrize("layout", ["slices", "tiled"])
+@pytest.mark.parametrize("W", [1, 3, 8])
+def test_step_in_full_precision(W, layout):
+    """Five steps of small matrices and others together."""
+    c = Case([(130, 70), (70, 340), (3, 40, 36), (1, 515), (513, 1),
+              (2, 90, 91)], W, layout, seed=60 + W)
+    d = c.device()
+    c.step(d, "full", nesterov=W != 3)
+    c.check(d, "full", nesterov=W != 3)
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+def test_steps_at_once(precision):
+    """Two owners' steps on two streams, a workspace each."""
+    cs = [Case([(130, 270), (3, 40, 36), (200, 150)], 2, "tiled",
+               seed=70 + k) for k in range(2)]
+    want, ds = [], []
+    for c in cs:
+        d = c.device()
+        for _ in range(3):
+            c.step(d, precision)
+        want.append(d)
+        ds.append(c.device())
+    ws = [torch.empty(zs.zs_muon_workspace(c.lay, c.tensors(), precision),
+                      dtype=torch.uint8, device="cuda") for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for c, d, w, st in zip(cs, ds, ws, streams):
+            c.step(d, precision, ws=w, stream=st)
+    torch.cuda.synchronize()
+    for a, b in zip(want, ds):
+        assert torch.equal(a.state, b.state)
+        assert torch.equal(a.shard, b.shard) and torch.equal(a.flat, b.flat)

@@ -31,12 +31,12 @@ def ids(c):
                                       P.STEP: "step"}[c[1]], *c[2])
 
 
-def exact(U, steps=5):
+def exact(U, steps=5, eps=1e-7):
     """The formulas in 64 bits on the GPU, of one matrix there."""
     U = U.double()
     if U.shape[0] > U.shape[1]:
-        return exact(U.t().contiguous(), steps).t()
-    X = U / (U.norm() + np.float64(np.float32(1e-7)))
+        return exact(U.t().contiguous(), steps, eps).t()
+    X = U / (U.norm() + np.float64(np.float32(eps)))
     a, b, c = OM.COEF
     for _ in range(steps):
         A = X @ X.t().contiguous()

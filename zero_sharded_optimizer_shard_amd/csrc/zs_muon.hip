@@ -12,8 +12,8 @@
 // caller has it and Xt [cols][rows].
 //
 // Numbers.  Operands are fp16 times 2^10: |X| <= 1, so entries reach from
-// 2^10 down to the mean 2^10 / sqrt(rows cols) = 0.07 of the largest shapes,
-// in fp16's normal range.  Sums are fp32.  What is rounded to fp16, and what
+// 2^10 down to the mean 2^10 / sqrt(rows cols) = 0.022 of the largest shapes
+// (2^31 elements), in fp16's normal range.  Sums are fp32.  What is rounded to fp16, and what
 // is not:
 //  - X is a pair (hi, lo), 22 bits; products use hi, the term a X uses both.
 //    Rounded to fp16 alone, the rounding of each step would enter the null
@@ -35,14 +35,14 @@
 //    it by g takes t = ceil(log2 g) from e, by way of C alone: with
 //    e' = max(e - t, 0) and A' = 2^2e A as the gram gives it
 //      2^(e' - e) C = 2^(e' - e) (a + b 2^-2e A' + c 2^-4e A' A')
-//    (zs_muon_plan.h: shift_of).  Matrices above eps / 2 have e = 0 and
-//    powers of two round nothing.
+//    (zs_muon_plan.h: shift_of).  Matrices of norm eps and above have e = 0,
+//    and powers of two round nothing.
 //
 // Launches: the norm (or the momentum, which leaves U and its norm), X_0, and
 // three products a step, for all matrices of a call at once; small matrices
 // take all steps in one launch.  What bounds them on MI355X: from 4096 a side
-// on the matrix cores, which are busy 52-64 % of the cycles of a square's
-// launch and 42-57 % of an update's, whose epilogue moves ten bytes an element
+// on the matrix cores, which are busy 52-66 % of the cycles of a square's
+// launch and 43-57 % of an update's, whose epilogue moves ten bytes an element
 // (more with the master) with nothing beside it; up to about 1024 a side the
 // launches themselves, each 5-7 us plus 0.18 us for 64 k (0.5 us in full
 // precision).
@@ -592,9 +592,11 @@ struct Shape {
 };
 
 // Two waves a SIMD taking turns (the loop is described in the kernel): the
-// large tile feeds the matrix cores best (4096^3: 1300 TFLOP/s, 8192^3: 1380;
-// the 128 tile 1090 and 1100, the 64 tile 740), the smaller ones fill the
-// chip where there are few of the larger.
+// large tile feeds the matrix cores best (updates of 4096 x 4096 and 8192 x
+// 8192, epilogues with them: 147 and 1025 us, 0.93 and 1.07 PFLOP/s; the 192
+// tile 190 and 1312 us, the 128 tile 173 and 1165, the 64 tile 241 and 1830),
+// the smaller ones fill the chip where there are few of the larger (squares of
+// 4096: 136 tiles of 256 103 us, 256 of 192 85 us).
 typedef Shape<256, 2, 4, 2> Shape256;
 typedef Shape<192, 2, 4, 2> Shape192;
 typedef Shape<128, 2, 4, 2> Shape128;
@@ -1000,9 +1002,10 @@ __global__ __launch_bounds__(SH::kThreads) void ns_gemm_kernel(GemmArgs a)
         // ended by a barrier.  The loads for the next stage go out in the
         // stage's first slot; they have landed for every wave when it waits
         // for its own before the barrier that ends the last part's reads,
-        // the later half's one slot before the earlier half reads them.  They
-        // overwrite what was read two slots earlier or before, and each read
-        // has returned before the barrier that ends its slot.
+        // the later half's one slot before the earlier half reads them.  What
+        // they overwrite the later half may have read in the slot just before;
+        // those reads have returned, as every wave waits for its own before
+        // the barrier that ends their slot.
         auto stage = [&](const char* cur, char* other, int kt) {
             if (kt + 1 < total)
                 load(other);

@@ -64,6 +64,7 @@ extern "C" {
  * A matrix of rank 8 (64 x 256): at 6, 8 and 10 steps FAST 2e-2, 0.2 and more
  * than the result itself, FULL 1e-4, 1e-3 and 1e-2, fp32 the same.  Matrices
  * with a floor of noise are not of that kind (1.5e-3 at ten steps in FAST).
+ * Sums are fp32: those of sides of 2^22 add up to 1e-4.
  * Small values: what X holds is exact to 2^-23 of a value or to 2^-35,
  * whichever is more.  An entry 10^6 times all others leaves them 6e-6 off in
  * FULL (5 steps), 2e-5 (10), one 10^8 times all others 6e-6, 2e-4 (8) and 2e-3

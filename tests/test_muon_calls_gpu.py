@@ -382,3 +382,64 @@ def test_steps_at_once(precision):
     for a, b in zip(want, ds):
         assert torch.equal(a.state, b.state)
         assert torch.equal(a.shard, b.shard) and torch.equal(a.flat, b.flat)
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("shape", [(48, 72), (70, 300)],
+                         ids=lambda s: "%dx%d" % s)
+@pytest.mark.parametrize("far", ["members", "rows"])
+def test_offsets_past_32_bits(far, shape, precision):
+    """Members, and rows, more than 2^32 elements from the first."""
+    r, c = shape
+    U = gen(10).standard_normal((2, r, c)).astype(np.float32)
+    step, row = ((1 << 32) + 4, c) if far == "members" else \
+        ((1 << 20), (1 << 32) // (r - 1) + 4)
+
+    def place(dtype):
+        span = step + (r - 1) * row + c
+        return torch.as_strided(torch.empty(span, dtype=dtype, device="cuda"),
+                                (2, r, c), (step, row, 1))
+    x = place(BF16)
+    x.copy_(torch.from_numpy(U))
+    o = run([x], [place(BF16)], precision)[0]
+    for k in range(2):
+        check(x[k].double().cpu().numpy(), o[k], precision)
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+@pytest.mark.parametrize("shape", [(1, 1 << 22), (3, 1 << 22), (1 << 22, 2)],
+                         ids=lambda s: "%dx%d" % s)
+def test_longest_matrices(shape, precision):
+    """2^-18 is for sums of a few thousand; these have 2^17 additions of a
+    chain of 32 products, 2^-24 sqrt(2^17) = 2e-5 of the sum each as random
+    draws, which muon_bounds.arithmetic counts (1.5e-4)."""
+    U = gen(11).standard_normal(shape).astype(np.float32)
+    x = torch.from_numpy(U).cuda()
+    o = run([x], [torch.empty_like(x)], precision)[0]
+    e = OM.orthogonalize(U)
+    t = bound(U, e, precision) + arithmetic(U.shape)
+    assert rel(o.cpu().numpy(), e) <= t
+
+
+@pytest.mark.parametrize("precision", PRECISIONS)
+def test_largest_matrix(precision):
+    """The longest smaller side, one step: its products have sums as long as
+    any, so the bound of one row of such a matrix holds for it."""
+    n = 32768
+    g = torch.Generator(device="cuda").manual_seed(12)
+    x = torch.randn(n, n, generator=g, device="cuda").bfloat16()
+    o = run([x], [torch.empty_like(x)], precision, steps=1)[0]
+    # b A + c A A of X, row by row of the result: a few of them, in 64 bits
+    X = x.double()
+    X /= X.norm() + np.float64(np.float32(1e-7))
+    a, b, c = OM.COEF
+    for i in (0, 1, 191, 192, 20000, n - 1):
+        row = X[i:i + 1]
+        A = (X @ row.t().contiguous()).t().contiguous()     # row i of A
+        AA = (X @ (A @ X).t().contiguous()).t()
+        e = a * row + (b * A + c * AA) @ X
+        got = o[i:i + 1].double()
+        # one step rounds its update by 2^-11 of C's off-diagonal part, whose
+        # size beside a is below 1/100 here, and the result to bf16
+        t = 2.0 ** -8 + 2.0 ** -16
+        assert ((got - e).norm() / e.norm()).item() <= t

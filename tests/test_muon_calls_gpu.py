@@ -443,3 +443,58 @@ def test_largest_matrix(precision):
         # size beside a is below 1/100 here, and the result to bf16
         t = 2.0 ** -8 + 2.0 ** -16
         assert ((got - e).norm() / e.norm()).item() <= t
+
+
+@pytest.mark.parametrize("layout", ["slices", "tiled"])
+def test_step_behind_a_tensor_of_2_to_the_32(layout):
+    """A matrix whose state, gradients and outputs lie past 32 bits."""
+    r, c = 130, 72
+    n, W = r * c, 2
+    big = (1 << 32) + 1000
+    lay = zs.zs_layout_build_tensors([big, big, n, n], W, 0)
+    flat_numel, shard, tiles, _, buckets = lay.sizes()
+    b = buckets[1]
+    assert b.slice_numel < 2 * n and b.shard_off > 1 << 32
+    rng = gen(13)
+    G = rng.standard_normal((W, n))
+    P0, M0 = (rng.standard_normal(n).astype(np.float32) for _ in range(2))
+    nt = tiles - b.tile_off
+    state = torch.empty(tiles, 3, zs.ZS_TILE, device="cuda")
+    rows = torch.zeros(3, nt * zs.ZS_TILE)
+    rows[0, :n], rows[1, :n] = torch.from_numpy(P0), torch.from_numpy(M0)
+    state[b.tile_off:] = rows.view(3, nt, zs.ZS_TILE).transpose(0, 1).cuda()
+    g = torch.from_numpy(G).to(BF16)
+    if layout == "tiled":
+        grads = torch.zeros(nt, W, zs.ZS_TILE, dtype=BF16)
+        for s in range(W):
+            row = torch.zeros(nt * zs.ZS_TILE, dtype=BF16)
+            row[:n] = g[s]
+            grads[:, s] = row.view(nt, zs.ZS_TILE)
+        grads, stride = grads.cuda(), 0
+    else:                               # rows of whole-shard gradients
+        stride = shard
+        whole = torch.empty(W * shard, dtype=BF16, device="cuda")
+        grads = whole[b.shard_off:]
+        for s in range(W):
+            grads[s * stride:s * stride + n] = g[s].cuda()
+    p = torch.empty(shard, dtype=BF16, device="cuda")
+    flat = torch.empty(flat_numel, dtype=BF16, device="cuda")
+    t = [(1, r, c)]
+    ws = torch.empty(zs.zs_muon_workspace(lay, t, "full"), dtype=torch.uint8,
+                     device="cuda")
+    zs.zs_muon_step(lay, t, [grads], state, p, flat, grad_layout=layout,
+                    grad_stride=stride, lr=0.5, momentum=0.9,
+                    weight_decay=0.1, precision="full", workspace=ws)
+    mean = (g[0].float().numpy() + g[1].float().numpy()) / np.float32(2)
+    M, U = OM.momentum(mean, M0, 0.9, True)
+    got = state[b.tile_off:].transpose(0, 1).reshape(3, -1)[:, :n].cpu()
+    assert np.array_equal(got[1].numpy(), M)
+    U = U.reshape(r, c)
+    O = OM.orthogonalize(U)
+    s = OM.scale("rms", r, c)
+    want = OM.apply(P0, O.ravel(), 0.5, 0.1, s)
+    tol = full_bound(U, O) * 0.5 * s * np.linalg.norm(O) + \
+        3 * 2.0 ** -24 * np.linalg.norm(want)
+    assert np.linalg.norm(got[0].numpy() - want) <= tol
+    for out, off in ((p, b.shard_off), (flat, b.flat_off)):
+        assert torch.equal(out[off:off + n].cpu(), got[0].to(BF16))

@@ -100,10 +100,10 @@ typedef struct {
  * may (x_batch_stride >= 0).  With batch > 1 they lie one behind the other
  * (o_batch_stride >= (rows - 1)*o_row_stride + cols) or side by side, as the
  * heads of one matrix do (o_batch_stride >= cols and
- * o_row_stride >= (batch - 1)*o_batch_stride + cols).  A matrix's output may be the matrix itself; an
- * output that shares elements with another matrix of the call is an error
- * that is not detected (the order in which matrices are read and written is
- * not defined). */
+ * o_row_stride >= (batch - 1)*o_batch_stride + cols).  A matrix's output may
+ * be the matrix itself; an output that shares elements with another matrix of
+ * the call is an error that is not detected (the order in which matrices are
+ * read and written is not defined). */
 typedef struct {
     const void* x;
     void* o;

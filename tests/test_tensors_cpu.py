@@ -1,0 +1,480 @@
+"""zs_tensors.h without a GPU: every declared symbol is there, argument checks
+return the documented codes before any device work, tables and workspaces
+have the documented sizes, overlaps are found; and the oracle's 8-bit form
+against its definition."""
+
+import ctypes
+import math
+import os
+import random
+import re
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+import zero_sharded_optimizer_shard_amd as zs
+from oracle import tensors as OT
+from zero_sharded_optimizer_shard_amd import _tensors as zt
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+EINVAL, EALIGN, ERANGE = -1, -2, -3
+BASE = 1 << 40          # addresses that are never touched: calls that reach
+                        # the device are not made here
+GAP = 1 << 32
+
+
+def test_exports_every_declared_symbol():
+    text = open(os.path.join(ROOT, "include", "zs_tensors.h")).read()
+    text = re.sub(r"/\*.*?\*/", "", text, flags=re.S)
+    names = sorted(set(re.findall(r"\b(zs_[a-z0-9_]+)\s*\(", text)))
+    assert names == sorted(zs.TENSORS_EXPORTS)
+    for n in names:
+        assert hasattr(zs.lib(), n)
+
+
+def test_header_is_plain_c(tmp_path):
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not found")
+    c = tmp_path / "a.c"
+    # beside the other headers, in either order
+    c.write_text('#include "zs_tensors.h"\n#include "zs_muon.h"\n'
+                 'int size(void) { return (int)sizeof(zs_tensor) + ZS_F32; '
+                 '}\n')
+    subprocess.run(["gcc", "-std=c99", "-pedantic", "-Wall", "-Werror", "-I",
+                    os.path.join(ROOT, "include"), "-c", str(c), "-o",
+                    str(tmp_path / "a.o")], check=True)
+
+
+# ---- refusals ------------------------------------------------------------------
+
+def tensor(k=0, state=32, **kw):
+    """A good tensor of its own addresses, then changes."""
+    at = BASE + 16 * k * GAP
+    t = zt.zs_tensor(1000, at, 1000, at + GAP, at + 2 * GAP, at + 3 * GAP,
+                     at + 4 * GAP, None, None, 0)
+    if state == 8:
+        t.m_scale, t.v_scale = at + 5 * GAP, at + 6 * GAP
+    if state == 0:
+        t.m = t.v = None
+    for name, v in kw.items():
+        setattr(t, name, v)
+    return t
+
+
+def create(*ts, count=None, world=1, gt=0, pt=0, state=32, out=None):
+    arr = (zt.zs_tensor * max(len(ts), 1))(*ts)
+    h = ctypes.c_void_p() if out is None else out
+    rc = zt._lib().zs_tensors_create(len(ts) if count is None else count,
+                                     arr, world, gt, pt, state,
+                                     ctypes.byref(h))
+    assert (rc == 0) == bool(h.value)
+    return rc, zt.TensorList(h.value, None)
+
+
+def code(*ts, **kw):
+    rc, _ = create(*ts, **kw)
+    if rc:
+        assert zs.zs_last_error()
+    return rc
+
+
+def test_good_lists():
+    assert code() == 0
+    assert code(tensor()) == 0
+    assert code(tensor(), tensor(1)) == 0
+    assert code(tensor(state=8), state=8) == 0
+    assert code(tensor(state=0), state=0) == 0
+    assert code(tensor(master=None), gt=1, pt=1) == 0
+    assert code(tensor(grad=None, param=None, master=None)) == 0
+    assert code(tensor(state=0, param=None, master=None), state=0) == 0
+    # nothing of an empty tensor is looked at but its size and group
+    assert code(tensor(), zt.zs_tensor()) == 0
+    assert code(zt.zs_tensor(), tensor()) == 0
+
+
+@pytest.mark.parametrize("want,ts,kw", [
+    (EINVAL, [tensor()], dict(count=-1)),
+    (EINVAL, [tensor()], dict(world=0)),
+    (EINVAL, [tensor()], dict(world=-3)),
+    (EINVAL, [tensor()], dict(gt=2)), (EINVAL, [tensor()], dict(gt=-1)),
+    (EINVAL, [tensor()], dict(pt=2)), (EINVAL, [tensor()], dict(pt=-1)),
+    (EINVAL, [tensor()], dict(state=4)), (EINVAL, [tensor()], dict(state=1)),
+    (EINVAL, [tensor(numel=-1)], {}),
+    (EINVAL, [tensor(group=-1)], {}), (EINVAL, [tensor(group=16)], {}),
+    # given for some only
+    (EINVAL, [tensor(), tensor(1, grad=None)], {}),
+    (EINVAL, [tensor(grad=None), tensor(1)], {}),
+    (EINVAL, [tensor(), tensor(1, param=None, master=None)], {}),
+    (EINVAL, [tensor(), tensor(1, master=None)], {}),
+    (EINVAL, [tensor(m=None)], {}), (EINVAL, [tensor(v=None)], {}),
+    (EINVAL, [tensor()], dict(state=0)),
+    (EINVAL, [tensor(state=0)], {}),
+    # scales
+    (EINVAL, [tensor(state=8)], {}), (EINVAL, [tensor()], dict(state=8)),
+    (EINVAL, [tensor(state=8, m_scale=None)], dict(state=8)),
+    (EINVAL, [tensor(state=8, v_scale=None)], dict(state=8)),
+    # masters
+    (EINVAL, [tensor()], dict(pt=1)),
+    (EINVAL, [tensor(param=None)], {}),
+    # alignment
+    (EALIGN, [tensor(grad=BASE + 1)], {}),
+    (EALIGN, [tensor(grad=BASE + 2)], dict(gt=1)),
+    (EALIGN, [tensor(param=BASE + GAP + 1)], {}),
+    (EALIGN, [tensor(param=BASE + GAP + 2, master=None)], dict(pt=1)),
+    (EALIGN, [tensor(master=BASE + 2 * GAP + 2)], {}),
+    (EALIGN, [tensor(m=BASE + 3 * GAP + 2)], {}),
+    (EALIGN, [tensor(v=BASE + 4 * GAP + 1)], {}),
+    (EALIGN, [tensor(state=8, m=BASE + 3 * GAP + 2)], dict(state=8)),
+    (EALIGN, [tensor(state=8, v=BASE + 4 * GAP + 1)], dict(state=8)),
+    (EALIGN, [tensor(state=8, m_scale=BASE + 5 * GAP + 2)], dict(state=8)),
+    (EALIGN, [tensor(state=8, v_scale=BASE + 6 * GAP + 1)], dict(state=8)),
+    # sizes
+    (ERANGE, [tensor(numel=(1 << 46) + 1)], {}),
+    (ERANGE, [tensor(numel=1 << 62)], {}),
+    (ERANGE, [tensor(grad_stride=999)], dict(world=2)),
+    (ERANGE, [tensor(grad_stride=0)], dict(world=2)),
+    (ERANGE, [tensor(grad_stride=-1000)], dict(world=2)),
+    (ERANGE, [tensor(grad_stride=1 << 62)], dict(world=2)),
+    (ERANGE, [tensor(grad_stride=1 << 45)], dict(world=4)),
+    (ERANGE, [tensor(numel=1, grad_stride=1)], dict(world=(1 << 30) + 1)),
+    (ERANGE, [tensor(grad=None, param=None, master=None, numel=1 << 40,
+                     m=1 << 50, v=1 << 51)], {})])
+def test_create_refusals(want, ts, kw):
+    assert code(*ts, **kw) == want
+
+
+def test_create_nulls():
+    L = zt._lib()
+    h = ctypes.c_void_p(5)
+    assert L.zs_tensors_create(1, None, 1, 0, 0, 32, ctypes.byref(h)) == \
+        EINVAL
+    assert not h.value                  # cleared by a failed call
+    assert L.zs_tensors_create(0, None, 1, 0, 0, 32, None) == EINVAL
+    assert L.zs_tensors_create(0, None, 1, 0, 0, 32, ctypes.byref(h)) == 0
+    L.zs_tensors_free(h)
+    L.zs_tensors_free(None)
+
+
+@pytest.mark.parametrize("kw", [
+    dict(param=BASE + 16 * GAP),                    # gradient of the other
+    dict(m=tensor(1).m), dict(v=tensor(1).m), dict(master=tensor(1).v),
+    dict(m=tensor(1).m + 3996), dict(m=tensor(1).m - 3996),
+    dict(param=tensor(1).param + 1996),
+    dict(v=tensor(0).m), dict(param=tensor(0).grad + 1998),
+    dict(master=tensor(0).grad - 3996)])
+def test_overlaps_are_refused(kw):
+    assert code(tensor(0, **kw), tensor(1)) == EINVAL
+    assert code(tensor(1), tensor(0, **kw)) == EINVAL
+
+
+@pytest.mark.parametrize("kw", [
+    dict(m=tensor(1).m + 4000), dict(m=tensor(1).m - 4000),
+    dict(param=tensor(1).param + 2000),
+    dict(grad=tensor(1).grad),                      # read by both
+    dict(param=tensor(0).grad + 2000)])
+def test_neighbours_are_taken(kw):
+    assert code(tensor(0, **kw), tensor(1)) == 0
+
+
+def test_scales_and_slices_overlap():
+    t = tensor(state=8)
+    # 1000 elements have four blocks
+    assert code(tensor(state=8, v_scale=t.m_scale + 16), state=8) == 0
+    assert code(tensor(state=8, v_scale=t.m_scale + 12), state=8) == EINVAL
+    # between two slices is a place of its own
+    t = tensor(grad_stride=3000)
+    assert code(tensor(grad_stride=3000, param=t.grad + 2000), world=2) == 0
+    assert code(tensor(grad_stride=3000, param=t.grad + 4000),
+                world=2) == 0
+    assert code(tensor(grad_stride=3000, param=t.grad + 4002),
+                world=2) == EINVAL
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_overlaps_match_all_pairs(seed):
+    rng = random.Random(seed)
+    ts, spans = [], []
+    for k in range(rng.randint(1, 6)):
+        n = rng.randint(1, 40)
+        a = [BASE + 4 * rng.randrange(rng.choice([200, 2000]))
+             for _ in range(4)]
+        ts.append(zt.zs_tensor(n, a[0], 0, a[1], None, a[2], a[3], None,
+                               None, 0))
+        spans.append((a[0], a[0] + 2 * n, False))
+        spans += [(a[1], a[1] + 4 * n, True), (a[2], a[2] + 4 * n, True),
+                  (a[3], a[3] + 4 * n, True)]
+    hit = any((x[2] or y[2]) and x[0] < y[1] and y[0] < x[1]
+              for i, x in enumerate(spans) for y in spans[:i])
+    assert code(*ts, pt=1) == (EINVAL if hit else 0)
+
+
+HP = (3e-4, 0.9, 0.95, 1e-8, 0.1)
+
+
+def step(lst, hps=(HP,), n=None, t=1, sumsq=None, max_norm=1.0):
+    arr = (zs.zs_adamw * max(len(hps), 1))(*[zs.zs_adamw(*h) for h in hps])
+    return zt._lib().zs_tensors_step(lst.handle, arr,
+                                     len(hps) if n is None else n, t, sumsq,
+                                     max_norm, None)
+
+
+def hp(**kw):
+    d = dict(zip(("lr", "b1", "b2", "eps", "wd"), HP), **kw)
+    return tuple(d.values())
+
+
+@pytest.mark.parametrize("want,kw", [
+    (EINVAL, dict(n=0)), (EINVAL, dict(n=17)), (EINVAL, dict(n=-1)),
+    (EINVAL, dict(t=0)), (EINVAL, dict(t=-5)),
+    (EINVAL, dict(hps=[hp(lr=math.nan)])),
+    (EINVAL, dict(hps=[hp(lr=math.inf)])),
+    (EINVAL, dict(hps=[hp(wd=math.inf)])),
+    (EINVAL, dict(hps=[hp(wd=math.nan)])),
+    (EINVAL, dict(hps=[hp(b1=1.0)])), (EINVAL, dict(hps=[hp(b1=-0.1)])),
+    (EINVAL, dict(hps=[hp(b1=math.nan)])),
+    (EINVAL, dict(hps=[hp(b2=1.0)])), (EINVAL, dict(hps=[hp(b2=-1e-3)])),
+    (EINVAL, dict(hps=[hp(b2=math.nan)])),
+    (EINVAL, dict(hps=[hp(eps=0.0)])), (EINVAL, dict(hps=[hp(eps=-1.0)])),
+    (EINVAL, dict(hps=[hp(eps=1e-39)])),
+    (EINVAL, dict(hps=[hp(eps=math.inf)])),
+    (EINVAL, dict(hps=[hp(eps=math.nan)])),
+    (EINVAL, dict(hps=[hp(lr=3e38, b1=0.9)])),
+    (EINVAL, dict(hps=[hp(lr=1e30, wd=1e30)])),
+    (EINVAL, dict(hps=[hp(), hp(lr=math.nan)])),
+    (EINVAL, dict(sumsq=BASE, max_norm=0.0)),
+    (EINVAL, dict(sumsq=BASE, max_norm=-1.0)),
+    (EINVAL, dict(sumsq=BASE, max_norm=math.nan)),
+    (EALIGN, dict(sumsq=BASE + 4))])
+def test_step_refusals(want, kw):
+    for lst in (create(tensor())[1], create()[1]):      # empty lists too
+        assert step(lst, **kw) == want
+        assert zs.zs_last_error()
+
+
+def test_step_needs_its_parts_and_a_table():
+    for kw, t in ((dict(), tensor(grad=None)),
+                  (dict(), tensor(param=None, master=None)),
+                  (dict(state=0), tensor(state=0)),
+                  (dict(), tensor())):                  # no table
+        assert step(create(t, **kw)[1]) == EINVAL
+    lst = create(tensor(group=1), tensor(1))[1]
+    assert step(lst) == EINVAL
+    assert "group 1" in zs.zs_last_error()
+    L = zt._lib()
+    arr = (zs.zs_adamw * 1)(zs.zs_adamw(*HP))
+    assert L.zs_tensors_step(None, arr, 1, 1, None, 1.0, None) == EINVAL
+    assert L.zs_tensors_step(lst.handle, None, 1, 1, None, 1.0,
+                             None) == EINVAL
+
+
+def test_empty_lists_step_nothing():
+    assert step(create()[1]) == 0
+    assert step(create(zt.zs_tensor(), zt.zs_tensor())[1]) == 0
+
+
+def table_bytes(lst):
+    out = ctypes.c_int64()
+    assert zt._lib().zs_tensors_table_bytes(lst.handle,
+                                            ctypes.byref(out)) == 0
+    return out.value
+
+
+def workspace_bytes(lst):
+    out = ctypes.c_int64()
+    assert zt._lib().zs_tensors_sumsq_workspace(lst.handle,
+                                                ctypes.byref(out)) == 0
+    return out.value
+
+
+def test_table_and_workspace_sizes():
+    assert table_bytes(create()[1]) == 0
+    assert workspace_bytes(create()[1]) == 0
+    one = table_bytes(create(tensor())[1])
+    assert 88 + 4 <= one <= 88 + 32
+    assert table_bytes(create(tensor(), zt.zs_tensor())[1]) == one
+    only = dict(param=None, master=None, state=0)
+    big = create(tensor(numel=1 << 30, **only), state=0)[1]
+    assert 1 << 20 <= table_bytes(big) / 4 <= 1 << 22
+    assert 8 <= workspace_bytes(big) <= 1 << 20
+    # a list past 32 bits of elements
+    big = create(tensor(numel=3 << 32, grad=1 << 50, **only), state=0)[1]
+    assert workspace_bytes(big) <= 1 << 20
+    L = zt._lib()
+    assert L.zs_tensors_table_bytes(None, ctypes.byref(
+        ctypes.c_int64())) == EINVAL
+    assert L.zs_tensors_table_bytes(big.handle, None) == EINVAL
+    assert L.zs_tensors_sumsq_workspace(None, ctypes.byref(
+        ctypes.c_int64())) == EINVAL
+    assert L.zs_tensors_sumsq_workspace(big.handle, None) == EINVAL
+
+
+def test_upload_refusals():
+    L = zt._lib()
+    lst = create(tensor())[1]
+    n = table_bytes(lst)
+    assert L.zs_tensors_upload(None, BASE, n, None) == EINVAL
+    assert L.zs_tensors_upload(lst.handle, None, n, None) == EINVAL
+    assert L.zs_tensors_upload(lst.handle, BASE + 8, n, None) == EALIGN
+    assert L.zs_tensors_upload(lst.handle, BASE, n - 1, None) == ERANGE
+    assert L.zs_tensors_upload(lst.handle, BASE, -1, None) == ERANGE
+    assert L.zs_tensors_upload(create()[1].handle, None, 0, None) == 0
+
+
+def test_sumsq_refusals():
+    L = zt._lib()
+    big = create(tensor(numel=1 << 24, grad_stride=1 << 24))[1]
+    n = workspace_bytes(big)
+
+    def call(lst, out=BASE, ws=BASE, nbytes=n):
+        return L.zs_tensors_sumsq(lst.handle, out, ws, nbytes, None)
+    assert n > 0
+    assert L.zs_tensors_sumsq(None, BASE, BASE, n, None) == EINVAL
+    assert call(big, out=None) == EINVAL
+    assert call(big, out=BASE + 4) == EALIGN
+    assert call(big, ws=None) == EINVAL
+    assert call(big, ws=BASE + 8) == EALIGN
+    assert call(big, nbytes=n - 1) == ERANGE
+    assert call(big, nbytes=-1) == ERANGE
+    assert call(big) == EINVAL                          # no table
+    assert call(create(tensor(grad=None))[1]) == EINVAL
+
+
+def test_convert_refusals():
+    L = zt._lib()
+
+    def states(*numels, state=32, at=0):
+        return create(*[zt.zs_tensor(n, None, 0, None, None,
+                                     tensor(k + at).m, tensor(k + at).v,
+                                     tensor(k + at).m + GAP // 2
+                                     if state == 8 else None,
+                                     tensor(k + at).v + GAP // 2
+                                     if state == 8 else None, 0)
+                        for k, n in enumerate(numels)], state=state)[1]
+    a = states(5, 300)
+
+    def call(x, y):
+        rc = L.zs_tensors_convert(x.handle if x else None,
+                                  y.handle if y else None, None)
+        if rc:
+            assert zs.zs_last_error()
+        return rc
+    assert call(None, a) == EINVAL and call(a, None) == EINVAL
+    assert call(a, states(5, 300, at=9)) == EINVAL          # both 32 bits
+    assert call(states(5, 300, state=8), states(5, 300, state=8, at=9)) == \
+        EINVAL
+    assert call(a, create(tensor(9, state=0), state=0)[1]) == EINVAL
+    for other in ((5,), (300, 5), (5, 300, 1), (5, 301), (0, 5, 300)):
+        b = states(*other, state=8, at=9)
+        assert call(a, b) == EINVAL and "sizes" in zs.zs_last_error()
+        assert call(b, a) == EINVAL
+    assert call(a, states(5, 300, state=8)) == EINVAL       # in place
+    assert "overlap" in zs.zs_last_error()
+    assert call(a, states(5, 300, state=8, at=1)) == EINVAL
+    assert "overlap" in zs.zs_last_error()
+    assert call(a, states(5, 300, state=8, at=9)) == EINVAL
+    assert "table" in zs.zs_last_error()
+    assert call(states(), states(state=8)) == 0
+    assert call(states(0, 0), states(0, 0, state=8)) == 0
+
+
+def test_binding_refuses_host_tensors():
+    import torch
+    x = [torch.zeros(8)]
+    with pytest.raises(ValueError):
+        zs.zs_tensors_create(params=x, grads=x, m=x, v=x)
+    with pytest.raises(ValueError):
+        zs.zs_tensors_create()
+    with pytest.raises(ValueError):
+        zs.zs_tensors_create(m=x)
+    with pytest.raises(ValueError):
+        zs.zs_tensors_create(m=x, v=x + x)
+    with pytest.raises(ValueError):
+        zs.zs_tensors_create(m=x, v=x, world=1 << 31)
+
+
+# ---- the oracle ------------------------------------------------------------------
+
+@pytest.mark.parametrize("top", [127, 255])
+def test_encode_takes_the_nearest_code(top):
+    rng = np.random.default_rng(top)
+    x = (rng.standard_normal(1000) * np.exp(3 * rng.standard_normal(1000))
+         ).astype(np.float32)
+    if top == 255:
+        x = np.abs(x)
+    q, S = OT.encode(x, top)
+    val = OT.decode(q, S)
+    assert np.abs(q).max() == top
+    # half a step of the squares around q, and roundings of S, y and q^2 S
+    A = np.repeat([np.abs(x[i:i + 256]).max() for i in range(0, 1000, 256)],
+                  256)[:1000]
+    half = (np.abs(q) + 0.25) * A / top ** 2
+    extra = np.where((q == 1) & (top == 255), A / top ** 2, 0)
+    assert np.all(np.abs(val - x) <= half + extra + 6e-7 * np.abs(x))
+    assert np.all(np.sign(val) * np.sign(x) >= 0)
+    if top == 255:
+        assert np.all((q > 0) == (x > 0))
+
+
+@pytest.mark.parametrize("top", [127, 255])
+def test_encode_at_the_borders(top):
+    """y just below, at and above (q + 1/2)^2, in a block whose A is top^2,
+    so that y is x itself."""
+    k = np.arange(1, top, 5)
+    b = ((k + 0.5) ** 2).astype(np.float32)
+    for x, want in ((np.nextafter(b, np.float32(0)), k), (b, k + 1),
+                    (np.nextafter(b, np.float32(1e9)), k + 1)):
+        blk = np.append(x, np.float32(top ** 2))
+        q, S = OT.encode(blk, top)
+        assert S[0] == np.float32(top ** 2) * np.float32(1 / top ** 2)
+        assert np.array_equal(q[:-1], want) and q[-1] == top
+
+
+def test_encode_special_blocks():
+    for bad in (np.inf, -np.inf, np.nan):
+        x = np.ones(600, np.float32)
+        x[300] = bad
+        q, S = OT.encode(x, 127)
+        assert np.isnan(S[1]) and np.isfinite(S[[0, 2]]).all()
+        assert np.all(q[256:512] == 0) and np.all(q[512:] == 127)
+        assert np.isnan(OT.decode(q, S)[256:512]).all()
+    tiny = np.full(10, 2.0 ** -100, np.float32)
+    assert np.all(OT.encode(tiny, 127)[0] == 127)
+    tiny = np.nextafter(tiny, np.float32(0))
+    q, S = OT.encode(tiny, 127)
+    assert not q.any() and not S.any()
+    q, S = OT.encode(np.zeros(5, np.float32), 255)
+    assert not q.any() and not S.any()
+    # a root far below its block's largest keeps a code of 1
+    q, S = OT.encode(np.float32([1, 1e-30, 0]), 255)
+    assert list(q) == [255, 1, 0]
+
+
+def test_codes_come_back_the_same():
+    rng = np.random.default_rng(3)
+    m = (rng.standard_normal(5000) * 10 ** rng.uniform(-6, 6, 5000)
+         ).astype(np.float32)
+    held = OT.hold(m, m * m)
+    again = OT.hold(*OT.stands_for(*held))
+    assert np.array_equal(held[0], again[0])
+    assert np.array_equal(held[2], again[2])
+
+
+def test_oracle_step_is_zs_steps():
+    """fp32 states: the formula's arithmetic equals the step oracle's bits."""
+    from oracle import step as O
+    rng = np.random.default_rng(5)
+    n, W, t = 3000, 3, 7
+    G = OT.to_bf16(rng.standard_normal((W, n)).astype(np.float32) * 1e-3)
+    w = rng.standard_normal(n).astype(np.float32) * np.float32(0.02)
+    m = rng.standard_normal(n).astype(np.float32) * np.float32(1e-3)
+    v = np.square(rng.standard_normal(n).astype(np.float32)
+                  * np.float32(1e-3))
+    g = OT.mean(OT.bf16(G))
+    m1, v1, r = OT.moments(g, m, v, HP, t)
+    w1 = OT.weights(w, m1, r, HP, t)
+    mo, vo, wo = m.copy(), v.copy(), w.copy()
+    p = O.step(G, wo, mo, vo, O.AdamW(*HP), t)
+    assert np.array_equal(m1, mo) and np.array_equal(v1, vo)
+    assert np.array_equal(w1, wo) and np.array_equal(OT.to_bf16(w1), p)

@@ -1,8 +1,8 @@
 """One data-parallel rank's ZeRO-1/2 optimizer step on MI355X (gfx950).
 
-The HIP library libzs.so (C-ABI in include/zs.h, and include/zs_muon.h for
-the Muon step) does all the work; this package is its ctypes binding, with
-the same names.
+The HIP library libzs.so (C-ABI in include/zs.h, include/zs_muon.h for the
+Muon step and include/zs_tensors.h for lists of tensors) does all the work;
+this package is its ctypes binding, with the same names.
 """
 
 from ._muon import (MUON_EXPORTS, ZS_BF16, ZS_F32, ZS_MUON_SCALE_NONE,
@@ -11,6 +11,13 @@ from ._muon import (MUON_EXPORTS, ZS_BF16, ZS_F32, ZS_MUON_SCALE_NONE,
                     zs_muon_step, zs_muon_tensor, zs_muon_workspace,
                     zs_newton_schulz, zs_ns_matrices, zs_orthogonalize,
                     zs_orthogonalize_workspace)
+
+from ._tensors import (TENSORS_EXPORTS, ZS_STATE8_BLOCK, ZS_STATE_8,
+                       ZS_STATE_32, ZS_STATE_NONE, ZS_TENSORS_MAX_GROUPS,
+                       TensorList, zs_tensor, zs_tensors_convert,
+                       zs_tensors_create, zs_tensors_step, zs_tensors_sumsq,
+                       zs_tensors_sumsq_workspace, zs_tensors_table_bytes,
+                       zs_tensors_upload)
 
 from ._zs import (EXPORTS, LIB_PATH, ZS_ACC_ADD, ZS_ACC_FIRST, ZS_ACC_LAST,
                   ZS_EIO, ZS_EMISMATCH, zs_checkpoint_load,
@@ -56,4 +63,10 @@ __all__ = ["EXPORTS", "LIB_PATH", "ZS_ACC_ADD", "ZS_ACC_FIRST", "ZS_ACC_LAST",
            "ZS_NS_FAST", "ZS_NS_FULL", "ZS_NS_MAX_STEPS", "zs_muon",
            "zs_muon_step", "zs_muon_tensor", "zs_muon_workspace",
            "zs_newton_schulz", "zs_ns_matrices", "zs_orthogonalize",
-           "zs_orthogonalize_workspace"]
+           "zs_orthogonalize_workspace",
+           "TENSORS_EXPORTS", "ZS_STATE8_BLOCK", "ZS_STATE_8", "ZS_STATE_32",
+           "ZS_STATE_NONE", "ZS_TENSORS_MAX_GROUPS", "TensorList",
+           "zs_tensor", "zs_tensors_convert", "zs_tensors_create",
+           "zs_tensors_step", "zs_tensors_sumsq",
+           "zs_tensors_sumsq_workspace", "zs_tensors_table_bytes",
+           "zs_tensors_upload"]

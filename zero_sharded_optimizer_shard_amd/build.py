@@ -1,5 +1,5 @@
-"""Build libzs.so (the C-ABI library of include/zs.h and include/zs_muon.h)
-for gfx950, in-tree.
+"""Build libzs.so (the C-ABI library of include/zs.h, zs_muon.h and
+zs_tensors.h) for gfx950, in-tree.
 
 Flags that matter for the arithmetic: -ffp-contract=off (one rounding per
 fp32 operation, no fused multiply-add), hipcc's default correctly rounded
@@ -28,6 +28,7 @@ SOURCES = [os.path.join(CSRC, "zs_layout.cpp"),
            os.path.join(CSRC, "zs_gather.hip"),
            os.path.join(CSRC, "zs_accum.hip"),
            os.path.join(CSRC, "zs_muon.hip"),
+           os.path.join(CSRC, "zs_tensors.hip"),
            os.path.join(CSRC, "zs_stream.cpp"),
            os.path.join(CSRC, "zs_prefetch.cpp"),
            os.path.join(CSRC, "zs_ckpt.cpp")]

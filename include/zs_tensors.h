@@ -97,7 +97,7 @@ typedef struct zs_tensors zs_tensors;
  * [0, ZS_TENSORS_MAX_GROUPS), pointers given for some tensors only, scales
  * missing or out of place, a master with fp32 or no parameters, overlaps);
  * ZS_EALIGN; ZS_ERANGE (world > 1 and grad_stride < numel, slices reaching
- * past 2^46 elements, more than 2^36 elements or 2^30 slices in all);
+ * past 2^46 elements, 2^38 elements or more or more than 2^30 slices in all);
  * ZS_ENOMEM. */
 int zs_tensors_create(int32_t count, const zs_tensor* tensors, int32_t world,
                       int32_t grad_type, int32_t param_type, int32_t state,
@@ -107,15 +107,17 @@ void zs_tensors_free(zs_tensors* list);
 /* The list's table in device memory: its size (about 4 bytes per 1024
  * elements and 88 per tensor), and the call that writes it, once, before the
  * list is used.  `table` (16-byte aligned) stays the caller's; it must live
- * unchanged as long as the list is used, captured calls included.  The
- * upload waits for its copy on hip_stream, so it is refused under capture
- * (ZS_EINVAL); a second upload moves the list to another table.  Errors
- * also: ZS_EALIGN, ZS_ERANGE (bytes too few), ZS_EDEVICE. */
+ * unchanged as long as calls of the list may run, replays of captured ones
+ * included (those do not need the handle any more).  The upload waits for its
+ * copy on hip_stream.  Errors: ZS_EINVAL (NULL, a stream under capture, a
+ * list that has its table), ZS_EALIGN, ZS_ERANGE (bytes too few),
+ * ZS_EDEVICE. */
 int zs_tensors_table_bytes(const zs_tensors* list, int64_t* bytes);
 int zs_tensors_upload(zs_tensors* list, void* table, int64_t bytes,
                       void* hip_stream);
 
-/* One AdamW step of every tensor of the list, in one launch.  Per element,
+/* One AdamW step of every tensor of the list, in one launch (one for each 2^34
+ * elements).  Per element,
  * with one fp32 rounding per operation, in the order of zs_step:
  *   g = (G_0 + G_1 + ... + G_{W-1}) / W              (sum in rank order)
  *   g = g * c                                        (with sumsq, below)
@@ -133,7 +135,8 @@ int zs_tensors_upload(zs_tensors* list, void* table, int64_t bytes,
  * sumsq: DEVICE pointer to one double (8-byte aligned), or NULL.  With it the
  *   gradients are clipped by their global norm n = sqrt(*sumsq):
  *   c = f32(max_norm / n) where n > max_norm, else 1 (in double, rounded
- *   once); where *sumsq is not finite, nothing is written at all.  It is read
+ *   once); where *sumsq is negative or not finite, nothing is written at all
+ *   (the caller's t goes on or not, as it likes).  It is read
  *   when the step runs: zs_tensors_sumsq writes it, ranks may add theirs
  *   before the step.  max_norm may be infinite (no clipping, but no step on
  *   a sum that is not finite); it is not read where sumsq is NULL.

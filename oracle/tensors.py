@@ -47,7 +47,7 @@ def constants(hp, t):
 
 def coefficient(sumsq, max_norm):
     """The clipping coefficient, or None where the step writes nothing."""
-    if not np.isfinite(sumsq):
+    if not np.isfinite(sumsq) or sumsq < 0:
         return None
     norm = float(sumsq) ** 0.5
     return F(float(F(max_norm)) / norm) if norm > F(max_norm) else F(1)

@@ -279,8 +279,8 @@ def test_step_clipped(bits, max_norm):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
-@pytest.mark.parametrize("sum_", [math.inf, math.nan, -math.inf])
-def test_step_writes_nothing_on_a_sum_that_is_not_finite(bits, sum_):
+@pytest.mark.parametrize("sum_", [math.inf, math.nan, -math.inf, -1.0])
+def test_step_writes_nothing_on_a_sum_that_is_none(bits, sum_):
     c = Case(SIZES, bits, world=2)
     was = [{k: x.clone() for k, x in d.items()} for d in c.dev]
     s = torch.full((1,), sum_, dtype=torch.float64, device="cuda")
@@ -734,12 +734,12 @@ def test_explicit_stream():
     c.check()
 
 
-def test_second_table():
+def test_second_table_is_refused():
+    """Captured calls and calls on their way may read the first."""
     c = Case([3000, 5], 32)
-    first = c.list._table
-    upload(c.list)
-    assert c.list._table.data_ptr() != first.data_ptr()
-    first.fill_(0xff)
+    with pytest.raises(zs.ZsError) as ei:
+        upload(c.list)
+    assert ei.value.code == -1
     c.step()
     c.expect()
     c.check()
@@ -782,6 +782,30 @@ def test_offsets_past_32_bits():
                   (2.0 ** -8 + 2.0 ** -20) * np.abs(kept - update) +
                   2.0 ** -20 * np.abs(update))
     assert not m[:lead].any() and not p[:lead].any()
+
+
+def test_more_pieces_than_a_launch_takes():
+    """More than 2^34 elements go in two launches; what is at the ends of both
+    is stepped once, and counted."""
+    n, first = (1 << 34) + 5000, ((1 << 24) - 1) * 1024
+    p = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    g = torch.zeros(n, dtype=torch.bfloat16, device="cuda")
+    m = torch.zeros(n, dtype=torch.int8, device="cuda")
+    v = torch.zeros(n, dtype=torch.uint8, device="cuda")
+    S = [torch.zeros(-(-n // 256), device="cuda") for _ in range(2)]
+    at = torch.tensor([0, first - 1, first, n - 1], device="cuda")
+    p[at], g[at] = 1.0, 0.5
+    lst = zs.zs_tensors_create(params=[p], grads=[g], m=[m], v=[v],
+                               m_scale=[S[0]], v_scale=[S[1]])
+    upload(lst)
+    assert sumsq_of(lst).item() == 1.0
+    # a step of lr 0.1 moves a weight by 0.1: to 0.8984 in bf16
+    zs.zs_tensors_step(lst, zs.zs_adamw(0.1, 0.9, 0.95, 1e-8, 0.0), step=1)
+    assert p[at].tolist() == [0.8984375] * 4
+    assert m[at].tolist() == [127] * 4 and v[at].tolist() == [255] * 4
+    for x in (p, m, v):
+        x[at] = 0
+        assert not x[:1 << 33].any() and not x[1 << 33:].any()
 
 
 # ---- the binding's refusals ----------------------------------------------------------

@@ -10,8 +10,8 @@ import ctypes
 import math
 from typing import Optional, Sequence
 
-from ._muon import (ZS_BF16, ZS_F32, _device, _int, _on_stream, _type,
-                    _workspace)
+from ._muon import ZS_BF16, ZS_F32, _device, _int, _type, _workspace
+from ._muon import _on_stream as _muon_stream
 from ._zs import _check, zs_adamw
 from ._zs import lib as _zs_lib
 
@@ -34,6 +34,16 @@ class zs_tensor(ctypes.Structure):
 
 
 _ready = None
+
+
+def _on_stream(stream):
+    """The given stream, or the current one: by its address, where torch has
+    it, as making a stream object takes longer than the launch."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    if stream is not None or raw is None:
+        return _muon_stream(stream)
+    return raw(torch.cuda.current_device())
 
 
 def _lib():
@@ -61,7 +71,8 @@ def _lib():
 
 class TensorList:
     """Owning handle of a zs_tensors*.  It keeps the tensors and the table
-    alive, not what they hold."""
+    alive: keep it as long as its calls may run, replays of captured ones
+    included."""
 
     def __init__(self, handle: int, tensors):
         self._h = ctypes.c_void_p(handle)
@@ -217,8 +228,8 @@ def zs_tensors_step(lst: TensorList, hp, *, step: int, sumsq=None,
     """One AdamW step of every tensor of the list.  hp: a zs_adamw, or one
     for each hyper-parameter group; step: the counter t, from 1.  sumsq: a
     device float64 that zs_tensors_sumsq wrote (or ranks added up): the
-    gradients are clipped to the global norm max_norm, and where it is not
-    finite the step writes nothing."""
+    gradients are clipped to the global norm max_norm, and where it is
+    negative or not finite the step writes nothing."""
     hps = [hp] if isinstance(hp, zs_adamw) else hp
     arr = (zs_adamw * max(len(hps), 1))(*hps)
     ptr = None

@@ -48,5 +48,8 @@ namespace zs {
 int fail(int code, const char* fmt, ...);
 // Clear the calling thread's failure text.
 void clear_error();
+// LDS a workgroup reserves so that at most `wgs` of them share a CU; 0 for no
+// cap (wgs <= 0, or zs_set_residency_cap(0)).
+unsigned residency_lds(int wgs);
 
 }  // namespace zs

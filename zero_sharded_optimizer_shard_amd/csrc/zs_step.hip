@@ -1816,6 +1816,11 @@ int scratch_on(int dev, unsigned char** out)
 
 }  // namespace
 
+unsigned zs::residency_lds(int wgs)
+{
+    return residency_cap_lds(wgs);
+}
+
 extern "C" int32_t zs_set_residency_cap(int32_t on)
 {
     return g_cap_on.exchange(on ? 1 : 0);

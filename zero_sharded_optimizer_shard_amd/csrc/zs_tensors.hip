@@ -2,16 +2,28 @@
 // gradients' sum of squares, and the conversion of states, with their host
 // side.  Written for gfx950 (CDNA4, wave64).
 //
-// All four are streams bounded by HBM: per element a step reads W gradients,
-// the weights and the states and writes weights and states back (28 bytes
-// with bf16 gradients, a master and fp32 states; 16 with 8-bit ones; 10 with
-// 8-bit states and no master).
+// All are streams bounded by HBM: per element a step reads W gradients, the
+// weights and the states and writes weights and states back (28 bytes with
+// bf16 gradients of one rank, a master and fp32 states; 16 with 8-bit states;
+// 10 with 8-bit states and no master).  Measured on MI355X over 218 M elements
+// in nine tensors (124 M in 148 with the master), of 8 TB/s:
+//   fp32 states, W = 1: bf16 weights 6.6 TB/s, fp32 weights and gradients 6.7,
+//     a master 6.5; W = 2, 3, 4, 5, 8 with a master 6.6, 6.6, 6.6, 6.5, 6.6
+//     (rows of gradients at multiples of 256 bytes; at multiples of 16 every
+//     load takes a line more: 6.5, 6.4, 6.3, 6.2, 6.1)
+//   8-bit states: 6.2 (master and bf16 weights), 6.5 (fp32)
+//   to 8 bits 6.7, to 32 bits 6.2, sum of squares 6.2 (both launches)
+// Large streams of the same mixes reach 6.8 here.
 //
-// A list's tensors are cut into pieces of kPiece elements, one one-wave
-// workgroup each, so one launch takes any number of tensors of any sizes.  A
-// workgroup finds its tensor in the list's table in device memory (the
-// tensor's number for each piece, then the tensor's record; both are
-// wave-uniform and come by scalar loads).
+// Work decomposition.  A list's tensors are cut into pieces of kPiece
+// elements, each taken by one to four one-wave workgroups, so one launch takes
+// any number of tensors of any sizes.  A workgroup finds its tensor in the
+// list's table in device memory: the tensor's number for each piece, then the
+// tensor's record, both wave-uniform scalar loads.  As in zs_step.hip every
+// load or store of a wave covers one contiguous run, all loads of a part are
+// issued before its arithmetic, loads are non-temporal and aligned stores
+// stream to HBM with system scope.  Consecutive workgroups go to the XCDs in
+// turn; giving each XCD runs of 2, 4 or 32 of them cost 2 to 6 %.
 
 #include <hip/hip_runtime.h>
 
@@ -20,6 +32,7 @@
 #include <cmath>
 #include <cstdint>
 #include <new>
+#include <type_traits>
 #include <vector>
 
 #include "zs_device.h"
@@ -29,19 +42,33 @@
 namespace {
 
 typedef unsigned int u32x2 __attribute__((ext_vector_type(2)));
+typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 // the same at any element's address; the hardware takes vector accesses at
 // such addresses whole
 typedef u32x2 u32x2_2 __attribute__((aligned(2)));
 typedef f32x4 f32x4_4 __attribute__((aligned(4)));
+typedef u32x4 u32x4_2 __attribute__((aligned(2)));
+typedef u32x4 u32x4_4 __attribute__((aligned(4)));
 
 constexpr int kWave = 64;
 constexpr int kBlock = ZS_STATE8_BLOCK;
 static_assert(kBlock == 4 * kWave, "a wave's unit is one block");
-constexpr int kUnits = 4;
-constexpr int kPiece = kBlock * kUnits;
-// HIP launches fewer than 2^32 work-items along x
-constexpr int64_t kMaxPieces = (int64_t(1) << 26) - 1;
+constexpr int kPiece = 4 * kBlock;
+// Pieces that one launch takes: HIP launches fewer than 2^32 work-items along
+// x, and a piece is four workgroups at most.
+constexpr int64_t kLaunchPieces = (int64_t(1) << 24) - 1;
+constexpr int64_t kMaxPieces = (int64_t(1) << 28) - 1;
+// Units of kBlock elements to a workgroup.  One keeps what is in flight most
+// compact: the 124 M step with fp32 states 537 us, 559 with two, 627 with four.
+// With 8-bit states two share the reductions and the division (bf16 weights
+// 351 us, 391 with one, 380 with four); where those cost little it is even
+// (with a master 318 us, 316 with one).
+constexpr int kStep32Units = 1, kStep8Units = 2;
+// To 8 bits 325 us (two units 340), to 32 bits 200 us with two at 20 workgroups
+// per CU (222 at as many as fit; one unit 209).
+constexpr int kPackUnits = 1, kUnpackUnits = 2;
+constexpr int kUnpackResidency = 20;
 constexpr int64_t kMaxReach = int64_t(1) << 46;
 constexpr int64_t kMaxSlices = int64_t(1) << 30;
 
@@ -74,15 +101,21 @@ struct Hp {
 struct Table {
     const Rec* recs;
     const int32_t* tensor;      // of each piece
+    int32_t first;              // a launch's first piece
+};
+
+// Of W ranks' gradients.
+struct Ranks {
+    int32_t W;
+    float fw, invw;     // W and 1/W
+    int32_t pow2;       // W is a power of two (1/W exact)
 };
 
 struct StepArgs {
     Table t;
     const double* sumsq;        // nullable
     float max_norm;
-    int32_t W;
-    float fw, invw;             // W and 1/W
-    int32_t pow2;               // W is a power of two (1/W exact)
+    Ranks ranks;
     Hp hp[ZS_TENSORS_MAX_GROUPS];
 };
 
@@ -98,35 +131,98 @@ __device__ __forceinline__ float bf16_hi(uint32_t u)
     return __uint_as_float(u & 0xffff0000u);
 }
 
-// fp32 -> bf16 bits, nearest even; NaN -> quiet NaN keeping sign and the
-// top payload bits.
-__device__ __forceinline__ uint32_t to_bf16(float f)
+// Two fp32 values -> bf16 bits, nearest even; NaN -> quiet NaN keeping sign
+// and the top payload bits (the instruction gives what the step kernels of
+// zs_step.hip compute, for every one of the 2^32 inputs).
+__device__ __forceinline__ uint32_t to_bf16(float lo, float hi)
 {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7fffffffu) > 0x7f800000u)
-        return (u >> 16) | 0x40u;
-    return (u + 0x7fffu + ((u >> 16) & 1u)) >> 16;
+    typedef float f32x2 __attribute__((ext_vector_type(2)));
+    typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+    return __builtin_bit_cast(
+        uint32_t, __builtin_convertvector((f32x2{lo, hi}), bf16x2));
+}
+
+// A pointer to device memory.  Pointers that come from the table are generic
+// to the compiler, and accesses through them would be flat ones.
+template <class T>
+using Global = __attribute__((address_space(1))) T*;
+
+template <class T, class P>
+__device__ __forceinline__ Global<T> global(P* p)
+{
+    return (Global<T>)p;
 }
 
 struct V4 {
     float x[4];
 };
 
-// Elements i .. i+3 of p.  FAST: all four exist and lie at an aligned
-// address.  Else those below n; the others are 0.
-template <bool FAST>
-__device__ __forceinline__ V4 load4(const float* p, int i, int n)
+// What a workgroup works on: U units of kBlock elements, a part of a piece.
+template <int U>
+struct Part {
+    int64_t off;        // of its tensor
+    int n;              // elements, none if not above 0
+    bool whole;
+};
+
+// Workgroup b of a launch has part b % (kPiece / U units) of its piece.
+template <int U>
+__device__ __forceinline__ int32_t record_of(const Table& t)
 {
-    if constexpr (FAST) {
-        const f32x4 a = __builtin_nontemporal_load(
-            reinterpret_cast<const f32x4*>(p + i));
-        return {a.x, a.y, a.z, a.w};
-    }
-    if (i + 4 <= n) {
-        const f32x4 a = *reinterpret_cast<const f32x4_4*>(p + i);
-        return {a.x, a.y, a.z, a.w};
-    }
-    V4 r = {0, 0, 0, 0};
+    return t.tensor[t.first + (int32_t)(blockIdx.x / (4 / U))];
+}
+
+template <int U>
+__device__ __forceinline__ Part<U> part_of(const Table& t, const Rec& r)
+{
+    const int32_t p = t.first + (int32_t)(blockIdx.x / (4 / U));
+    Part<U> q;
+    q.off = (int64_t)(p - r.piece0) * kPiece +
+            (int)(blockIdx.x % (4 / U)) * (U * kBlock);
+    const int64_t left = r.numel - q.off;
+    q.whole = left >= U * kBlock;
+    q.n = q.whole ? U * kBlock : (int)left;
+    return q;
+}
+
+// How a part is accessed.  kAligned: all its elements exist, at addresses
+// aligned to four of them.  kWhole: all exist, at any addresses.  kEdge: those
+// below n exist.
+constexpr int kAligned = 0, kWhole = 1, kEdge = 2;
+
+// Four elements as they lie in memory.  Kept so until all loads of a part are
+// on their way: a conversion waits for its load.
+template <class T>
+struct Raw;
+template <>
+struct Raw<float> {
+    f32x4 x;
+};
+template <>
+struct Raw<uint16_t> {
+    u32x2 x;
+};
+
+__device__ __forceinline__ V4 wide(const Raw<float>& r)
+{
+    return {r.x.x, r.x.y, r.x.z, r.x.w};
+}
+
+__device__ __forceinline__ V4 wide(const Raw<uint16_t>& r)
+{
+    return {bf16_lo(r.x.x), bf16_hi(r.x.x), bf16_lo(r.x.y), bf16_hi(r.x.y)};
+}
+
+// Elements i .. i+3 of p; 0 for those from n on.
+template <int MODE>
+__device__ __forceinline__ Raw<float> load4(Global<const float> p, int i,
+                                            int n)
+{
+    if constexpr (MODE == kAligned)
+        return {__builtin_nontemporal_load((Global<const f32x4>)(p + i))};
+    if (MODE == kWhole || i + 4 <= n)
+        return {__builtin_nontemporal_load((Global<const f32x4_4>)(p + i))};
+    Raw<float> r = {{0, 0, 0, 0}};
 #pragma unroll
     for (int j = 0; j < 3; ++j)
         if (i + j < n)
@@ -134,38 +230,35 @@ __device__ __forceinline__ V4 load4(const float* p, int i, int n)
     return r;
 }
 
-template <bool FAST>
-__device__ __forceinline__ V4 load4(const uint16_t* p, int i, int n)
+template <int MODE>
+__device__ __forceinline__ Raw<uint16_t> load4(Global<const uint16_t> p,
+                                               int i, int n)
 {
-    u32x2 a;
-    if constexpr (FAST) {
-        a = __builtin_nontemporal_load(reinterpret_cast<const u32x2*>(p + i));
-    } else if (i + 4 <= n) {
-        a = *reinterpret_cast<const u32x2_2*>(p + i);
-    } else {
-        V4 r = {0, 0, 0, 0};
+    if constexpr (MODE == kAligned)
+        return {__builtin_nontemporal_load((Global<const u32x2>)(p + i))};
+    if (MODE == kWhole || i + 4 <= n)
+        return {__builtin_nontemporal_load((Global<const u32x2_2>)(p + i))};
+    Raw<uint16_t> r = {{0, 0}};
 #pragma unroll
-        for (int j = 0; j < 3; ++j)
-            if (i + j < n)
-                r.x[j] = __uint_as_float((uint32_t)p[i + j] << 16);
-        return r;
-    }
-    return {bf16_lo(a.x), bf16_hi(a.x), bf16_lo(a.y), bf16_hi(a.y)};
+    for (int j = 0; j < 3; ++j)
+        if (i + j < n)
+            r.x[j / 2] |= (uint32_t)p[i + j] << (16 * (j % 2));
+    return r;
 }
 
-// Stores of a piece whose first element is at p (wave-uniform): streamed on
-// to HBM where it is whole, else element by element below n.
-template <bool FAST>
-__device__ __forceinline__ void store4(float* p, int i, int n, const V4& r)
+// Stores of a part whose first element is at p (wave-uniform): streamed on to
+// HBM where they are aligned.
+template <int MODE>
+__device__ __forceinline__ void store4(Global<float> p, int i, int n,
+                                       const V4& r)
 {
-    if constexpr (FAST) {
-        zsdev::stream_store(p, kPiece * 4u, (uint32_t)i * 4u,
-                            f32x4{r.x[0], r.x[1], r.x[2], r.x[3]});
+    const f32x4 q = {r.x[0], r.x[1], r.x[2], r.x[3]};
+    if constexpr (MODE == kAligned) {
+        zsdev::stream_store((void*)p, (uint32_t)n * 4u, (uint32_t)i * 4u, q);
         return;
     }
-    if (i + 4 <= n) {
-        *reinterpret_cast<f32x4_4*>(p + i) =
-            f32x4{r.x[0], r.x[1], r.x[2], r.x[3]};
+    if (MODE == kWhole || i + 4 <= n) {
+        __builtin_nontemporal_store(q, (Global<f32x4_4>)(p + i));
         return;
     }
 #pragma unroll
@@ -174,35 +267,32 @@ __device__ __forceinline__ void store4(float* p, int i, int n, const V4& r)
             p[i + j] = r.x[j];
 }
 
-template <bool FAST>
-__device__ __forceinline__ void store4(uint16_t* p, int i, int n, const V4& r)
+template <int MODE>
+__device__ __forceinline__ void store4(Global<uint16_t> p, int i, int n,
+                                       const V4& r)
 {
-    const uint32_t b[4] = {to_bf16(r.x[0]), to_bf16(r.x[1]), to_bf16(r.x[2]),
-                           to_bf16(r.x[3])};
-    const u32x2 q = {b[0] | (b[1] << 16), b[2] | (b[3] << 16)};
-    if constexpr (FAST) {
-        zsdev::stream_store(p, kPiece * 2u, (uint32_t)i * 2u, q);
+    const u32x2 q = {to_bf16(r.x[0], r.x[1]), to_bf16(r.x[2], r.x[3])};
+    if constexpr (MODE == kAligned) {
+        zsdev::stream_store((void*)p, (uint32_t)n * 2u, (uint32_t)i * 2u, q);
         return;
     }
-    if (i + 4 <= n) {
-        *reinterpret_cast<u32x2_2*>(p + i) = q;
+    if (MODE == kWhole || i + 4 <= n) {
+        __builtin_nontemporal_store(q, (Global<u32x2_2>)(p + i));
         return;
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j)
         if (i + j < n)
-            p[i + j] = (uint16_t)b[j];
+            p[i + j] = (uint16_t)(q[j / 2] >> (16 * (j % 2)));
 }
 
-// Four codes in a word.
-template <bool FAST>
-__device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int i, int n)
+// Four codes in a word (codes are always aligned to four).
+template <int MODE>
+__device__ __forceinline__ uint32_t load_codes(Global<const uint8_t> p, int i,
+                                               int n)
 {
-    if constexpr (FAST)
-        return __builtin_nontemporal_load(
-            reinterpret_cast<const uint32_t*>(p + i));
-    if (i + 4 <= n)
-        return *reinterpret_cast<const uint32_t*>(p + i);
+    if (MODE != kEdge || i + 4 <= n)
+        return __builtin_nontemporal_load((Global<const uint32_t>)(p + i));
     uint32_t r = 0;
 #pragma unroll
     for (int j = 0; j < 3; ++j)
@@ -211,16 +301,16 @@ __device__ __forceinline__ uint32_t load_codes(const uint8_t* p, int i, int n)
     return r;
 }
 
-template <bool FAST>
-__device__ __forceinline__ void store_codes(uint8_t* p, int i, int n,
+template <int MODE>
+__device__ __forceinline__ void store_codes(Global<uint8_t> p, int i, int n,
                                             uint32_t q)
 {
-    if constexpr (FAST) {
-        zsdev::stream_store(p, kPiece, (uint32_t)i, q);
+    if constexpr (MODE != kEdge) {
+        zsdev::stream_store((void*)p, (uint32_t)n, (uint32_t)i, q);
         return;
     }
     if (i + 4 <= n) {
-        *reinterpret_cast<uint32_t*>(p + i) = q;
+        *(Global<uint32_t>)(p + i) = q;
         return;
     }
 #pragma unroll
@@ -229,109 +319,294 @@ __device__ __forceinline__ void store_codes(uint8_t* p, int i, int n,
             p[i + j] = (uint8_t)(q >> (8 * j));
 }
 
-// The sum over W slices in rank order, from the first (so that the sign of a
-// zero sum is its own), then the mean.  All loads of a batch of slices come
-// before its adds.
-template <bool FAST, int WT, class G>
-__device__ __forceinline__ void mean4(const G* g0, int64_t gs, int n, int W,
-                                      float fw, float invw, int pow2,
-                                      V4 (&g)[kUnits])
-{
-    const int lane = (int)threadIdx.x;
-    if constexpr (WT == 1) {
+// Elements of a part's gradients from the ranks, WT of them at compile time
+// (0: as many as there are, eight at a time): all loads, then the sum in rank
+// order from the first (so that the sign of a zero sum is its own) and the
+// mean.
+template <int MODE, int U, int WT, class T>
+struct Gradients {
+    static constexpr int NB = WT > 0 ? WT : 8;
+    Raw<T> x[NB][U];
+
+    __device__ __forceinline__ void load(Global<const T> g0, int64_t gs,
+                                         int s0, int W, int n)
+    {
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k)
-            g[k] = load4<FAST>(g0, 4 * (k * kWave + lane), n);
-        return;
+        for (int s = 0; s < NB; ++s)
+            if (WT > 0 || s0 + s < W)
+#pragma unroll
+                for (int k = 0; k < U; ++k)
+                    x[s][k] = load4<MODE>(
+                        g0 + (int64_t)(s0 + s) * gs,
+                        4 * (k * kWave + (int)threadIdx.x), n);
     }
-    constexpr int NB = 4;
-#pragma unroll
-    for (int k = 0; k < kUnits; ++k)
-        g[k] = load4<FAST>(g0, 4 * (k * kWave + lane), n);
-#pragma unroll 1
-    for (int s0 = 1; s0 < W; s0 += NB) {
-        V4 x[NB][kUnits];
+
+    __device__ __forceinline__ void add(int s0, int W, V4 (&g)[U]) const
+    {
 #pragma unroll
         for (int s = 0; s < NB; ++s)
-            if (s0 + s < W)
+            if (WT > 0 || s0 + s < W)
 #pragma unroll
-                for (int k = 0; k < kUnits; ++k)
-                    x[s][k] = load4<FAST>(g0 + (int64_t)(s0 + s) * gs,
-                                          4 * (k * kWave + lane), n);
-#pragma unroll
-        for (int s = 0; s < NB; ++s)
-            if (s0 + s < W)
-#pragma unroll
-                for (int k = 0; k < kUnits; ++k)
+                for (int k = 0; k < U; ++k) {
+                    const V4 y = wide(x[s][k]);
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        g[k].x[j] = g[k].x[j] + x[s][k].x[j];
+                        g[k].x[j] =
+                            s0 + s == 0 ? y.x[j] : g[k].x[j] + y.x[j];
+                }
     }
+
+    // The mean, the first slices loaded by load(g0, gs, 0, W, n).
+    __device__ __forceinline__ void mean(Global<const T> g0, int64_t gs,
+                                         const Ranks& r, int n, V4 (&g)[U])
+    {
+        add(0, r.W, g);
+        if constexpr (WT == 0)
+            for (int s0 = NB; s0 < r.W; s0 += NB) {
+                load(g0, gs, s0, r.W, n);
+                add(s0, r.W, g);
+            }
+        if constexpr (WT == 1)
+            return;
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k)
+        for (int k = 0; k < U; ++k)
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            g[k].x[j] = pow2 ? g[k].x[j] * invw : g[k].x[j] / fw;
-}
+            for (int j = 0; j < 4; ++j)
+                if (WT > 0 ? (WT & (WT - 1)) == 0 : r.pow2 != 0)
+                    g[k].x[j] = g[k].x[j] * r.invw;
+                else
+                    g[k].x[j] = g[k].x[j] / r.fw;
+    }
+};
 
 // ---- codes
-
-// The largest of a wave's unsigned numbers, in every lane: bits of |x| order
-// as |x| does, with infinity above all numbers and NaN above infinity.
-__device__ __forceinline__ uint32_t wave_max(uint32_t x)
-{
-#define ZS_DPP_MAX(ctrl, rows)                                               \
-    {                                                                        \
-        const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(            \
-            0, (int)x, ctrl, rows, 0xf, false);                              \
-        x = x > y ? x : y;                                                   \
-    }
-    ZS_DPP_MAX(0x111, 0xf)      // row_shr 1, 2, 4, 8: lane 15 of each row
-    ZS_DPP_MAX(0x112, 0xf)
-    ZS_DPP_MAX(0x114, 0xf)
-    ZS_DPP_MAX(0x118, 0xf)
-    ZS_DPP_MAX(0x142, 0xa)      // row_bcast 15 into rows 1 and 3
-    ZS_DPP_MAX(0x143, 0xc)      // row_bcast 31 into rows 2 and 3
-#undef ZS_DPP_MAX
-    return (uint32_t)__builtin_amdgcn_readlane((int)x, 63);
-}
 
 __device__ __forceinline__ uint32_t abs_bits(float x)
 {
     return __float_as_uint(x) & 0x7fffffffu;
 }
 
-// S and f32(top^2 / A) of a block whose largest |x| has the bits a.
-template <int TOP>
-__device__ __forceinline__ void scale_of(uint32_t a, float& S, float& inv)
+template <int CTRL>
+__device__ __forceinline__ uint32_t max_dpp(uint32_t x)
 {
-    constexpr float kTop2 = (float)(TOP * TOP);
-    const float A = __uint_as_float(a);
-    S = A * (float)(1.0 / (double)(TOP * TOP));
-    inv = kTop2 / A;
-    if (a < 0x0d800000u) {              // below 2^-100
-        S = 0.0f;
-        inv = 0.0f;
+    const uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(
+        0, (int)x, CTRL, 0xf, 0xf, true);
+    return max(x, y);
+}
+constexpr int kRor1 = 0x121, kRor2 = 0x122, kRor4 = 0x124, kRor8 = 0x128;
+
+// a's upper 32 lanes change places with b's lower ones; the larger of each.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b)
+{
+    const auto p = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    return max(p[0], p[1]);
+}
+
+// a's rows 1 and 3 (of 16 lanes) change places with b's rows 0 and 2; the
+// larger of each.
+__device__ __forceinline__ uint32_t max_rows(uint32_t a, uint32_t b)
+{
+    const auto p = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    return max(p[0], p[1]);
+}
+
+// The largest of each unit's m and r over the wave, as bits: those of |x|
+// order as |x| does, with infinity above all numbers and NaN above infinity.
+// The 2 U reductions go together, m in the lower and r in the upper lanes: of
+// unit k, m's largest is in lane 16 k and r's in lane 32 + 16 k (and their
+// neighbours).
+template <int U>
+__device__ __forceinline__ uint32_t wave_max(const uint32_t (&m)[U],
+                                             const uint32_t (&r)[U])
+{
+    static_assert(U == 1 || U == 2, "a row of 16 lanes to each of m and r");
+    uint32_t x[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+        x[k] = max_halves(m[k], r[k]);
+    uint32_t y = max_rows(x[0], x[U - 1]);
+    y = max_dpp<kRor4>(max_dpp<kRor8>(y));
+    return max_dpp<kRor1>(max_dpp<kRor2>(y));
+}
+
+// The root of x, correctly rounded, for x in [2^-96, infinity).  From the
+// reciprocal root y: g = x y, then g + (x - g g) y / 2.  These four operations
+// after y gave the rounded root for every such x (all were compared); the
+// compiler's root takes 17.
+__device__ __forceinline__ float root_of(float x)
+{
+    const float y = __builtin_amdgcn_rsqf(x);
+    const float g = x * y;
+    return __builtin_fmaf(__builtin_fmaf(-g, g, x), 0.5f * y, g);
+}
+
+// The roots of U units, correctly rounded; 0, smaller and larger values take
+// the compiler's form.
+template <int U>
+__device__ __forceinline__ void roots(const float (&x)[U][4],
+                                      float (&r)[U][4])
+{
+    float lo = INFINITY;
+    uint32_t hi = 0;
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            lo = fminf(lo, x[k][j]);
+            hi = max(hi, __float_as_uint(x[k][j]));
+        }
+    if (__builtin_expect(__any(lo < 0x1p-96f || hi >= 0x7f800000u), 0)) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                r[k][j] = sqrtf(x[k][j]);
+        return;
     }
-    if (a >= 0x7f800000u) {             // an infinity or a NaN
-        S = __uint_as_float(0x7fc00000u);
-        inv = 0.0f;
-    }
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            r[k][j] = root_of(x[k][j]);
 }
 
 // The whole number q with (q - 1/2)^2 <= y < (q + 1/2)^2, y >= 0, as a float.
 // The hardware's root is within an ulp; less 2^-10 the guess is q or one
-// below it, and (q + 1/2)^2 = (q^2 + 1/4) + q is exact in fp32 up to 255.
+// below it, and (q + 1/2)^2 = q (q + 1) + 1/4 is exact in fp32 up to 255.
 __device__ __forceinline__ float root_code(float y)
 {
-    float q = floorf(__builtin_amdgcn_sqrtf(y) + (0.5f - 0x1p-10f));
-    const float up = __builtin_fmaf(q, q, 0.25f) + q;
-    return up <= y ? q + 1.0f : q;
+    const float q = floorf(__builtin_amdgcn_sqrtf(y) + (0.5f - 0x1p-10f));
+    return __builtin_fmaf(q, q + 1.0f, 0.25f) <= y ? q + 1.0f : q;
+}
+
+// Low bytes of four words.
+__device__ __forceinline__ uint32_t low_bytes(uint32_t a, uint32_t b,
+                                              uint32_t c, uint32_t d)
+{
+    return __builtin_amdgcn_perm(b, a, 0x0c0c0400u) |
+           __builtin_amdgcn_perm(d, c, 0x04000c0cu);
+}
+
+// Codes of four m whose scaled sizes are |m| im, and of four roots.
+//
+// The hardware's root s of y is within 2^-16 of the true one below 256, so
+// the whole number nearest to s is the code unless s is within 2^-15 of
+// halfway between two: about one unit in 30 has such a value (2^-14 for each
+// of 512 codes) and takes root_code().  Adding 2^23 (for m with its sign
+// 1.5 2^23) rounds s to a whole number, which is then the sum's low byte, in
+// two's complement.
+constexpr float kNear = 0.5f - 0x1p-15f;
+
+__device__ __forceinline__ void codes(const float (&m)[4],
+                                      const float (&r)[4], float im, float ir,
+                                      uint32_t& cm, uint32_t& cr)
+{
+    float tm[4], tr[4], ym[4], yr[4], far = 0.0f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        ym[j] = fabsf(m[j]) * im;
+        const float s = copysignf(__builtin_amdgcn_sqrtf(ym[j]), m[j]);
+        tm[j] = s + 0x1.8p+23f;
+        const float dm = s - (tm[j] - 0x1.8p+23f);
+        // a root that is not 0 keeps a code of 1: y is at least 2^-123 there
+        // and is lifted to 0.36
+        yr[j] = r[j] * ir;
+        yr[j] = __builtin_amdgcn_fmed3f(yr[j], 0.36f, yr[j] * 0x1p+125f);
+        const float u = __builtin_amdgcn_sqrtf(yr[j]);
+        tr[j] = u + 0x1p+23f;
+        const float dr = u - (tr[j] - 0x1p+23f);
+        far = fmaxf(far, fmaxf(fabsf(dm), fabsf(dr)));
+    }
+    if (__builtin_expect(__any(!(far < kNear)), 0)) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            tm[j] = copysignf(root_code(ym[j]), m[j]) + 0x1.8p+23f;
+            tr[j] = root_code(yr[j]) + 0x1p+23f;
+        }
+    }
+    cm = low_bytes(__float_as_uint(tm[0]), __float_as_uint(tm[1]),
+                   __float_as_uint(tm[2]), __float_as_uint(tm[3]));
+    cr = low_bytes(__float_as_uint(tr[0]), __float_as_uint(tr[1]),
+                   __float_as_uint(tr[2]), __float_as_uint(tr[3]));
+}
+
+constexpr float kTopM = 127.0f * 127.0f, kTopR = 255.0f * 255.0f;
+
+// Holds U units' m and roots of v: codes, and scales in the lanes that
+// wave_max() has them in.
+template <int U>
+__device__ __forceinline__ void hold(const float (&m)[U][4],
+                                     const float (&r)[U][4],
+                                     uint32_t (&cm)[U], uint32_t (&cr)[U],
+                                     float& S)
+{
+    uint32_t am[U], ar[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        am[k] = max(max(abs_bits(m[k][0]), abs_bits(m[k][1])),
+                    max(abs_bits(m[k][2]), abs_bits(m[k][3])));
+        ar[k] = max(max(abs_bits(r[k][0]), abs_bits(r[k][1])),
+                    max(abs_bits(r[k][2]), abs_bits(r[k][3])));
+    }
+    const uint32_t a = wave_max<U>(am, ar);
+    const float A = __uint_as_float(a);
+    const bool upper = threadIdx.x >= 32;
+    const float top = upper ? kTopR : kTopM;
+    S = A * (upper ? (float)(1.0 / 65025.0) : (float)(1.0 / 16129.0));
+    // top / A, correctly rounded for every A of [2^-100, 2^126) (all were
+    // compared)
+    const float rcp = __builtin_amdgcn_rcpf(A);
+    const float q0 = top * rcp;
+    float inv = __builtin_fmaf(__builtin_fmaf(-A, q0, top), rcp, q0);
+    const bool odd = __any(a - 0x0d800000u >= 0x7e800000u - 0x0d800000u);
+    if (__builtin_expect(odd, 0)) {
+        inv = top / A;
+        if (a < 0x0d800000u)            // below 2^-100
+            S = inv = 0.0f;
+        if (a >= 0x7f800000u)           // an infinity or a NaN
+            S = __uint_as_float(0x7fc00000u);
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        const int at = 16 * k;
+        auto lane = [](float x, int i) {
+            return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+                (int)__float_as_uint(x), i));
+        };
+        codes(m[k], r[k], lane(inv, at), lane(inv, at + 32), cm[k], cr[k]);
+        if (__builtin_expect(odd, 0)) {
+            cm[k] = lane(S, at) == lane(S, at) ? cm[k] : 0;
+            cr[k] = lane(S, at + 32) == lane(S, at + 32) ? cr[k] : 0;
+        }
+    }
+}
+
+// Writes what hold() gave for a part.
+template <int MODE, int U>
+__device__ __forceinline__ void store_held(Global<uint8_t> mp,
+                                           Global<uint8_t> vp,
+                                           Global<float> msp,
+                                           Global<float> vsp, int n,
+                                           const uint32_t (&cm)[U],
+                                           const uint32_t (&cr)[U], float S)
+{
+    const int lane = (int)threadIdx.x;
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (MODE == kEdge && k * kBlock >= n)
+            break;
+        store_codes<MODE>(mp, 4 * (k * kWave + lane), n, cm[k]);
+        store_codes<MODE>(vp, 4 * (k * kWave + lane), n, cr[k]);
+    }
+    const int k = lane % 32 / 16;
+    if (lane % 16 == 0 && k < U && (MODE != kEdge || k * kBlock < n))
+        (lane < 32 ? msp : vsp)[k] = S;
 }
 
 // ---- the step
 
-// g c, or no step at all: *sumsq not finite.
+// The factor of the gradients; false for no step at all: *sumsq negative or
+// not finite.
 __device__ __forceinline__ bool clip_of(const double* sumsq, float max_norm,
                                         float& c)
 {
@@ -342,179 +617,183 @@ __device__ __forceinline__ bool clip_of(const double* sumsq, float max_norm,
     const double norm = sqrt(s);
     if (norm > (double)max_norm)
         c = (float)((double)max_norm / norm);
-    return s - s == 0.0;
+    return norm - norm == 0.0;
 }
 
 // Kinds of weights.
 constexpr int kMaster = 0, kBf16 = 1, kF32 = 2;
 
-template <bool FAST, int WM>
+template <int MODE, int U, int WM>
 struct Weights {
-    V4 w[kUnits];
-    __device__ void load(const Rec& r, int64_t off, int n)
+    using T = std::conditional_t<WM == kBf16, uint16_t, float>;
+    Raw<T> x[U];
+
+    __device__ __forceinline__ void load(const Rec& r, int64_t off, int n)
     {
+        const Global<const T> p =
+            global<const T>(WM == kMaster ? r.master : r.param) + off;
 #pragma unroll
-        for (int k = 0; k < kUnits; ++k) {
-            const int i = 4 * (k * kWave + (int)threadIdx.x);
-            if constexpr (WM == kMaster)
-                w[k] = load4<FAST>(r.master + off, i, n);
-            else if constexpr (WM == kBf16)
-                w[k] = load4<FAST>(static_cast<const uint16_t*>(r.param) +
-                                   off, i, n);
-            else
-                w[k] = load4<FAST>(static_cast<const float*>(r.param) + off,
-                                   i, n);
-        }
-    }
-    __device__ void store(const Rec& r, int64_t off, int n, int k) const
-    {
-        const int i = 4 * (k * kWave + (int)threadIdx.x);
-        if constexpr (WM == kMaster)
-            store4<FAST>(r.master + off, i, n, w[k]);
-        if constexpr (WM == kF32)
-            store4<FAST>(static_cast<float*>(r.param) + off, i, n, w[k]);
-        else
-            store4<FAST>(static_cast<uint16_t*>(r.param) + off, i, n, w[k]);
+        for (int k = 0; k < U; ++k)
+            x[k] = load4<MODE>(p, 4 * (k * kWave + (int)threadIdx.x), n);
     }
 };
 
-template <bool FAST, int WM, int WT, class G>
-__device__ __forceinline__ void step32_piece(const StepArgs& a, const Rec& r,
-                                             int64_t off, int n)
+template <int MODE, int WM>
+__device__ __forceinline__ void store_weights(const Rec& r, int64_t off,
+                                              int i, int n, const V4& w)
 {
-    float* const mp = static_cast<float*>(r.m) + off;
-    float* const vp = static_cast<float*>(r.v) + off;
+    if constexpr (WM == kMaster)
+        store4<MODE>(global<float>(r.master) + off, i, n, w);
+    using T = std::conditional_t<WM == kF32, float, uint16_t>;
+    store4<MODE>(global<T>(r.param) + off, i, n, w);
+}
+
+template <int MODE, int U, int WM, int WT, class G>
+__device__ __forceinline__ void step32_part(const StepArgs& a, const Rec& r,
+                                            int64_t off, int n)
+{
+    const Global<float> mp = global<float>(r.m) + off;
+    const Global<float> vp = global<float>(r.v) + off;
+    const Global<const G> gp = global<const G>(r.grad) + off;
     const int lane = (int)threadIdx.x;
-    Weights<FAST, WM> w;
-    V4 m[kUnits], v[kUnits], g[kUnits];
-    w.load(r, off, n);
+    Weights<MODE, U, WM> wx;
+    Raw<float> mx[U], vx[U];
+    Gradients<MODE, U, WT, G> gx;
+    wx.load(r, off, n);
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        m[k] = load4<FAST>(mp, 4 * (k * kWave + lane), n);
-        v[k] = load4<FAST>(vp, 4 * (k * kWave + lane), n);
+    for (int k = 0; k < U; ++k) {
+        mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), n);
+        vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), n);
     }
-    mean4<FAST, WT>(static_cast<const G*>(r.grad) + off, r.gstride, n, a.W,
-                    a.fw, a.invw, a.pow2, g);
+    gx.load(gp, r.gstride, 0, a.ranks.W, n);
     const Hp h = a.hp[r.group];
     float c;
     if (!clip_of(a.sumsq, a.max_norm, c))
         return;
+    V4 g[U];
+    gx.mean(gp, r.gstride, a.ranks, n, g);
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
+    for (int k = 0; k < U; ++k) {
+        V4 w = wide(wx.x[k]), m = wide(mx[k]), v = wide(vx[k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float gi = g[k].x[j] * c;
-            const float mi = h.b1 * m[k].x[j] + h.omb1 * gi;
-            const float vi = h.b2 * v[k].x[j] + h.omb2 * (gi * gi);
-            const float den = sqrtf(vi) / h.bc2s + h.eps;
-            w.w[k].x[j] = w.w[k].x[j] * h.dec - h.ss * (mi / den);
-            m[k].x[j] = mi;
-            v[k].x[j] = vi;
+            m.x[j] = h.b1 * m.x[j] + h.omb1 * gi;
+            v.x[j] = h.b2 * v.x[j] + h.omb2 * (gi * gi);
+            const float den = sqrtf(v.x[j]) / h.bc2s + h.eps;
+            w.x[j] = w.x[j] * h.dec - h.ss * (m.x[j] / den);
         }
-        w.store(r, off, n, k);
-        store4<FAST>(mp, 4 * (k * kWave + lane), n, m[k]);
-        store4<FAST>(vp, 4 * (k * kWave + lane), n, v[k]);
+        const int i = 4 * (k * kWave + lane);
+        store_weights<MODE, WM>(r, off, i, n, w);
+        store4<MODE>(mp, i, n, m);
+        store4<MODE>(vp, i, n, v);
     }
 }
 
-template <bool FAST, int WM, int WT, class G>
-__device__ __forceinline__ void step8_piece(const StepArgs& a, const Rec& r,
-                                            int64_t off, int n)
+template <int MODE, int U, int WM, int WT, class G>
+__device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
+                                           int64_t off, int n)
 {
-    uint8_t* const mp = static_cast<uint8_t*>(r.m) + off;
-    uint8_t* const vp = static_cast<uint8_t*>(r.v) + off;
-    float* const msp = r.ms + off / kBlock;
-    float* const vsp = r.vs + off / kBlock;
+    const Global<uint8_t> mp = global<uint8_t>(r.m) + off;
+    const Global<uint8_t> vp = global<uint8_t>(r.v) + off;
+    const Global<float> msp = global<float>(r.ms) + off / kBlock;
+    const Global<float> vsp = global<float>(r.vs) + off / kBlock;
+    const Global<const G> gp = global<const G>(r.grad) + off;
     const int lane = (int)threadIdx.x;
-    Weights<FAST, WM> w;
-    uint32_t mq[kUnits], vq[kUnits];
-    float ms[kUnits], vs[kUnits];
-    V4 g[kUnits];
-    w.load(r, off, n);
+    Weights<MODE, U, WM> wx;
+    uint32_t mq[U], vq[U];
+    float ms[U], vs[U];
+    Gradients<MODE, U, WT, G> gx;
+    wx.load(r, off, n);
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        mq[k] = load_codes<FAST>(mp, 4 * (k * kWave + lane), n);
-        vq[k] = load_codes<FAST>(vp, 4 * (k * kWave + lane), n);
-        const bool there = FAST || k * kBlock < n;
+    for (int k = 0; k < U; ++k) {
+        mq[k] = load_codes<MODE>(mp, 4 * (k * kWave + lane), n);
+        vq[k] = load_codes<MODE>(vp, 4 * (k * kWave + lane), n);
+        const bool there = MODE != kEdge || k * kBlock < n;
         ms[k] = there ? msp[k] : 0.0f;
         vs[k] = there ? vsp[k] : 0.0f;
     }
-    mean4<FAST, WT>(static_cast<const G*>(r.grad) + off, r.gstride, n, a.W,
-                    a.fw, a.invw, a.pow2, g);
+    gx.load(gp, r.gstride, 0, a.ranks.W, n);
     const Hp h = a.hp[r.group];
-    float c;
+    float c = 1.0f;
     if (!clip_of(a.sumsq, a.max_norm, c))
         return;
+    V4 g[U];
+    gx.mean(gp, r.gstride, a.ranks, n, g);
+    if (a.sumsq) {
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        if (!FAST && k * kBlock >= n)
-            break;
-        float m[4], root[4];
-        uint32_t am = 0, ar = 0;
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                g[k].x[j] *= c;
+    }
+    // elements behind the tensor's last are 0 here: gradients and codes were
+    // loaded as 0
+    float m[U][4], v[U][4], root[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float qm = (float)(int8_t)(mq[k] >> (8 * j));
             const float qv = (float)(uint8_t)(vq[k] >> (8 * j));
             const float r0 = (qv * qv) * vs[k];
-            const float gi = g[k].x[j] * c;
-            const float mi = h.b1 * ((qm * fabsf(qm)) * ms[k]) + h.omb1 * gi;
-            const float vi = h.b2 * (r0 * r0) + h.omb2 * (gi * gi);
-            root[j] = sqrtf(vi);
-            m[j] = mi;
-            const float den = root[j] * h.ibc2s + h.eps;
-            w.w[k].x[j] = w.w[k].x[j] * h.dec -
-                          h.ss * (mi * __builtin_amdgcn_rcpf(den));
-            // elements behind the tensor's last are 0 here: gradient and
-            // codes were loaded as 0
-            am = max(am, abs_bits(mi));
-            ar = max(ar, abs_bits(root[j]));
+            const float gi = g[k].x[j];
+            m[k][j] = h.b1 * ((qm * fabsf(qm)) * ms[k]) + h.omb1 * gi;
+            v[k][j] = h.b2 * (r0 * r0) + h.omb2 * (gi * gi);
         }
-        w.store(r, off, n, k);
-        float Sm, im, Sr, ir;
-        scale_of<127>(wave_max(am), Sm, im);
-        scale_of<255>(wave_max(ar), Sr, ir);
-        uint32_t cm = 0, cr = 0;
+    roots<U>(v, root);
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+        if (MODE == kEdge && k * kBlock >= n)
+            break;
+        V4 w = wide(wx.x[k]);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            float q = root_code(fabsf(m[j]) * im);
-            cm |= ((uint32_t)(int)copysignf(q, m[j]) & 0xffu) << (8 * j);
-            q = root_code(root[j] * ir);
-            if (root[j] > 0.0f && ir > 0.0f)
-                q = fmaxf(q, 1.0f);
-            cr |= (uint32_t)q << (8 * j);
+            const float rden = __builtin_amdgcn_rcpf(
+                __builtin_fmaf(root[k][j], h.ibc2s, h.eps));
+            w.x[j] = __builtin_fmaf(-(h.ss * m[k][j]), rden,
+                                    w.x[j] * h.dec);
         }
-        store_codes<FAST>(mp, 4 * (k * kWave + lane), n, cm);
-        store_codes<FAST>(vp, 4 * (k * kWave + lane), n, cr);
-        if (lane == 0) {
-            msp[k] = Sm;
-            vsp[k] = Sr;
-        }
+        store_weights<MODE, WM>(r, off, 4 * (k * kWave + lane), n, w);
     }
+    uint32_t cm[U], cr[U];
+    float S;
+    hold<U>(m, root, cm, cr, S);
+    store_held<MODE, U>(mp, vp, msp, vsp, n, cm, cr, S);
 }
 
-template <int BITS, int WM, int WT, class G>
+template <int BITS, int MODE, int U, int WM, int WT, class G>
+__device__ __forceinline__ void step_part(const StepArgs& a, const Rec& r,
+                                          int64_t off, int n)
+{
+    if constexpr (BITS == 32)
+        step32_part<MODE, U, WM, WT, G>(a, r, off, n);
+    else
+        step8_part<MODE, U, WM, WT, G>(a, r, off, n);
+}
+
+template <int BITS, int U, int WM, int WT, class G>
 __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
 {
-    const int32_t p = (int32_t)blockIdx.x;
-    const Rec& r = a.t.recs[a.t.tensor[p]];
-    const int64_t off = (int64_t)(p - r.piece0) * kPiece;
-    const int64_t left = r.numel - off;
-    if (left >= kPiece && r.vec) {
-        if constexpr (BITS == 32)
-            step32_piece<true, WM, WT, G>(a, r, off, kPiece);
-        else
-            step8_piece<true, WM, WT, G>(a, r, off, kPiece);
-    } else {
-        const int n = left < kPiece ? (int)left : kPiece;
-        if constexpr (BITS == 32)
-            step32_piece<false, WM, WT, G>(a, r, off, n);
-        else
-            step8_piece<false, WM, WT, G>(a, r, off, n);
-    }
+    const Rec r = a.t.recs[record_of<U>(a.t)];
+    const Part<U> q = part_of<U>(a.t, r);
+    if (q.n <= 0)
+        return;
+    if (q.whole && r.vec)
+        step_part<BITS, kAligned, U, WM, WT, G>(a, r, q.off, U * kBlock);
+    else if (q.whole)
+        step_part<BITS, kWhole, U, WM, WT, G>(a, r, q.off, U * kBlock);
+    else
+        step_part<BITS, kEdge, U, WM, WT, G>(a, r, q.off, q.n);
 }
 
 // ---- the sum of squares
 
+// Squares and sums are fp64, whose fused multiply-add runs at fp32's rate
+// here, so no gradient's square overflows or is lost.  Each wave takes a run
+// of consecutive pieces (32 waves to a CU), workgroups leave one partial sum
+// each, and a second launch adds those: 70 us over 218 M bf16 elements, 5 of
+// them the second launch.
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / kWave;
 constexpr int kSumMaxGroups = 2048;     // workgroups, and so partial sums
@@ -524,24 +803,23 @@ struct SumArgs {
     Table t;
     int32_t pieces;
     int32_t per_wave;           // consecutive pieces of a wave
-    int32_t W;
-    float fw, invw;
-    int32_t pow2;
+    Ranks ranks;
     double* out;                // one per workgroup
 };
 
-template <bool FAST, int WT, class G>
+template <int MODE, int WT, class G>
 __device__ __forceinline__ double sum_piece(const SumArgs& a, const Rec& r,
                                             int64_t off, int n)
 {
-    V4 g[kUnits];
-    const int lane = (int)threadIdx.x & (kWave - 1);
-    (void)lane;
-    mean4<FAST, WT>(static_cast<const G*>(r.grad) + off, r.gstride, n, a.W,
-                    a.fw, a.invw, a.pow2, g);
+    constexpr int U = 4;
+    const Global<const G> gp = global<const G>(r.grad) + off;
+    Gradients<MODE, U, WT, G> gx;
+    gx.load(gp, r.gstride, 0, a.ranks.W, n);
+    V4 g[U];
+    gx.mean(gp, r.gstride, a.ranks, n, g);
     double s = 0.0;
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k)
+    for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const double x = g[k].x[j];
@@ -567,6 +845,66 @@ __device__ __forceinline__ double group_sum(double s, double* lds, int waves)
     return s;
 }
 
+// The sum over n whole pieces from p on, one rank's: sixteen bytes of a lane to
+// a load, and while a batch of kSumBatch loads is added the next is on its way
+// (70 us; piece by piece with a lookup and a wait each 75).
+constexpr int kSumBatch = 4;
+
+template <class G>
+__device__ __forceinline__ double square_sum(u32x4 x)
+{
+    double s = 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const double lo = sizeof(G) == 4 ? __uint_as_float(x[j])
+                                         : bf16_lo(x[j]);
+        s = __builtin_fma(lo, lo, s);
+        if constexpr (sizeof(G) == 2) {
+            const double hi = bf16_hi(x[j]);
+            s = __builtin_fma(hi, hi, s);
+        }
+    }
+    return s;
+}
+
+template <class G>
+__device__ __forceinline__ double sum_run(Global<const G> p, int n)
+{
+    constexpr int kStep = 16 / sizeof(G) * kWave;       // elements of a load
+    constexpr int kLoads = kPiece / kStep;              // of a piece
+    static_assert(kSumBatch % kLoads == 0, "batches of whole pieces");
+    using Load = std::conditional_t<sizeof(G) == 2, u32x4_2, u32x4_4>;
+    p += (int)threadIdx.x * (16 / (int)sizeof(G));
+    const int loads = n * kLoads;
+    u32x4 x[kSumBatch], y[kSumBatch];
+#pragma unroll
+    for (int k = 0; k < kSumBatch; ++k)
+        if (k < loads)
+            x[k] = __builtin_nontemporal_load(
+                (Global<const Load>)(p + k * kStep));
+    double s[kSumBatch] = {};
+    for (int i = 0; i < loads; i += kSumBatch) {
+        p += kSumBatch * kStep;
+#pragma unroll
+        for (int k = 0; k < kSumBatch; ++k)
+            if (i + kSumBatch + k < loads)
+                y[k] = __builtin_nontemporal_load(
+                    (Global<const Load>)(p + k * kStep));
+#pragma unroll
+        for (int k = 0; k < kSumBatch; ++k)
+            if (i + k < loads)
+                s[k] += square_sum<G>(x[k]);
+#pragma unroll
+        for (int k = 0; k < kSumBatch; ++k)
+            x[k] = y[k];
+    }
+    double t = 0.0;
+#pragma unroll
+    for (int k = 0; k < kSumBatch; ++k)
+        t += s[k];
+    return t;
+}
+
 // threadIdx.x: lane, threadIdx.y: wave of the workgroup.
 template <int WT, class G>
 __global__ __launch_bounds__(kSumThreads) void sumsq_kernel(SumArgs a)
@@ -577,15 +915,22 @@ __global__ __launch_bounds__(kSumThreads) void sumsq_kernel(SumArgs a)
         ((int64_t)blockIdx.x * kSumWaves + wave) * a.per_wave;
     const int64_t end = min(first + a.per_wave, (int64_t)a.pieces);
     double s = 0.0;
-    for (int64_t p = first; p < end; ++p) {
-        const Rec& r = a.t.recs[a.t.tensor[p]];
-        const int64_t off = (int64_t)((int32_t)p - r.piece0) * kPiece;
+    for (int64_t p = first; p < end;) {
+        const Rec r = a.t.recs[a.t.tensor[p]];
+        const int64_t off = (p - r.piece0) * kPiece;
         const int64_t left = r.numel - off;
-        if (left >= kPiece && r.vec)
-            s += sum_piece<true, WT, G>(a, r, off, kPiece);
-        else
-            s += sum_piece<false, WT, G>(a, r, off,
-                                         left < kPiece ? (int)left : kPiece);
+        if (left < kPiece) {
+            s += sum_piece<kEdge, WT, G>(a, r, off, (int)left);
+            ++p;
+        } else if constexpr (WT == 1) {
+            const int n = (int)min(left / kPiece, end - p);
+            s += sum_run<G>(global<const G>(r.grad) + off, n);
+            p += n;
+        } else {
+            s += r.vec ? sum_piece<kAligned, WT, G>(a, r, off, kPiece)
+                       : sum_piece<kWhole, WT, G>(a, r, off, kPiece);
+            ++p;
+        }
     }
     s = group_sum(s, lds, kSumWaves);
     if (threadIdx.x == 0 && threadIdx.y == 0)
@@ -612,74 +957,57 @@ struct ConvertArgs {
     Table from, to;
 };
 
-template <bool FAST>
-__device__ __forceinline__ void pack_piece(const Rec& f, const Rec& t,
-                                           int64_t off, int n)
+template <int MODE, int U>
+__device__ __forceinline__ void pack_part(const Rec& f, const Rec& t,
+                                          int64_t off, int n)
 {
-    const float* const mp = static_cast<const float*>(f.m) + off;
-    const float* const vp = static_cast<const float*>(f.v) + off;
+    const Global<const float> mp = global<const float>(f.m) + off;
+    const Global<const float> vp = global<const float>(f.v) + off;
     const int lane = (int)threadIdx.x;
-    V4 m[kUnits], v[kUnits];
+    Raw<float> mx[U], vx[U];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        m[k] = load4<FAST>(mp, 4 * (k * kWave + lane), n);
-        v[k] = load4<FAST>(vp, 4 * (k * kWave + lane), n);
+    for (int k = 0; k < U; ++k) {
+        mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), n);
+        vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), n);
     }
+    float m[U][4], v[U][4], root[U][4];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        if (!FAST && k * kBlock >= n)
-            break;
-        uint32_t am = 0, ar = 0;
+    for (int k = 0; k < U; ++k)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            v[k].x[j] = sqrtf(v[k].x[j]);
-            am = max(am, abs_bits(m[k].x[j]));
-            ar = max(ar, abs_bits(v[k].x[j]));
+            m[k][j] = mx[k].x[j];
+            v[k][j] = vx[k].x[j];
         }
-        float Sm, im, Sr, ir;
-        scale_of<127>(wave_max(am), Sm, im);
-        scale_of<255>(wave_max(ar), Sr, ir);
-        uint32_t cm = 0, cr = 0;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            float q = root_code(fabsf(m[k].x[j]) * im);
-            cm |= ((uint32_t)(int)copysignf(q, m[k].x[j]) & 0xffu)
-                  << (8 * j);
-            q = root_code(v[k].x[j] * ir);
-            if (v[k].x[j] > 0.0f && ir > 0.0f)
-                q = fmaxf(q, 1.0f);
-            cr |= (uint32_t)q << (8 * j);
-        }
-        store_codes<FAST>(static_cast<uint8_t*>(t.m) + off,
-                          4 * (k * kWave + lane), n, cm);
-        store_codes<FAST>(static_cast<uint8_t*>(t.v) + off,
-                          4 * (k * kWave + lane), n, cr);
-        if (lane == 0) {
-            t.ms[off / kBlock + k] = Sm;
-            t.vs[off / kBlock + k] = Sr;
-        }
-    }
+    roots<U>(v, root);
+    uint32_t cm[U], cr[U];
+    float S;
+    hold<U>(m, root, cm, cr, S);
+    store_held<MODE, U>(global<uint8_t>(t.m) + off, global<uint8_t>(t.v) + off,
+                        global<float>(t.ms) + off / kBlock,
+                        global<float>(t.vs) + off / kBlock, n, cm, cr, S);
 }
 
-template <bool FAST>
-__device__ __forceinline__ void unpack_piece(const Rec& f, const Rec& t,
-                                             int64_t off, int n)
+template <int MODE, int U>
+__device__ __forceinline__ void unpack_part(const Rec& f, const Rec& t,
+                                            int64_t off, int n)
 {
-    const uint8_t* const mp = static_cast<const uint8_t*>(f.m) + off;
-    const uint8_t* const vp = static_cast<const uint8_t*>(f.v) + off;
+    const Global<const uint8_t> mp = global<const uint8_t>(f.m) + off;
+    const Global<const uint8_t> vp = global<const uint8_t>(f.v) + off;
+    const Global<const float> msp = global<const float>(f.ms) + off / kBlock;
+    const Global<const float> vsp = global<const float>(f.vs) + off / kBlock;
     const int lane = (int)threadIdx.x;
-    uint32_t mq[kUnits], vq[kUnits];
-    float ms[kUnits], vs[kUnits];
+    uint32_t mq[U], vq[U];
+    float ms[U], vs[U];
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
-        mq[k] = load_codes<FAST>(mp, 4 * (k * kWave + lane), n);
-        vq[k] = load_codes<FAST>(vp, 4 * (k * kWave + lane), n);
-        const bool there = FAST || k * kBlock < n;
-        ms[k] = there ? f.ms[off / kBlock + k] : 0.0f;
-        vs[k] = there ? f.vs[off / kBlock + k] : 0.0f;
+    for (int k = 0; k < U; ++k) {
+        mq[k] = load_codes<MODE>(mp, 4 * (k * kWave + lane), n);
+        vq[k] = load_codes<MODE>(vp, 4 * (k * kWave + lane), n);
+        const bool there = MODE != kEdge || k * kBlock < n;
+        ms[k] = there ? msp[k] : 0.0f;
+        vs[k] = there ? vsp[k] : 0.0f;
     }
 #pragma unroll
-    for (int k = 0; k < kUnits; ++k) {
+    for (int k = 0; k < U; ++k) {
         V4 m, v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -689,34 +1017,36 @@ __device__ __forceinline__ void unpack_piece(const Rec& f, const Rec& t,
             m.x[j] = (qm * fabsf(qm)) * ms[k];
             v.x[j] = r0 * r0;
         }
-        store4<FAST>(static_cast<float*>(t.m) + off, 4 * (k * kWave + lane),
-                     n, m);
-        store4<FAST>(static_cast<float*>(t.v) + off, 4 * (k * kWave + lane),
-                     n, v);
+        store4<MODE>(global<float>(t.m) + off, 4 * (k * kWave + lane), n, m);
+        store4<MODE>(global<float>(t.v) + off, 4 * (k * kWave + lane), n, v);
     }
 }
 
-template <bool PACK>
+template <bool PACK, int MODE, int U>
+__device__ __forceinline__ void convert_part(const Rec& f, const Rec& t,
+                                             int64_t off, int n)
+{
+    if constexpr (PACK)
+        pack_part<MODE, U>(f, t, off, n);
+    else
+        unpack_part<MODE, U>(f, t, off, n);
+}
+
+template <bool PACK, int U>
 __global__ __launch_bounds__(kWave) void convert_kernel(ConvertArgs a)
 {
-    const int32_t p = (int32_t)blockIdx.x;
-    const int32_t i = a.from.tensor[p];
-    const Rec& f = a.from.recs[i];
-    const Rec& t = a.to.recs[i];
-    const int64_t off = (int64_t)(p - f.piece0) * kPiece;
-    const int64_t left = f.numel - off;
-    if (left >= kPiece && f.vec && t.vec) {
-        if constexpr (PACK)
-            pack_piece<true>(f, t, off, kPiece);
-        else
-            unpack_piece<true>(f, t, off, kPiece);
-    } else {
-        const int n = left < kPiece ? (int)left : kPiece;
-        if constexpr (PACK)
-            pack_piece<false>(f, t, off, n);
-        else
-            unpack_piece<false>(f, t, off, n);
-    }
+    const int32_t i = record_of<U>(a.from);
+    const Rec f = a.from.recs[i];
+    const Rec t = a.to.recs[i];
+    const Part<U> q = part_of<U>(a.from, f);
+    if (q.n <= 0)
+        return;
+    if (q.whole && f.vec && t.vec)
+        convert_part<PACK, kAligned, U>(f, t, q.off, U * kBlock);
+    else if (q.whole)
+        convert_part<PACK, kWhole, U>(f, t, q.off, U * kBlock);
+    else
+        convert_part<PACK, kEdge, U>(f, t, q.off, q.n);
 }
 
 }  // namespace
@@ -742,7 +1072,7 @@ struct zs_tensors {
     std::vector<Rec> recs;              // of those with elements
     std::vector<int32_t> tensor;        // record of each piece
     std::vector<Span> states;           // m, v and scales, in order
-    Table table = {nullptr, nullptr};
+    Table table = {nullptr, nullptr, 0};
     int device = -1;
 };
 
@@ -944,13 +1274,9 @@ int check_launch(const char* what)
     return ZS_OK;
 }
 
-template <class A>
-void set_world(A& a, int32_t W)
+Ranks ranks_of(int32_t W)
 {
-    a.W = W;
-    a.fw = (float)W;
-    a.invw = (float)(1.0 / (double)W);
-    a.pow2 = (W & (W - 1)) == 0;
+    return {W, (float)W, (float)(1.0 / (double)W), (W & (W - 1)) == 0};
 }
 
 int make_hp(const zs_adamw& hp, int64_t t, int32_t k, Hp& h)
@@ -981,34 +1307,89 @@ int make_hp(const zs_adamw& hp, int64_t t, int32_t k, Hp& h)
     return ZS_OK;
 }
 
-template <int BITS, int WM, class G>
-void launch_step_w(const StepArgs& a, uint32_t pieces, hipStream_t s)
+// One launch for each kLaunchPieces pieces of a list: run(first, workgroups),
+// U units to a workgroup.
+template <int U, class Run>
+void for_pieces(int64_t pieces, Run run)
 {
-    if (a.W == 1)
-        step_kernel<BITS, WM, 1, G><<<pieces, kWave, 0, s>>>(a);
-    else
-        step_kernel<BITS, WM, 0, G><<<pieces, kWave, 0, s>>>(a);
+    for (int64_t first = 0; first < pieces; first += kLaunchPieces)
+        run((int32_t)first,
+            (uint32_t)(std::min(pieces - first, kLaunchPieces) * (4 / U)));
+}
+
+// Bytes that a CU's workgroups may have on their way from memory in a step.  A
+// few workgroups per CU keep the rows that are open in HBM few (zs_step.hip
+// has the same cap): with fp32 states 50 KB run the 124 M step in 537 us
+// against 573 at as many workgroups as fit, W = 8 in 1392 against 1508 and
+// fp32 weights in 914 against 1018; 44 to 60 KB are within 2 %.  The 8-bit
+// step's waves live longer for their arithmetic and want 80 to 100 KB (318
+// against 328 us with a master, W = 4 763 against 824).
+constexpr int kInFlight32 = 50 << 10, kInFlight8 = 88 << 10;
+
+// Workgroups of U units per CU, 0 for as many as fit.
+template <int BITS, int U, int WM, class G>
+int step_residency(int32_t W)
+{
+    constexpr int kRest = (WM == kBf16 ? 2 : 4) + (BITS == 32 ? 8 : 2);
+    const int64_t bytes =
+        (int64_t)U * kBlock * (kRest + (int64_t)W * (int)sizeof(G));
+    const int64_t k = (BITS == 32 ? kInFlight32 : kInFlight8) / bytes;
+    return k > 24 ? 0 : (int)std::max<int64_t>(k, 6);
+}
+
+template <int BITS, int WM, int WT, class G>
+void launch_step_u(const zs_tensors* L, StepArgs& a, hipStream_t s)
+{
+    constexpr int U = BITS == 32 ? kStep32Units : kStep8Units;
+    const unsigned lds =
+        zs::residency_lds(step_residency<BITS, U, WM, G>(a.ranks.W));
+    for_pieces<U>((int64_t)L->tensor.size(), [&](int32_t first,
+                                                 uint32_t groups) {
+        a.t.first = first;
+        step_kernel<BITS, U, WM, WT, G><<<groups, kWave, lds, s>>>(a);
+    });
+}
+
+template <int BITS, int WM, class G>
+void launch_step_w(const zs_tensors* L, StepArgs& a, hipStream_t s)
+{
+    switch (a.ranks.W) {
+    case 1: launch_step_u<BITS, WM, 1, G>(L, a, s); break;
+    case 2: launch_step_u<BITS, WM, 2, G>(L, a, s); break;
+    case 4: launch_step_u<BITS, WM, 4, G>(L, a, s); break;
+    case 8: launch_step_u<BITS, WM, 8, G>(L, a, s); break;
+    default: launch_step_u<BITS, WM, 0, G>(L, a, s); break;
+    }
 }
 
 template <int BITS, class G>
-void launch_step_wm(const zs_tensors* L, const StepArgs& a, hipStream_t s)
+void launch_step_wm(const zs_tensors* L, StepArgs& a, hipStream_t s)
 {
-    const uint32_t pieces = (uint32_t)L->tensor.size();
     if (L->master)
-        launch_step_w<BITS, kMaster, G>(a, pieces, s);
+        launch_step_w<BITS, kMaster, G>(L, a, s);
     else if (L->param_type == ZS_BF16)
-        launch_step_w<BITS, kBf16, G>(a, pieces, s);
+        launch_step_w<BITS, kBf16, G>(L, a, s);
     else
-        launch_step_w<BITS, kF32, G>(a, pieces, s);
+        launch_step_w<BITS, kF32, G>(L, a, s);
 }
 
 template <int BITS>
-void launch_step(const zs_tensors* L, const StepArgs& a, hipStream_t s)
+void launch_step(const zs_tensors* L, StepArgs& a, hipStream_t s)
 {
     if (L->grad_type == ZS_BF16)
         launch_step_wm<BITS, uint16_t>(L, a, s);
     else
         launch_step_wm<BITS, float>(L, a, s);
+}
+
+template <bool PACK, int U>
+void launch_convert(int64_t pieces, ConvertArgs& a, hipStream_t s)
+{
+    const unsigned lds = zs::residency_lds(PACK ? 0 : kUnpackResidency);
+    for_pieces<U>(pieces, [&](int32_t first, uint32_t groups) {
+        a.from.first = a.to.first = first;
+        convert_kernel<PACK, U><<<groups, kWave, lds, s>>>(a);
+    });
 }
 
 // How zs_tensors_sumsq cuts a list: pieces of each wave, and workgroups.
@@ -1027,7 +1408,7 @@ template <class G>
 void launch_sum(const SumArgs& a, uint32_t groups, hipStream_t s)
 {
     const dim3 block(kWave, kSumWaves);
-    if (a.W == 1)
+    if (a.ranks.W == 1)
         sumsq_kernel<1, G><<<groups, block, 0, s>>>(a);
     else
         sumsq_kernel<0, G><<<groups, block, 0, s>>>(a);
@@ -1095,6 +1476,8 @@ extern "C" int zs_tensors_upload(zs_tensors* L, void* table, int64_t bytes,
         return rc;
     if (need == 0)
         return ZS_OK;
+    if (L->table.recs)
+        return fail(ZS_EINVAL, "the list has its table");
     if (!table) return fail(ZS_EINVAL, "table is NULL");
     if (!aligned(table, 16))
         return fail(ZS_EALIGN, "table not 16-byte aligned");
@@ -1167,7 +1550,7 @@ extern "C" int zs_tensors_step(const zs_tensors* L, const zs_adamw* hp,
     a.t = L->table;
     a.sumsq = sumsq;
     a.max_norm = max_norm;
-    set_world(a, L->world);
+    a.ranks = ranks_of(L->world);
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     if (L->state == ZS_STATE_32)
         launch_step<32>(L, a, s);
@@ -1214,7 +1597,7 @@ extern "C" int zs_tensors_sumsq(const zs_tensors* L, double* out,
     sum_plan(L, a.per_wave, groups);
     a.t = L->table;
     a.pieces = (int32_t)L->tensor.size();
-    set_world(a, L->world);
+    a.ranks = ranks_of(L->world);
     a.out = groups > 1 ? static_cast<double*>(workspace) : out;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     if (L->grad_type == ZS_BF16)
@@ -1245,12 +1628,12 @@ extern "C" int zs_tensors_convert(const zs_tensors* from,
         return rc;
     if (int rc = check_list(to, "to"))
         return rc;
-    const ConvertArgs a = {from->table, to->table};
-    const uint32_t pieces = (uint32_t)from->tensor.size();
+    ConvertArgs a = {from->table, to->table};
+    const int64_t pieces = (int64_t)from->tensor.size();
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     if (pack)
-        convert_kernel<true><<<pieces, kWave, 0, s>>>(a);
+        launch_convert<true, kPackUnits>(pieces, a, s);
     else
-        convert_kernel<false><<<pieces, kWave, 0, s>>>(a);
+        launch_convert<false, kUnpackUnits>(pieces, a, s);
     return check_launch("state conversion kernel");
 }

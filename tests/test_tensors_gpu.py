@@ -54,8 +54,8 @@ class Arena:
     def put(self, x, shift=0):
         """A device tensor of numpy array x (uint16: bf16), `shift` elements
         past a 256-byte boundary."""
-        whole = torch.full((x.nbytes + 1024,), 0x5a, dtype=torch.uint8,
-                           device="cuda")
+        whole = torch.full((x.nbytes + 1024 + shift * x.itemsize,), 0x5a,
+                           dtype=torch.uint8, device="cuda")
         at = -whole.data_ptr() % 256 + 256 + shift * x.itemsize
         view = whole[at:at + x.nbytes]
         view.copy_(torch.from_numpy(bits(x).reshape(-1)))
@@ -79,7 +79,10 @@ class Case:
     """A list with its host copy."""
 
     def __init__(self, sizes, bits=32, weights="master", grad="bf16",
-                 world=1, shift=0, seed=0, groups=None, edit=None):
+                 world=1, shift=0, seed=0, groups=None, edit=None,
+                 apart=0):
+        """shift: elements past an aligned address; apart: as many more with
+        every array."""
         rng = np.random.default_rng(seed)
         self.arena, self.sizes, self.world = Arena(), sizes, world
         self.bits, self.weights, self.grad = bits, weights, grad
@@ -108,8 +111,8 @@ class Case:
                 edit(h)
             self.host.append(h)
             d = {k: self.arena.put(
-                x, 0 if bits == 8 and k in ("m", "v") else shift)
-                for k, x in h.items() if k != "grad"}
+                x, 0 if bits == 8 and k in ("m", "v") else shift + apart * i)
+                for i, (k, x) in enumerate(h.items()) if k != "grad"}
             stride = n + 5 + shift if world > 1 else n
             rows = np.zeros((world, stride), h["grad"].dtype)
             rows[:, :n] = h["grad"]
@@ -249,9 +252,15 @@ def test_step_many_ranks(bits, world):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
-@pytest.mark.parametrize("shift", [2, 3])
-def test_step_other_addresses(bits, shift):
-    c = Case([5, 1024, 2051], bits, "master", "bf16", 2, shift)
+@pytest.mark.parametrize("weights", ["master", "f32"])
+@pytest.mark.parametrize("shift,apart", [
+    (2, 0), (3, 0), (4, 0), (8, 0), (31, 0), (33, 0), (37, 0), (60, 0),
+    (63, 0), (0, 1), (0, 4), (0, 32), (3, 16), (1, 64)])
+def test_step_other_addresses(bits, weights, shift, apart):
+    """Arrays that share their distance from a line, or four elements, or
+    nothing; tensors that end before the first line."""
+    c = Case([1, 3, 5, 40, 64, 255, 256, 300, 1024, 2051], bits, weights,
+             "bf16", 2, shift, apart=apart)
     c.step()
     c.expect()
     c.check()
@@ -495,7 +504,7 @@ def test_empty_list():
 
 @pytest.mark.parametrize("grad", ["bf16", "f32"])
 @pytest.mark.parametrize("world", [1, 2, 3, 8])
-@pytest.mark.parametrize("shift", [0, 1])
+@pytest.mark.parametrize("shift", [0, 1, 37])
 @pytest.mark.parametrize("sizes", [[1], [768], SIZES, [33000, 5, 70001]])
 def test_sumsq(grad, world, shift, sizes):
     c = Case(sizes, 32, "f32", grad, world, shift, seed=9)
@@ -594,6 +603,35 @@ def test_convert(shift):
     zs.zs_tensors_convert(s.lists[2], s.lists[1])
     for a, b in zip(was, s.q["m"] + s.q["v"]):
         same(a, b)
+
+
+@pytest.mark.parametrize("shift", [0, 1, 37])
+def test_convert_of_step_lists(shift):
+    """A step's fp32 list, whose units start at a line, to 8 bits and back
+    while both step on."""
+    sizes = [1, 300, 1024, 5003]
+    a = Case(sizes, 32, "bf16", shift=shift, seed=3)
+    b = Case(sizes, 8, "bf16", shift=shift, seed=4)
+    a.step()
+    a.expect()
+    a.check()
+    zs.zs_tensors_convert(a.list, b.list)
+    for x, y, d in zip(a.host, b.host, b.dev):
+        q = OT.hold(x["m"], x["v"])
+        y.update(m=q[0].astype(np.int8), m_scale=q[1],
+                 v=q[2].astype(np.uint8), v_scale=q[3])
+        for k in ("m", "m_scale", "v", "v_scale"):
+            same(d[k], y[k])
+    b.step()
+    b.expect()
+    b.check()
+    zs.zs_tensors_convert(b.list, a.list)
+    for x, y in zip(a.host, b.host):
+        x["m"], x["v"] = OT.stands_for(y["m"], y["m_scale"], y["v"],
+                                       y["v_scale"])
+    a.step(t=9)
+    a.expect(t=9)
+    a.check()
 
 
 def test_convert_at_every_border():

@@ -85,8 +85,8 @@ struct Rec {
     int64_t numel;
     int32_t piece0;     // its first piece
     int32_t group;
-    int32_t vec;        // every pointer and stride aligned to four elements
-    int32_t pad;
+    int32_t pre;        // places before its first element in that piece
+    int32_t vec;        // four elements from a unit's start on are aligned
 };
 static_assert(sizeof(Rec) == 88, "the header states it");
 
@@ -157,11 +157,12 @@ struct V4 {
     float x[4];
 };
 
-// What a workgroup works on: U units of kBlock elements, a part of a piece.
+// What a workgroup works on: U units of kBlock places, a part of a piece.  The
+// tensor's elements are those of its places lo .. n-1.
 template <int U>
 struct Part {
-    int64_t off;        // of its tensor
-    int n;              // elements, none if not above 0
+    int64_t off;        // the first place's element of the tensor, or below 0
+    int lo, n;
     bool whole;
 };
 
@@ -178,16 +179,17 @@ __device__ __forceinline__ Part<U> part_of(const Table& t, const Rec& r)
     const int32_t p = t.first + (int32_t)(blockIdx.x / (4 / U));
     Part<U> q;
     q.off = (int64_t)(p - r.piece0) * kPiece +
-            (int)(blockIdx.x % (4 / U)) * (U * kBlock);
+            (int)(blockIdx.x % (4 / U)) * (U * kBlock) - r.pre;
     const int64_t left = r.numel - q.off;
-    q.whole = left >= U * kBlock;
-    q.n = q.whole ? U * kBlock : (int)left;
+    q.lo = q.off < 0 ? (int)-q.off : 0;
+    q.n = left < U * kBlock ? (int)left : U * kBlock;
+    q.whole = q.lo == 0 && q.n == U * kBlock;
     return q;
 }
 
 // How a part is accessed.  kAligned: all its elements exist, at addresses
 // aligned to four of them.  kWhole: all exist, at any addresses.  kEdge: those
-// below n exist.
+// of lo .. n-1 exist.
 constexpr int kAligned = 0, kWhole = 1, kEdge = 2;
 
 // Four elements as they lie in memory.  Kept so until all loads of a part are
@@ -213,110 +215,127 @@ __device__ __forceinline__ V4 wide(const Raw<uint16_t>& r)
     return {bf16_lo(r.x.x), bf16_hi(r.x.x), bf16_lo(r.x.y), bf16_hi(r.x.y)};
 }
 
-// Elements i .. i+3 of p; 0 for those from n on.
+// A part's places lo .. n-1.
+struct Places {
+    int lo, n;
+    // whether place i, or places i .. i+3, are of it
+    __device__ __forceinline__ bool has(int i) const
+    {
+        return i >= lo && i < n;
+    }
+    __device__ __forceinline__ bool has4(int i) const
+    {
+        return i >= lo && i + 4 <= n;
+    }
+};
+
+// Elements at places i .. i+3 of p; 0 where there is none.
 template <int MODE>
 __device__ __forceinline__ Raw<float> load4(Global<const float> p, int i,
-                                            int n)
+                                            Places q)
 {
     if constexpr (MODE == kAligned)
         return {__builtin_nontemporal_load((Global<const f32x4>)(p + i))};
-    if (MODE == kWhole || i + 4 <= n)
+    if (MODE == kWhole || q.has4(i))
         return {__builtin_nontemporal_load((Global<const f32x4_4>)(p + i))};
     Raw<float> r = {{0, 0, 0, 0}};
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-        if (i + j < n)
+    for (int j = 0; j < 4; ++j)
+        if (q.has(i + j))
             r.x[j] = p[i + j];
     return r;
 }
 
 template <int MODE>
 __device__ __forceinline__ Raw<uint16_t> load4(Global<const uint16_t> p,
-                                               int i, int n)
+                                               int i, Places q)
 {
     if constexpr (MODE == kAligned)
         return {__builtin_nontemporal_load((Global<const u32x2>)(p + i))};
-    if (MODE == kWhole || i + 4 <= n)
+    if (MODE == kWhole || q.has4(i))
         return {__builtin_nontemporal_load((Global<const u32x2_2>)(p + i))};
     Raw<uint16_t> r = {{0, 0}};
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-        if (i + j < n)
+    for (int j = 0; j < 4; ++j)
+        if (q.has(i + j))
             r.x[j / 2] |= (uint32_t)p[i + j] << (16 * (j % 2));
     return r;
 }
 
-// Stores of a part whose first element is at p (wave-uniform): streamed on to
+// Stores of a part whose first place is at p (wave-uniform): streamed on to
 // HBM where they are aligned.
 template <int MODE>
-__device__ __forceinline__ void store4(Global<float> p, int i, int n,
+__device__ __forceinline__ void store4(Global<float> p, int i, Places q,
                                        const V4& r)
 {
-    const f32x4 q = {r.x[0], r.x[1], r.x[2], r.x[3]};
+    const f32x4 x = {r.x[0], r.x[1], r.x[2], r.x[3]};
     if constexpr (MODE == kAligned) {
-        zsdev::stream_store((void*)p, (uint32_t)n * 4u, (uint32_t)i * 4u, q);
+        zsdev::stream_store((void*)p, (uint32_t)q.n * 4u, (uint32_t)i * 4u,
+                            x);
         return;
     }
-    if (MODE == kWhole || i + 4 <= n) {
-        __builtin_nontemporal_store(q, (Global<f32x4_4>)(p + i));
+    if (MODE == kWhole || q.has4(i)) {
+        __builtin_nontemporal_store(x, (Global<f32x4_4>)(p + i));
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-        if (i + j < n)
+    for (int j = 0; j < 4; ++j)
+        if (q.has(i + j))
             p[i + j] = r.x[j];
 }
 
 template <int MODE>
-__device__ __forceinline__ void store4(Global<uint16_t> p, int i, int n,
+__device__ __forceinline__ void store4(Global<uint16_t> p, int i, Places q,
                                        const V4& r)
 {
-    const u32x2 q = {to_bf16(r.x[0], r.x[1]), to_bf16(r.x[2], r.x[3])};
+    const u32x2 x = {to_bf16(r.x[0], r.x[1]), to_bf16(r.x[2], r.x[3])};
     if constexpr (MODE == kAligned) {
-        zsdev::stream_store((void*)p, (uint32_t)n * 2u, (uint32_t)i * 2u, q);
+        zsdev::stream_store((void*)p, (uint32_t)q.n * 2u, (uint32_t)i * 2u,
+                            x);
         return;
     }
-    if (MODE == kWhole || i + 4 <= n) {
-        __builtin_nontemporal_store(q, (Global<u32x2_2>)(p + i));
+    if (MODE == kWhole || q.has4(i)) {
+        __builtin_nontemporal_store(x, (Global<u32x2_2>)(p + i));
         return;
     }
 #pragma unroll
-    for (int j = 0; j < 3; ++j)
-        if (i + j < n)
-            p[i + j] = (uint16_t)(q[j / 2] >> (16 * (j % 2)));
+    for (int j = 0; j < 4; ++j)
+        if (q.has(i + j))
+            p[i + j] = (uint16_t)(x[j / 2] >> (16 * (j % 2)));
 }
 
-// Four codes in a word (codes are always aligned to four).
+// Four codes in a word (codes are always aligned to four, and none lies before
+// a part's first place).
 template <int MODE>
 __device__ __forceinline__ uint32_t load_codes(Global<const uint8_t> p, int i,
-                                               int n)
+                                               Places q)
 {
-    if (MODE != kEdge || i + 4 <= n)
+    if (MODE != kEdge || q.has4(i))
         return __builtin_nontemporal_load((Global<const uint32_t>)(p + i));
     uint32_t r = 0;
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-        if (i + j < n)
+        if (q.has(i + j))
             r |= (uint32_t)p[i + j] << (8 * j);
     return r;
 }
 
 template <int MODE>
-__device__ __forceinline__ void store_codes(Global<uint8_t> p, int i, int n,
-                                            uint32_t q)
+__device__ __forceinline__ void store_codes(Global<uint8_t> p, int i,
+                                            Places q, uint32_t x)
 {
     if constexpr (MODE != kEdge) {
-        zsdev::stream_store((void*)p, (uint32_t)n, (uint32_t)i, q);
+        zsdev::stream_store((void*)p, (uint32_t)q.n, (uint32_t)i, x);
         return;
     }
-    if (i + 4 <= n) {
-        *(Global<uint32_t>)(p + i) = q;
+    if (q.has4(i)) {
+        *(Global<uint32_t>)(p + i) = x;
         return;
     }
 #pragma unroll
     for (int j = 0; j < 3; ++j)
-        if (i + j < n)
-            p[i + j] = (uint8_t)(q >> (8 * j));
+        if (q.has(i + j))
+            p[i + j] = (uint8_t)(x >> (8 * j));
 }
 
 // Elements of a part's gradients from the ranks, WT of them at compile time
@@ -329,7 +348,7 @@ struct Gradients {
     Raw<T> x[NB][U];
 
     __device__ __forceinline__ void load(Global<const T> g0, int64_t gs,
-                                         int s0, int W, int n)
+                                         int s0, int W, Places q)
     {
 #pragma unroll
         for (int s = 0; s < NB; ++s)
@@ -338,7 +357,7 @@ struct Gradients {
                 for (int k = 0; k < U; ++k)
                     x[s][k] = load4<MODE>(
                         g0 + (int64_t)(s0 + s) * gs,
-                        4 * (k * kWave + (int)threadIdx.x), n);
+                        4 * (k * kWave + (int)threadIdx.x), q);
     }
 
     __device__ __forceinline__ void add(int s0, int W, V4 (&g)[U]) const
@@ -356,14 +375,15 @@ struct Gradients {
                 }
     }
 
-    // The mean, the first slices loaded by load(g0, gs, 0, W, n).
+    // The mean, the first slices loaded by load(g0, gs, 0, W, q).
     __device__ __forceinline__ void mean(Global<const T> g0, int64_t gs,
-                                         const Ranks& r, int n, V4 (&g)[U])
+                                         const Ranks& r, Places q,
+                                         V4 (&g)[U])
     {
         add(0, r.W, g);
         if constexpr (WT == 0)
             for (int s0 = NB; s0 < r.W; s0 += NB) {
-                load(g0, gs, s0, r.W, n);
+                load(g0, gs, s0, r.W, q);
                 add(s0, r.W, g);
             }
         if constexpr (WT == 1)
@@ -586,20 +606,20 @@ template <int MODE, int U>
 __device__ __forceinline__ void store_held(Global<uint8_t> mp,
                                            Global<uint8_t> vp,
                                            Global<float> msp,
-                                           Global<float> vsp, int n,
+                                           Global<float> vsp, Places q,
                                            const uint32_t (&cm)[U],
                                            const uint32_t (&cr)[U], float S)
 {
     const int lane = (int)threadIdx.x;
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        if (MODE == kEdge && k * kBlock >= n)
+        if (MODE == kEdge && k * kBlock >= q.n)
             break;
-        store_codes<MODE>(mp, 4 * (k * kWave + lane), n, cm[k]);
-        store_codes<MODE>(vp, 4 * (k * kWave + lane), n, cr[k]);
+        store_codes<MODE>(mp, 4 * (k * kWave + lane), q, cm[k]);
+        store_codes<MODE>(vp, 4 * (k * kWave + lane), q, cr[k]);
     }
     const int k = lane % 32 / 16;
-    if (lane % 16 == 0 && k < U && (MODE != kEdge || k * kBlock < n))
+    if (lane % 16 == 0 && k < U && (MODE != kEdge || k * kBlock < q.n))
         (lane < 32 ? msp : vsp)[k] = S;
 }
 
@@ -628,29 +648,29 @@ struct Weights {
     using T = std::conditional_t<WM == kBf16, uint16_t, float>;
     Raw<T> x[U];
 
-    __device__ __forceinline__ void load(const Rec& r, int64_t off, int n)
+    __device__ __forceinline__ void load(const Rec& r, int64_t off, Places q)
     {
         const Global<const T> p =
             global<const T>(WM == kMaster ? r.master : r.param) + off;
 #pragma unroll
         for (int k = 0; k < U; ++k)
-            x[k] = load4<MODE>(p, 4 * (k * kWave + (int)threadIdx.x), n);
+            x[k] = load4<MODE>(p, 4 * (k * kWave + (int)threadIdx.x), q);
     }
 };
 
 template <int MODE, int WM>
 __device__ __forceinline__ void store_weights(const Rec& r, int64_t off,
-                                              int i, int n, const V4& w)
+                                              int i, Places q, const V4& w)
 {
     if constexpr (WM == kMaster)
-        store4<MODE>(global<float>(r.master) + off, i, n, w);
+        store4<MODE>(global<float>(r.master) + off, i, q, w);
     using T = std::conditional_t<WM == kF32, float, uint16_t>;
-    store4<MODE>(global<T>(r.param) + off, i, n, w);
+    store4<MODE>(global<T>(r.param) + off, i, q, w);
 }
 
 template <int MODE, int U, int WM, int WT, class G>
 __device__ __forceinline__ void step32_part(const StepArgs& a, const Rec& r,
-                                            int64_t off, int n)
+                                            int64_t off, Places q)
 {
     const Global<float> mp = global<float>(r.m) + off;
     const Global<float> vp = global<float>(r.v) + off;
@@ -659,19 +679,19 @@ __device__ __forceinline__ void step32_part(const StepArgs& a, const Rec& r,
     Weights<MODE, U, WM> wx;
     Raw<float> mx[U], vx[U];
     Gradients<MODE, U, WT, G> gx;
-    wx.load(r, off, n);
+    wx.load(r, off, q);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), n);
-        vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), n);
+        mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), q);
+        vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), q);
     }
-    gx.load(gp, r.gstride, 0, a.ranks.W, n);
+    gx.load(gp, r.gstride, 0, a.ranks.W, q);
     const Hp h = a.hp[r.group];
     float c;
     if (!clip_of(a.sumsq, a.max_norm, c))
         return;
     V4 g[U];
-    gx.mean(gp, r.gstride, a.ranks, n, g);
+    gx.mean(gp, r.gstride, a.ranks, q, g);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         V4 w = wide(wx.x[k]), m = wide(mx[k]), v = wide(vx[k]);
@@ -684,15 +704,15 @@ __device__ __forceinline__ void step32_part(const StepArgs& a, const Rec& r,
             w.x[j] = w.x[j] * h.dec - h.ss * (m.x[j] / den);
         }
         const int i = 4 * (k * kWave + lane);
-        store_weights<MODE, WM>(r, off, i, n, w);
-        store4<MODE>(mp, i, n, m);
-        store4<MODE>(vp, i, n, v);
+        store_weights<MODE, WM>(r, off, i, q, w);
+        store4<MODE>(mp, i, q, m);
+        store4<MODE>(vp, i, q, v);
     }
 }
 
 template <int MODE, int U, int WM, int WT, class G>
 __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
-                                           int64_t off, int n)
+                                           int64_t off, Places q)
 {
     const Global<uint8_t> mp = global<uint8_t>(r.m) + off;
     const Global<uint8_t> vp = global<uint8_t>(r.v) + off;
@@ -704,22 +724,22 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
     uint32_t mq[U], vq[U];
     float ms[U], vs[U];
     Gradients<MODE, U, WT, G> gx;
-    wx.load(r, off, n);
+    wx.load(r, off, q);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        mq[k] = load_codes<MODE>(mp, 4 * (k * kWave + lane), n);
-        vq[k] = load_codes<MODE>(vp, 4 * (k * kWave + lane), n);
-        const bool there = MODE != kEdge || k * kBlock < n;
+        mq[k] = load_codes<MODE>(mp, 4 * (k * kWave + lane), q);
+        vq[k] = load_codes<MODE>(vp, 4 * (k * kWave + lane), q);
+        const bool there = MODE != kEdge || k * kBlock < q.n;
         ms[k] = there ? msp[k] : 0.0f;
         vs[k] = there ? vsp[k] : 0.0f;
     }
-    gx.load(gp, r.gstride, 0, a.ranks.W, n);
+    gx.load(gp, r.gstride, 0, a.ranks.W, q);
     const Hp h = a.hp[r.group];
     float c = 1.0f;
     if (!clip_of(a.sumsq, a.max_norm, c))
         return;
     V4 g[U];
-    gx.mean(gp, r.gstride, a.ranks, n, g);
+    gx.mean(gp, r.gstride, a.ranks, q, g);
     if (a.sumsq) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
@@ -744,7 +764,7 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
     roots<U>(v, root);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        if (MODE == kEdge && k * kBlock >= n)
+        if (MODE == kEdge && k * kBlock >= q.n)
             break;
         V4 w = wide(wx.x[k]);
 #pragma unroll
@@ -754,22 +774,22 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
             w.x[j] = __builtin_fmaf(-(h.ss * m[k][j]), rden,
                                     w.x[j] * h.dec);
         }
-        store_weights<MODE, WM>(r, off, 4 * (k * kWave + lane), n, w);
+        store_weights<MODE, WM>(r, off, 4 * (k * kWave + lane), q, w);
     }
     uint32_t cm[U], cr[U];
     float S;
     hold<U>(m, root, cm, cr, S);
-    store_held<MODE, U>(mp, vp, msp, vsp, n, cm, cr, S);
+    store_held<MODE, U>(mp, vp, msp, vsp, q, cm, cr, S);
 }
 
 template <int BITS, int MODE, int U, int WM, int WT, class G>
 __device__ __forceinline__ void step_part(const StepArgs& a, const Rec& r,
-                                          int64_t off, int n)
+                                          int64_t off, Places q)
 {
     if constexpr (BITS == 32)
-        step32_part<MODE, U, WM, WT, G>(a, r, off, n);
+        step32_part<MODE, U, WM, WT, G>(a, r, off, q);
     else
-        step8_part<MODE, U, WM, WT, G>(a, r, off, n);
+        step8_part<MODE, U, WM, WT, G>(a, r, off, q);
 }
 
 template <int BITS, int U, int WM, int WT, class G>
@@ -780,11 +800,12 @@ __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
     if (q.n <= 0)
         return;
     if (q.whole && r.vec)
-        step_part<BITS, kAligned, U, WM, WT, G>(a, r, q.off, U * kBlock);
+        step_part<BITS, kAligned, U, WM, WT, G>(a, r, q.off,
+                                                {0, U * kBlock});
     else if (q.whole)
-        step_part<BITS, kWhole, U, WM, WT, G>(a, r, q.off, U * kBlock);
+        step_part<BITS, kWhole, U, WM, WT, G>(a, r, q.off, {0, U * kBlock});
     else
-        step_part<BITS, kEdge, U, WM, WT, G>(a, r, q.off, q.n);
+        step_part<BITS, kEdge, U, WM, WT, G>(a, r, q.off, {q.lo, q.n});
 }
 
 // ---- the sum of squares
@@ -809,14 +830,14 @@ struct SumArgs {
 
 template <int MODE, int WT, class G>
 __device__ __forceinline__ double sum_piece(const SumArgs& a, const Rec& r,
-                                            int64_t off, int n)
+                                            int64_t off, Places q)
 {
     constexpr int U = 4;
     const Global<const G> gp = global<const G>(r.grad) + off;
     Gradients<MODE, U, WT, G> gx;
-    gx.load(gp, r.gstride, 0, a.ranks.W, n);
+    gx.load(gp, r.gstride, 0, a.ranks.W, q);
     V4 g[U];
-    gx.mean(gp, r.gstride, a.ranks, n, g);
+    gx.mean(gp, r.gstride, a.ranks, q, g);
     double s = 0.0;
 #pragma unroll
     for (int k = 0; k < U; ++k)
@@ -917,18 +938,20 @@ __global__ __launch_bounds__(kSumThreads) void sumsq_kernel(SumArgs a)
     double s = 0.0;
     for (int64_t p = first; p < end;) {
         const Rec r = a.t.recs[a.t.tensor[p]];
-        const int64_t off = (p - r.piece0) * kPiece;
+        const int64_t off = (p - r.piece0) * kPiece - r.pre;
         const int64_t left = r.numel - off;
-        if (left < kPiece) {
-            s += sum_piece<kEdge, WT, G>(a, r, off, (int)left);
+        if (left < kPiece || off < 0) {
+            s += sum_piece<kEdge, WT, G>(
+                a, r, off, {off < 0 ? (int)-off : 0,
+                            left < kPiece ? (int)left : kPiece});
             ++p;
         } else if constexpr (WT == 1) {
             const int n = (int)min(left / kPiece, end - p);
             s += sum_run<G>(global<const G>(r.grad) + off, n);
             p += n;
         } else {
-            s += r.vec ? sum_piece<kAligned, WT, G>(a, r, off, kPiece)
-                       : sum_piece<kWhole, WT, G>(a, r, off, kPiece);
+            s += r.vec ? sum_piece<kAligned, WT, G>(a, r, off, {0, kPiece})
+                       : sum_piece<kWhole, WT, G>(a, r, off, {0, kPiece});
             ++p;
         }
     }
@@ -959,7 +982,7 @@ struct ConvertArgs {
 
 template <int MODE, int U>
 __device__ __forceinline__ void pack_part(const Rec& f, const Rec& t,
-                                          int64_t off, int n)
+                                          int64_t off, Places q)
 {
     const Global<const float> mp = global<const float>(f.m) + off;
     const Global<const float> vp = global<const float>(f.v) + off;
@@ -967,8 +990,8 @@ __device__ __forceinline__ void pack_part(const Rec& f, const Rec& t,
     Raw<float> mx[U], vx[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), n);
-        vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), n);
+        mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), q);
+        vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), q);
     }
     float m[U][4], v[U][4], root[U][4];
 #pragma unroll
@@ -984,12 +1007,12 @@ __device__ __forceinline__ void pack_part(const Rec& f, const Rec& t,
     hold<U>(m, root, cm, cr, S);
     store_held<MODE, U>(global<uint8_t>(t.m) + off, global<uint8_t>(t.v) + off,
                         global<float>(t.ms) + off / kBlock,
-                        global<float>(t.vs) + off / kBlock, n, cm, cr, S);
+                        global<float>(t.vs) + off / kBlock, q, cm, cr, S);
 }
 
 template <int MODE, int U>
 __device__ __forceinline__ void unpack_part(const Rec& f, const Rec& t,
-                                            int64_t off, int n)
+                                            int64_t off, Places q)
 {
     const Global<const uint8_t> mp = global<const uint8_t>(f.m) + off;
     const Global<const uint8_t> vp = global<const uint8_t>(f.v) + off;
@@ -1000,9 +1023,9 @@ __device__ __forceinline__ void unpack_part(const Rec& f, const Rec& t,
     float ms[U], vs[U];
 #pragma unroll
     for (int k = 0; k < U; ++k) {
-        mq[k] = load_codes<MODE>(mp, 4 * (k * kWave + lane), n);
-        vq[k] = load_codes<MODE>(vp, 4 * (k * kWave + lane), n);
-        const bool there = MODE != kEdge || k * kBlock < n;
+        mq[k] = load_codes<MODE>(mp, 4 * (k * kWave + lane), q);
+        vq[k] = load_codes<MODE>(vp, 4 * (k * kWave + lane), q);
+        const bool there = MODE != kEdge || k * kBlock < q.n;
         ms[k] = there ? msp[k] : 0.0f;
         vs[k] = there ? vsp[k] : 0.0f;
     }
@@ -1017,36 +1040,45 @@ __device__ __forceinline__ void unpack_part(const Rec& f, const Rec& t,
             m.x[j] = (qm * fabsf(qm)) * ms[k];
             v.x[j] = r0 * r0;
         }
-        store4<MODE>(global<float>(t.m) + off, 4 * (k * kWave + lane), n, m);
-        store4<MODE>(global<float>(t.v) + off, 4 * (k * kWave + lane), n, v);
+        store4<MODE>(global<float>(t.m) + off, 4 * (k * kWave + lane), q, m);
+        store4<MODE>(global<float>(t.v) + off, 4 * (k * kWave + lane), q, v);
     }
 }
 
 template <bool PACK, int MODE, int U>
 __device__ __forceinline__ void convert_part(const Rec& f, const Rec& t,
-                                             int64_t off, int n)
+                                             int64_t off, Places q)
 {
     if constexpr (PACK)
-        pack_part<MODE, U>(f, t, off, n);
+        pack_part<MODE, U>(f, t, off, q);
     else
-        unpack_part<MODE, U>(f, t, off, n);
+        unpack_part<MODE, U>(f, t, off, q);
+}
+
+// Whether a record's fp32 states are aligned to four elements (its vec is of
+// its own pieces).
+__device__ __forceinline__ bool aligned16(const Rec& r)
+{
+    return (((uintptr_t)r.m | (uintptr_t)r.v) & 15) == 0;
 }
 
 template <bool PACK, int U>
 __global__ __launch_bounds__(kWave) void convert_kernel(ConvertArgs a)
 {
-    const int32_t i = record_of<U>(a.from);
+    // the pieces of the list in 8 bits, whose units are its blocks
+    const Table& held = PACK ? a.to : a.from;
+    const int32_t i = record_of<U>(held);
     const Rec f = a.from.recs[i];
     const Rec t = a.to.recs[i];
-    const Part<U> q = part_of<U>(a.from, f);
+    const Part<U> q = part_of<U>(held, PACK ? t : f);
     if (q.n <= 0)
         return;
-    if (q.whole && f.vec && t.vec)
-        convert_part<PACK, kAligned, U>(f, t, q.off, U * kBlock);
+    if (q.whole && aligned16(PACK ? f : t))
+        convert_part<PACK, kAligned, U>(f, t, q.off, {0, U * kBlock});
     else if (q.whole)
-        convert_part<PACK, kWhole, U>(f, t, q.off, U * kBlock);
+        convert_part<PACK, kWhole, U>(f, t, q.off, {0, U * kBlock});
     else
-        convert_part<PACK, kEdge, U>(f, t, q.off, q.n);
+        convert_part<PACK, kEdge, U>(f, t, q.off, {0, q.n});
 }
 
 }  // namespace
@@ -1182,6 +1214,41 @@ int check_tensor(const zs_tensors* L, int32_t k, const zs_tensor& t)
     return ZS_OK;
 }
 
+// Where a tensor's units start.  Blocks of 8-bit states start at its first
+// element; with fp32 states the units may start later, where what the step
+// writes is aligned to lines of 128 bytes, or at least everything to four
+// elements (a flat buffer's views share their distance from a line).
+void place(const zs_tensors* L, Rec& r)
+{
+    const int gs = L->grad_type == ZS_F32 ? 4 : 2;
+    const int ps = L->param_type == ZS_F32 ? 4 : 2;
+    const int ss = L->state == ZS_STATE_8 ? 1 : 4;
+    auto at = [](const void* p, int lead, int size, int to) {
+        return !p || (reinterpret_cast<uintptr_t>(p) +
+                      (uintptr_t)(lead * size)) % to == 0;
+    };
+    auto fours = [&](int lead) {
+        return at(r.grad, lead, gs, 4 * gs) && r.gstride % 4 == 0 &&
+               at(r.param, lead, ps, 4 * ps) && at(r.master, lead, 4, 16) &&
+               at(r.m, lead, ss, 4 * ss) && at(r.v, lead, ss, 4 * ss);
+    };
+    auto lines = [&](int lead) {
+        return fours(lead) && at(r.param, lead, ps, 128) &&
+               at(r.master, lead, 4, 128) && at(r.m, lead, 4, 128) &&
+               at(r.v, lead, 4, 128);
+    };
+    int lead = 0;
+    if (L->state == ZS_STATE_32 && r.param) {
+        while (lead < 64 && !lines(lead))
+            ++lead;
+        if (lead == 64)
+            for (lead = 3; lead > 0 && !fours(lead);)
+                --lead;
+    }
+    r.pre = (kBlock - lead) % kBlock;
+    r.vec = fours(lead);
+}
+
 int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)
 {
     std::vector<Span> spans;
@@ -1219,11 +1286,8 @@ int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)
         r.numel = t.numel;
         r.piece0 = (int32_t)pieces;
         r.group = t.group;
-        const int ss = L->state == ZS_STATE_8 ? 1 : 4;
-        r.vec = aligned(t.grad, 4 * gs) && r.gstride % 4 == 0 &&
-                aligned(t.param, 4 * ps) && aligned(t.master, 16) &&
-                aligned(t.m, 4 * ss) && aligned(t.v, 4 * ss);
-        pieces += (t.numel + kPiece - 1) / kPiece;
+        place(L, r);
+        pieces += (r.pre + t.numel + kPiece - 1) / kPiece;
         if (pieces > kMaxPieces)
             return fail(ZS_ERANGE, "tensors 0 to %d have too many elements",
                         k);
@@ -1629,7 +1693,8 @@ extern "C" int zs_tensors_convert(const zs_tensors* from,
     if (int rc = check_list(to, "to"))
         return rc;
     ConvertArgs a = {from->table, to->table};
-    const int64_t pieces = (int64_t)from->tensor.size();
+    // those of the list in 8 bits, as in convert_kernel
+    const int64_t pieces = (int64_t)(pack ? to : from)->tensor.size();
     hipStream_t s = static_cast<hipStream_t>(hip_stream);
     if (pack)
         launch_convert<true, kPackUnits>(pieces, a, s);

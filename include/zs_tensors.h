@@ -15,8 +15,9 @@
  * zs_tensors_sumsq and zs_tensors_convert may be captured into a HIP graph:
  * they launch kernels only and read their host arguments during the call (a
  * captured step repeats with its lr, step and max_norm).  Results do not
- * depend on what else runs, nor on the stream: every sum is taken in a
- * fixed order.
+ * depend on what else runs, nor on the stream: every sum is taken in an order
+ * that the list fixes.  Steps and conversions to 32 bits reserve LDS that they
+ * do not use, as zs_step does; zs_set_residency_cap turns it off.
  */
 #ifndef ZS_TENSORS_H
 #define ZS_TENSORS_H
@@ -47,7 +48,15 @@ extern "C" {
  *       a root that is not 0 has q >= 1, so that no later step divides by
  *       eps alone
  * A block with A below 2^-100 has S = 0 and q = 0.  One with a NaN or an
- * infinity has S = NaN and q = 0: it stands for NaN from then on. */
+ * infinity has S = NaN and q = 0: it stands for NaN from then on (with a
+ * sum of squares, below, such a step is not taken).
+ *
+ * What it costs: on noise with a mean of a tenth of its sigma, beside fp32
+ * states after 1000 steps at beta2 0.95 (4000 at 0.999), an update is off by
+ * 2 % (5 %) of its norm where the sigmas of a block's elements differ by
+ * factors of about 1.35, by 6 % (10 %) where by e, and by more than half where
+ * by e^2: the small ones then change by less than half a step of their codes.
+ * The roots of v are right on average (to 1 %, 4 % in the last case). */
 #define ZS_STATE_NONE 0
 #define ZS_STATE_32 32
 #define ZS_STATE_8  8
@@ -117,8 +126,8 @@ int zs_tensors_upload(zs_tensors* list, void* table, int64_t bytes,
                       void* hip_stream);
 
 /* One AdamW step of every tensor of the list, in one launch (one for each 2^34
- * elements).  Per element,
- * with one fp32 rounding per operation, in the order of zs_step:
+ * elements).  Per element, with one fp32 rounding per operation, in the order
+ * of zs_step:
  *   g = (G_0 + G_1 + ... + G_{W-1}) / W              (sum in rank order)
  *   g = g * c                                        (with sumsq, below)
  *   m = b1*m + (1-b1)*g;  v = b2*v + (1-b2)*(g*g)

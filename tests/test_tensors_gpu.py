@@ -762,6 +762,20 @@ def test_two_streams():
         c.check()
 
 
+@pytest.mark.parametrize("bits", [32, 8])
+def test_without_residency_cap(bits):
+    was = zs.zs_set_residency_cap(False)
+    try:
+        c = Case([70000, 5], bits, world=8)
+        c.step()
+        c.expect()
+        c.check()
+        s = States([70000])
+        s.check()
+    finally:
+        zs.zs_set_residency_cap(bool(was))
+
+
 def test_explicit_stream():
     c = Case([3000], 32)
     st = torch.cuda.Stream()

@@ -7,12 +7,12 @@
 // bf16 gradients of one rank, a master and fp32 states; 16 with 8-bit states;
 // 10 with 8-bit states and no master).  Measured on MI355X over 218 M elements
 // in nine tensors (124 M in 148 with the master), of 8 TB/s:
-//   fp32 states, W = 1: bf16 weights 6.6 TB/s, fp32 weights and gradients 6.7,
+//   fp32 states, W = 1: bf16 weights 6.7 TB/s, fp32 weights and gradients 6.7,
 //     a master 6.5; W = 2, 3, 4, 5, 8 with a master 6.6, 6.6, 6.6, 6.5, 6.6
 //     (rows of gradients at multiples of 256 bytes; at multiples of 16 every
-//     load takes a line more: 6.5, 6.4, 6.3, 6.2, 6.1)
-//   8-bit states: 6.2 (master and bf16 weights), 6.5 (fp32)
-//   to 8 bits 6.7, to 32 bits 6.2, sum of squares 6.2 (both launches)
+//     load takes a line more: 6.6, 6.3, 6.5, 6.2, 6.2)
+//   8-bit states: 6.3 (a master), 6.2 (bf16 weights), 6.5 (fp32)
+//   to 8 bits 6.8, to 32 bits 6.2, sum of squares 6.2 (both launches)
 // Large streams of the same mixes reach 6.8 here.
 //
 // Work decomposition.  A list's tensors are cut into pieces of kPiece
@@ -65,10 +65,11 @@ constexpr int64_t kMaxPieces = (int64_t(1) << 28) - 1;
 // 351 us, 391 with one, 380 with four); where those cost little it is even
 // (with a master 318 us, 316 with one).
 constexpr int kStep32Units = 1, kStep8Units = 2;
-// To 8 bits 325 us (two units 340), to 32 bits 200 us with two at 20 workgroups
-// per CU (222 at as many as fit; one unit 209).
-constexpr int kPackUnits = 1, kUnpackUnits = 2;
-constexpr int kUnpackResidency = 20;
+// To 8 bits 326 us (two units 340); to 32 bits 349 us with four at 10
+// workgroups per CU (8 and 12 within 1 %, 16 382), with two at 24 353 and as
+// many as fit 380, with one 382.
+constexpr int kPackUnits = 1, kUnpackUnits = 4;
+constexpr int kUnpackResidency = 10;
 constexpr int64_t kMaxReach = int64_t(1) << 46;
 constexpr int64_t kMaxSlices = int64_t(1) << 30;
 
@@ -86,8 +87,11 @@ struct Rec {
     int32_t piece0;     // its first piece
     int32_t group;
     int32_t pre;        // places before its first element in that piece
-    int32_t vec;        // four elements from a unit's start on are aligned
+    int32_t flags;
 };
+// Four elements from a unit's start on are aligned; so are lines of all ranks'
+// gradients.
+constexpr int32_t kRecFours = 1, kRecLines = 2;
 static_assert(sizeof(Rec) == 88, "the header states it");
 
 struct Hp {
@@ -188,9 +192,10 @@ __device__ __forceinline__ Part<U> part_of(const Table& t, const Rec& r)
 }
 
 // How a part is accessed.  kAligned: all its elements exist, at addresses
-// aligned to four of them.  kWhole: all exist, at any addresses.  kEdge: those
-// of lo .. n-1 exist.
-constexpr int kAligned = 0, kWhole = 1, kEdge = 2;
+// aligned to four of them; kLines: and so do the ranks' gradients, at lines of
+// 128 bytes.  kWhole: all exist, at any addresses.  kEdge: those of lo .. n-1
+// exist.
+constexpr int kLines = 0, kAligned = 1, kWhole = 2, kEdge = 3;
 
 // Four elements as they lie in memory.  Kept so until all loads of a part are
 // on their way: a conversion waits for its load.
@@ -229,15 +234,17 @@ struct Places {
     }
 };
 
-// Elements at places i .. i+3 of p; 0 where there is none.
-template <int MODE>
+// Elements at places i .. i+3 of p; 0 where there is none.  NT: non-temporal.
+template <int MODE, bool NT = true>
 __device__ __forceinline__ Raw<float> load4(Global<const float> p, int i,
                                             Places q)
 {
-    if constexpr (MODE == kAligned)
-        return {__builtin_nontemporal_load((Global<const f32x4>)(p + i))};
+    const auto a = (Global<const f32x4>)(p + i);
+    const auto u = (Global<const f32x4_4>)(p + i);
+    if constexpr (MODE <= kAligned)
+        return {NT ? __builtin_nontemporal_load(a) : *a};
     if (MODE == kWhole || q.has4(i))
-        return {__builtin_nontemporal_load((Global<const f32x4_4>)(p + i))};
+        return {NT ? __builtin_nontemporal_load(u) : *u};
     Raw<float> r = {{0, 0, 0, 0}};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -246,14 +253,16 @@ __device__ __forceinline__ Raw<float> load4(Global<const float> p, int i,
     return r;
 }
 
-template <int MODE>
+template <int MODE, bool NT = true>
 __device__ __forceinline__ Raw<uint16_t> load4(Global<const uint16_t> p,
                                                int i, Places q)
 {
-    if constexpr (MODE == kAligned)
-        return {__builtin_nontemporal_load((Global<const u32x2>)(p + i))};
+    const auto a = (Global<const u32x2>)(p + i);
+    const auto u = (Global<const u32x2_2>)(p + i);
+    if constexpr (MODE <= kAligned)
+        return {NT ? __builtin_nontemporal_load(a) : *a};
     if (MODE == kWhole || q.has4(i))
-        return {__builtin_nontemporal_load((Global<const u32x2_2>)(p + i))};
+        return {NT ? __builtin_nontemporal_load(u) : *u};
     Raw<uint16_t> r = {{0, 0}};
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -269,7 +278,7 @@ __device__ __forceinline__ void store4(Global<float> p, int i, Places q,
                                        const V4& r)
 {
     const f32x4 x = {r.x[0], r.x[1], r.x[2], r.x[3]};
-    if constexpr (MODE == kAligned) {
+    if constexpr (MODE <= kAligned) {
         zsdev::stream_store((void*)p, (uint32_t)q.n * 4u, (uint32_t)i * 4u,
                             x);
         return;
@@ -289,7 +298,7 @@ __device__ __forceinline__ void store4(Global<uint16_t> p, int i, Places q,
                                        const V4& r)
 {
     const u32x2 x = {to_bf16(r.x[0], r.x[1]), to_bf16(r.x[2], r.x[3])};
-    if constexpr (MODE == kAligned) {
+    if constexpr (MODE <= kAligned) {
         zsdev::stream_store((void*)p, (uint32_t)q.n * 2u, (uint32_t)i * 2u,
                             x);
         return;
@@ -342,21 +351,29 @@ __device__ __forceinline__ void store_codes(Global<uint8_t> p, int i,
 // (0: as many as there are, eight at a time): all loads, then the sum in rank
 // order from the first (so that the sign of a zero sum is its own) and the
 // mean.
+//
+// Gradients of one or two ranks, and rows that do not start at lines, so that
+// every load shares a line with its neighbours', are loaded with the caches'
+// usual policy: W = 1 with bf16 weights 709 us against 717 non-temporal, W = 8
+// with rows at multiples of 16 bytes 1481 against 1511 (8-bit states 1026
+// against 1085).  Rows of three ranks and more that start at lines are
+// non-temporal: W = 8 1390 against 1447, W = 5 1198 against 1242.
 template <int MODE, int U, int WT, class T>
 struct Gradients {
     static constexpr int NB = WT > 0 ? WT : 8;
     Raw<T> x[NB][U];
 
-    __device__ __forceinline__ void load(Global<const T> g0, int64_t gs,
-                                         int s0, int W, Places q)
+    __device__ __forceinline__ void load(const Rec& r, int64_t off, int s0,
+                                         int W, Places q)
     {
+        const Global<const T> g0 = global<const T>(r.grad) + off;
 #pragma unroll
         for (int s = 0; s < NB; ++s)
             if (WT > 0 || s0 + s < W)
 #pragma unroll
                 for (int k = 0; k < U; ++k)
-                    x[s][k] = load4<MODE>(
-                        g0 + (int64_t)(s0 + s) * gs,
+                    x[s][k] = load4<MODE, MODE == kLines>(
+                        g0 + (int64_t)(s0 + s) * r.gstride,
                         4 * (k * kWave + (int)threadIdx.x), q);
     }
 
@@ -375,15 +392,15 @@ struct Gradients {
                 }
     }
 
-    // The mean, the first slices loaded by load(g0, gs, 0, W, q).
-    __device__ __forceinline__ void mean(Global<const T> g0, int64_t gs,
+    // The mean, the first slices loaded by load(rec, off, 0, W, q).
+    __device__ __forceinline__ void mean(const Rec& rec, int64_t off,
                                          const Ranks& r, Places q,
                                          V4 (&g)[U])
     {
         add(0, r.W, g);
         if constexpr (WT == 0)
             for (int s0 = NB; s0 < r.W; s0 += NB) {
-                load(g0, gs, s0, r.W, q);
+                load(rec, off, s0, r.W, q);
                 add(s0, r.W, g);
             }
         if constexpr (WT == 1)
@@ -674,7 +691,6 @@ __device__ __forceinline__ void step32_part(const StepArgs& a, const Rec& r,
 {
     const Global<float> mp = global<float>(r.m) + off;
     const Global<float> vp = global<float>(r.v) + off;
-    const Global<const G> gp = global<const G>(r.grad) + off;
     const int lane = (int)threadIdx.x;
     Weights<MODE, U, WM> wx;
     Raw<float> mx[U], vx[U];
@@ -685,13 +701,13 @@ __device__ __forceinline__ void step32_part(const StepArgs& a, const Rec& r,
         mx[k] = load4<MODE>(mp, 4 * (k * kWave + lane), q);
         vx[k] = load4<MODE>(vp, 4 * (k * kWave + lane), q);
     }
-    gx.load(gp, r.gstride, 0, a.ranks.W, q);
+    gx.load(r, off, 0, a.ranks.W, q);
     const Hp h = a.hp[r.group];
     float c;
     if (!clip_of(a.sumsq, a.max_norm, c))
         return;
     V4 g[U];
-    gx.mean(gp, r.gstride, a.ranks, q, g);
+    gx.mean(r, off, a.ranks, q, g);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
         V4 w = wide(wx.x[k]), m = wide(mx[k]), v = wide(vx[k]);
@@ -718,7 +734,6 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
     const Global<uint8_t> vp = global<uint8_t>(r.v) + off;
     const Global<float> msp = global<float>(r.ms) + off / kBlock;
     const Global<float> vsp = global<float>(r.vs) + off / kBlock;
-    const Global<const G> gp = global<const G>(r.grad) + off;
     const int lane = (int)threadIdx.x;
     Weights<MODE, U, WM> wx;
     uint32_t mq[U], vq[U];
@@ -733,13 +748,13 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
         ms[k] = there ? msp[k] : 0.0f;
         vs[k] = there ? vsp[k] : 0.0f;
     }
-    gx.load(gp, r.gstride, 0, a.ranks.W, q);
+    gx.load(r, off, 0, a.ranks.W, q);
     const Hp h = a.hp[r.group];
     float c = 1.0f;
     if (!clip_of(a.sumsq, a.max_norm, c))
         return;
     V4 g[U];
-    gx.mean(gp, r.gstride, a.ranks, q, g);
+    gx.mean(r, off, a.ranks, q, g);
     if (a.sumsq) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
@@ -799,7 +814,13 @@ __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
     const Part<U> q = part_of<U>(a.t, r);
     if (q.n <= 0)
         return;
-    if (q.whole && r.vec)
+    if constexpr (WT == 0 || WT > 2)
+        if (q.whole && r.flags == (kRecFours | kRecLines)) {
+            step_part<BITS, kLines, U, WM, WT, G>(a, r, q.off,
+                                                  {0, U * kBlock});
+            return;
+        }
+    if (q.whole && r.flags & kRecFours)
         step_part<BITS, kAligned, U, WM, WT, G>(a, r, q.off,
                                                 {0, U * kBlock});
     else if (q.whole)
@@ -833,11 +854,10 @@ __device__ __forceinline__ double sum_piece(const SumArgs& a, const Rec& r,
                                             int64_t off, Places q)
 {
     constexpr int U = 4;
-    const Global<const G> gp = global<const G>(r.grad) + off;
     Gradients<MODE, U, WT, G> gx;
-    gx.load(gp, r.gstride, 0, a.ranks.W, q);
+    gx.load(r, off, 0, a.ranks.W, q);
     V4 g[U];
-    gx.mean(gp, r.gstride, a.ranks, q, g);
+    gx.mean(r, off, a.ranks, q, g);
     double s = 0.0;
 #pragma unroll
     for (int k = 0; k < U; ++k)
@@ -950,7 +970,7 @@ __global__ __launch_bounds__(kSumThreads) void sumsq_kernel(SumArgs a)
             s += sum_run<G>(global<const G>(r.grad) + off, n);
             p += n;
         } else {
-            s += r.vec ? sum_piece<kAligned, WT, G>(a, r, off, {0, kPiece})
+            s += r.flags & kRecFours ? sum_piece<kAligned, WT, G>(a, r, off, {0, kPiece})
                        : sum_piece<kWhole, WT, G>(a, r, off, {0, kPiece});
             ++p;
         }
@@ -1055,8 +1075,8 @@ __device__ __forceinline__ void convert_part(const Rec& f, const Rec& t,
         unpack_part<MODE, U>(f, t, off, q);
 }
 
-// Whether a record's fp32 states are aligned to four elements (its vec is of
-// its own pieces).
+// Whether a record's fp32 states are aligned to four elements (its flags are of
+// its own units).
 __device__ __forceinline__ bool aligned16(const Rec& r)
 {
     return (((uintptr_t)r.m | (uintptr_t)r.v) & 15) == 0;
@@ -1246,7 +1266,9 @@ void place(const zs_tensors* L, Rec& r)
                 --lead;
     }
     r.pre = (kBlock - lead) % kBlock;
-    r.vec = fours(lead);
+    r.flags = (fours(lead) ? kRecFours : 0) |
+              (at(r.grad, lead, gs, 128) && r.gstride * gs % 128 == 0 ? kRecLines
+                                                              : 0);
 }
 
 int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)

@@ -106,7 +106,7 @@ typedef struct zs_tensors zs_tensors;
  * [0, ZS_TENSORS_MAX_GROUPS), pointers given for some tensors only, scales
  * missing or out of place, a master with fp32 or no parameters, overlaps);
  * ZS_EALIGN; ZS_ERANGE (world > 1 and grad_stride < numel, slices reaching
- * past 2^46 elements, 2^38 elements or more or more than 2^30 slices in all);
+ * past 2^46 elements, 2^38 elements or more or over 2^22 slices in all);
  * ZS_ENOMEM. */
 int zs_tensors_create(int32_t count, const zs_tensor* tensors, int32_t world,
                       int32_t grad_type, int32_t param_type, int32_t state,

@@ -138,7 +138,7 @@ def test_good_lists():
     (ERANGE, [tensor(grad_stride=-1000)], dict(world=2)),
     (ERANGE, [tensor(grad_stride=1 << 62)], dict(world=2)),
     (ERANGE, [tensor(grad_stride=1 << 45)], dict(world=4)),
-    (ERANGE, [tensor(numel=1, grad_stride=1)], dict(world=(1 << 30) + 1)),
+    (ERANGE, [tensor(numel=1, grad_stride=1)], dict(world=(1 << 22) + 1)),
     (ERANGE, [tensor(grad=None, param=None, master=None, numel=1 << 40,
                      m=1 << 50, v=1 << 51)], {})])
 def test_create_refusals(want, ts, kw):

@@ -65,13 +65,13 @@ constexpr int64_t kMaxPieces = (int64_t(1) << 28) - 1;
 // 351 us, 391 with one, 380 with four); where those cost little it is even
 // (with a master 318 us, 316 with one).
 constexpr int kStep32Units = 1, kStep8Units = 2;
-// To 8 bits 326 us (two units 340); to 32 bits 349 us with four at 10
-// workgroups per CU (8 and 12 within 1 %, 16 382), with two at 24 353 and as
-// many as fit 380, with one 382.
+// To 8 bits 326 us (two units 340); to 32 bits 348 us with four at 8
+// workgroups per CU (10: 358, 12: 351, 16: 382), with two at 22 353 and as many
+// as fit 380, with one 382.
 constexpr int kPackUnits = 1, kUnpackUnits = 4;
-constexpr int kUnpackResidency = 10;
+constexpr int kUnpackResidency = 8;
 constexpr int64_t kMaxReach = int64_t(1) << 46;
-constexpr int64_t kMaxSlices = int64_t(1) << 30;
+constexpr int64_t kMaxSlices = int64_t(1) << 22;
 
 // One tensor in the table.
 struct Rec {
@@ -1320,7 +1320,7 @@ int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)
         state_spans(L, r, L->states);
         if (L->grads) {
             if ((int64_t)L->recs.size() * L->world > kMaxSlices)
-                return fail(ZS_ERANGE, "more than 2^30 gradient slices");
+                return fail(ZS_ERANGE, "more than 2^22 gradient slices");
             for (int32_t s = 0; s < L->world; ++s)
                 add_span(spans, static_cast<const char*>(r.grad) +
                          (int64_t)s * r.gstride * gs, r.numel * gs, false);

@@ -348,19 +348,20 @@ __device__ __forceinline__ void store_codes(Global<uint8_t> p, int i,
 }
 
 // Elements of a part's gradients from the ranks, WT of them at compile time
-// (0: as many as there are, eight at a time): all loads, then the sum in rank
-// order from the first (so that the sign of a zero sum is its own) and the
-// mean.
+// (0: as many as there are, eight at a time; at a tensor's ends two): all
+// loads, then the sum in rank order from the first (so that the sign of a zero
+// sum is its own) and the mean.
 //
-// Gradients of one or two ranks, and rows that do not start at lines, so that
-// every load shares a line with its neighbours', are loaded with the caches'
-// usual policy: W = 1 with bf16 weights 709 us against 717 non-temporal, W = 8
-// with rows at multiples of 16 bytes 1481 against 1511 (8-bit states 1026
-// against 1085).  Rows of three ranks and more that start at lines are
-// non-temporal: W = 8 1390 against 1447, W = 5 1198 against 1242.
+// Gradients of one rank, and rows that do not start at lines, so that every
+// load shares a line with its neighbours', are loaded with the caches' usual
+// policy: W = 1 with bf16 weights 709 us against 717 non-temporal, W = 8 with
+// rows at multiples of 16 bytes 1481 against 1511 (8-bit states 1026 against
+// 1085).  Rows of several ranks that start at lines are non-temporal: W = 8
+// 1390 against 1447, W = 5 1198 against 1242.
 template <int MODE, int U, int WT, class T>
 struct Gradients {
-    static constexpr int NB = WT > 0 ? WT : 8;
+    static constexpr bool kAll = WT == 1 || (WT > 0 && MODE != kEdge);
+    static constexpr int NB = kAll ? WT : MODE == kEdge ? 2 : 8;
     Raw<T> x[NB][U];
 
     __device__ __forceinline__ void load(const Rec& r, int64_t off, int s0,
@@ -369,7 +370,7 @@ struct Gradients {
         const Global<const T> g0 = global<const T>(r.grad) + off;
 #pragma unroll
         for (int s = 0; s < NB; ++s)
-            if (WT > 0 || s0 + s < W)
+            if (kAll || s0 + s < W)
 #pragma unroll
                 for (int k = 0; k < U; ++k)
                     x[s][k] = load4<MODE, MODE == kLines>(
@@ -381,7 +382,7 @@ struct Gradients {
     {
 #pragma unroll
         for (int s = 0; s < NB; ++s)
-            if (WT > 0 || s0 + s < W)
+            if (kAll || s0 + s < W)
 #pragma unroll
                 for (int k = 0; k < U; ++k) {
                     const V4 y = wide(x[s][k]);
@@ -398,7 +399,7 @@ struct Gradients {
                                          V4 (&g)[U])
     {
         add(0, r.W, g);
-        if constexpr (WT == 0)
+        if constexpr (!kAll)
             for (int s0 = NB; s0 < r.W; s0 += NB) {
                 load(rec, off, s0, r.W, q);
                 add(s0, r.W, g);
@@ -814,7 +815,7 @@ __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
     const Part<U> q = part_of<U>(a.t, r);
     if (q.n <= 0)
         return;
-    if constexpr (WT == 0 || WT > 2)
+    if constexpr (WT != 1)
         if (q.whole && r.flags == (kRecFours | kRecLines)) {
             step_part<BITS, kLines, U, WM, WT, G>(a, r, q.off,
                                                   {0, U * kBlock});
@@ -1436,12 +1437,14 @@ void launch_step_u(const zs_tensors* L, StepArgs& a, hipStream_t s)
     });
 }
 
+// Four and eight ranks at compile time have all loads on their way without a
+// branch between them (W = 8 1390 us against 1463, W = 4 1123 against 1140;
+// W = 2 984 both ways).
 template <int BITS, int WM, class G>
 void launch_step_w(const zs_tensors* L, StepArgs& a, hipStream_t s)
 {
     switch (a.ranks.W) {
     case 1: launch_step_u<BITS, WM, 1, G>(L, a, s); break;
-    case 2: launch_step_u<BITS, WM, 2, G>(L, a, s); break;
     case 4: launch_step_u<BITS, WM, 4, G>(L, a, s); break;
     case 8: launch_step_u<BITS, WM, 8, G>(L, a, s); break;
     default: launch_step_u<BITS, WM, 0, G>(L, a, s); break;

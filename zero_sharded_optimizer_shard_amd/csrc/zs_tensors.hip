@@ -22,8 +22,7 @@
 // tensor's record, both wave-uniform scalar loads.  As in zs_step.hip every
 // load or store of a wave covers one contiguous run, all loads of a part are
 // issued before its arithmetic, loads are non-temporal and aligned stores
-// stream to HBM with system scope.  Consecutive workgroups go to the XCDs in
-// turn; giving each XCD runs of 2, 4 or 32 of them cost 2 to 6 %.
+// stream to HBM with system scope.
 
 #include <hip/hip_runtime.h>
 
@@ -65,6 +64,11 @@ constexpr int64_t kMaxPieces = (int64_t(1) << 28) - 1;
 // 351 us, 391 with one, 380 with four); where those cost little it is even
 // (with a master 318 us, 316 with one).
 constexpr int kStep32Units = 1, kStep8Units = 2;
+// Parts of the 8-bit step that an XCD takes in a run: 64 blocks, whose scales
+// are two lines.  218 M elements in fp32 524 us, 539 with the parts in turn, 24
+// M with a master 59.4 and 61; the larger bf16 lists are even.  With fp32 states
+// and in conversions runs of 2 to 256 parts are 1 to 6 % slower.
+constexpr int kStep8Run = 32;
 // To 8 bits 326 us (two units 340); to 32 bits 348 us with four at 8
 // workgroups per CU (10: 358, 12: 351, 16: 382), with two at 22 353 and as many
 // as fit 380, with one 382.
@@ -170,20 +174,34 @@ struct Part {
     bool whole;
 };
 
-// Workgroup b of a launch has part b % (kPiece / U units) of its piece.
-template <int U>
-__device__ __forceinline__ int32_t record_of(const Table& t)
+// Which of a launch's parts this workgroup has: with RUN > 1, each XCD (they
+// take workgroups in turn) has runs of RUN parts.  Those that do not fill
+// eight runs are in order.
+template <int RUN>
+__device__ __forceinline__ uint32_t part_index()
 {
-    return t.tensor[t.first + (int32_t)(blockIdx.x / (4 / U))];
+    const uint32_t b = blockIdx.x;
+    constexpr uint32_t kAll = 8 * RUN;
+    if (RUN == 1 || b >= gridDim.x / kAll * kAll)
+        return b;
+    return b / kAll * kAll + b % 8 * RUN + b % kAll / 8;
+}
+
+// Part i of a launch is number i % (4 / U) of its piece.
+template <int U>
+__device__ __forceinline__ int32_t record_of(const Table& t, uint32_t i)
+{
+    return t.tensor[t.first + (int32_t)(i / (4 / U))];
 }
 
 template <int U>
-__device__ __forceinline__ Part<U> part_of(const Table& t, const Rec& r)
+__device__ __forceinline__ Part<U> part_of(const Table& t, const Rec& r,
+                                           uint32_t i)
 {
-    const int32_t p = t.first + (int32_t)(blockIdx.x / (4 / U));
+    const int32_t p = t.first + (int32_t)(i / (4 / U));
     Part<U> q;
     q.off = (int64_t)(p - r.piece0) * kPiece +
-            (int)(blockIdx.x % (4 / U)) * (U * kBlock) - r.pre;
+            (int)(i % (4 / U)) * (U * kBlock) - r.pre;
     const int64_t left = r.numel - q.off;
     q.lo = q.off < 0 ? (int)-q.off : 0;
     q.n = left < U * kBlock ? (int)left : U * kBlock;
@@ -811,8 +829,9 @@ __device__ __forceinline__ void step_part(const StepArgs& a, const Rec& r,
 template <int BITS, int U, int WM, int WT, class G>
 __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
 {
-    const Rec r = a.t.recs[record_of<U>(a.t)];
-    const Part<U> q = part_of<U>(a.t, r);
+    const uint32_t part = part_index<BITS == 32 ? 1 : kStep8Run>();
+    const Rec r = a.t.recs[record_of<U>(a.t, part)];
+    const Part<U> q = part_of<U>(a.t, r, part);
     if (q.n <= 0)
         return;
     if constexpr (WT != 1)
@@ -1088,10 +1107,10 @@ __global__ __launch_bounds__(kWave) void convert_kernel(ConvertArgs a)
 {
     // the pieces of the list in 8 bits, whose units are its blocks
     const Table& held = PACK ? a.to : a.from;
-    const int32_t i = record_of<U>(held);
+    const int32_t i = record_of<U>(held, blockIdx.x);
     const Rec f = a.from.recs[i];
     const Rec t = a.to.recs[i];
-    const Part<U> q = part_of<U>(held, PACK ? t : f);
+    const Part<U> q = part_of<U>(held, PACK ? t : f, blockIdx.x);
     if (q.n <= 0)
         return;
     if (q.whole && aligned16(PACK ? f : t))

@@ -10,9 +10,9 @@
 //   fp32 states, W = 1: bf16 weights 6.7 TB/s, fp32 weights and gradients 6.7,
 //     a master 6.5; W = 2, 3, 4, 5, 8 with a master 6.6, 6.6, 6.6, 6.5, 6.6
 //     (rows of gradients at multiples of 256 bytes; at multiples of 16 every
-//     load takes a line more: 6.6, 6.3, 6.5, 6.2, 6.2)
-//   8-bit states: 6.3 (a master), 6.2 (bf16 weights), 6.5 (fp32)
-//   to 8 bits 6.8, to 32 bits 6.2, sum of squares 6.2 (both launches)
+//     load takes a line more: 6.5, 6.3, 6.5, 6.2, 6.2)
+//   8-bit states: 6.3 (a master), 6.2 (bf16 weights), 6.7 (fp32)
+//   to 8 bits 6.8, to 32 bits 6.3, sum of squares 6.2 (both launches)
 // Large streams of the same mixes reach 6.8 here.
 //
 // Work decomposition.  A list's tensors are cut into pieces of kPiece
@@ -64,10 +64,11 @@ constexpr int64_t kMaxPieces = (int64_t(1) << 28) - 1;
 // 351 us, 391 with one, 380 with four); where those cost little it is even
 // (with a master 318 us, 316 with one).
 constexpr int kStep32Units = 1, kStep8Units = 2;
-// Parts of the 8-bit step that an XCD takes in a run: 64 blocks, whose scales
-// are two lines.  218 M elements in fp32 524 us, 539 with the parts in turn, 24
-// M with a master 59.4 and 61; the larger bf16 lists are even.  With fp32 states
-// and in conversions runs of 2 to 256 parts are 1 to 6 % slower.
+// Parts that an XCD takes in a run where the 8-bit step's weights are fp32: 64
+// blocks, whose scales are two lines.  218 M elements in fp32 524 us, 539 with
+// the parts in turn, 24 M with a master 59.4 and 61; with bf16 weights alone
+// 359 and 355, so those go in turn.  With fp32 states and in conversions runs
+// of 2 to 256 parts are 1 to 6 % slower.
 constexpr int kStep8Run = 32;
 // To 8 bits 326 us (two units 340); to 32 bits 348 us with four at 8
 // workgroups per CU (10: 358, 12: 351, 16: 382), with two at 22 353 and as many
@@ -826,10 +827,16 @@ __device__ __forceinline__ void step_part(const StepArgs& a, const Rec& r,
         step8_part<MODE, U, WM, WT, G>(a, r, off, q);
 }
 
+template <int BITS, int WM>
+constexpr int step_run()
+{
+    return BITS == 32 || WM == kBf16 ? 1 : kStep8Run;
+}
+
 template <int BITS, int U, int WM, int WT, class G>
 __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
 {
-    const uint32_t part = part_index<BITS == 32 ? 1 : kStep8Run>();
+    const uint32_t part = part_index<step_run<BITS, WM>()>();
     const Rec r = a.t.recs[record_of<U>(a.t, part)];
     const Part<U> q = part_of<U>(a.t, r, part);
     if (q.n <= 0)

@@ -9,9 +9,10 @@
  * (each of its slices one tensor, its parameters the slice's place in the
  * flat buffer).  One launch steps all of them.
  *
- * The conventions of zs.h hold: 0 or a negative ZS_E* code, zs_last_error(),
- * caller-owned device memory on the current device, asynchronous calls on
- * the given stream.  Nothing is allocated on the device.  zs_tensors_step,
+ * The conventions of zs.h hold, but for the clipping and the steps that are
+ * not taken below: 0 or a negative ZS_E* code, zs_last_error(), caller-owned
+ * device memory on the current device, asynchronous calls on the given
+ * stream.  Nothing is allocated on the device.  zs_tensors_step,
  * zs_tensors_sumsq and zs_tensors_convert may be captured into a HIP graph:
  * they launch kernels only and read their host arguments during the call (a
  * captured step repeats with its lr, step and max_norm).  Results do not
@@ -137,7 +138,8 @@ int zs_tensors_upload(zs_tensors* list, void* table, int64_t bytes,
  * bit.  With states in 8 bits w is computed from the fp32 m and v of this
  * step, the two divisions as products with reciprocals (the update within
  * 4 * 2^-23 of itself), and m and v are then held as above, from the fp32
- * values and their correctly rounded roots.
+ * values and their correctly rounded roots.  A NaN or an infinity stays with
+ * its element in 32 bits, and with its block's states in 8.
  *
  * hp: n_hp (1 .. ZS_TENSORS_MAX_GROUPS) hyper-parameter groups, read during
  *   the call.  step: the 1-based counter t of all tensors.

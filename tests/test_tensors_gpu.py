@@ -170,9 +170,10 @@ class Case:
                 h["v"], h["v_scale"] = q[2].astype(np.uint8), q[3]
                 kept, update = OT.weights64(w, m, root, hp, t)
                 w1 = kept - update
-                # seven roundings of half a step and a reciprocal to one
-                # step in the update (8 * 2^-24), and w*dec and the
-                # difference rounded once each
+                # in the update: the constant of sqrt(1-b2^t) rounded on
+                # either side and the sum with eps (3 half steps of 2^-24),
+                # a reciprocal to one step (2) and its product (1), 6 in
+                # all; w*dec and the difference rounded once each
                 with np.errstate(all="ignore"):
                     h["off"] = 2.0 ** -24 * (8 * np.abs(update) +
                                              np.abs(kept) + np.abs(w1)) \
@@ -263,6 +264,25 @@ def test_step_other_addresses(bits, weights, shift, apart):
              "bf16", 2, shift, apart=apart)
     c.step()
     c.expect()
+    c.check()
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_step_tiny_gradients_and_eps(bits):
+    """Moments near fp32's least normal number over an eps of their size: the
+    update is of the usual size, and as exact."""
+    def edit(h):
+        h["grad"] *= np.float32(1e-33)
+        if bits == 32:
+            h["m"] *= np.float32(1e-33)
+            h["v"][:] = 0
+        else:
+            h["m_scale"] *= np.float32(1e-33)
+            h["v"][:], h["v_scale"][:] = 0, 0
+    c = Case([1500], bits, "f32", "f32", edit=edit)
+    hp = (1e-3, 0.9, 0.95, 1e-36, 0.1)
+    c.step([hp])
+    c.expect([hp])
     c.check()
 
 

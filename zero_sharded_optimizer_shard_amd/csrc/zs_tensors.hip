@@ -806,8 +806,7 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
         for (int j = 0; j < 4; ++j) {
             const float rden = __builtin_amdgcn_rcpf(
                 __builtin_fmaf(root[k][j], h.ibc2s, h.eps));
-            w.x[j] = __builtin_fmaf(-(h.ss * m[k][j]), rden,
-                                    w.x[j] * h.dec);
+            w.x[j] = __builtin_fmaf(-h.ss, m[k][j] * rden, w.x[j] * h.dec);
         }
         store_weights<MODE, WM>(r, off, 4 * (k * kWave + lane), q, w);
     }

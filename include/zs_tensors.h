@@ -16,8 +16,9 @@
  * zs_tensors_sumsq and zs_tensors_convert may be captured into a HIP graph:
  * they launch kernels only and read their host arguments during the call (a
  * captured step repeats with its lr, step and max_norm).  Results do not
- * depend on what else runs, nor on the stream: every sum is taken in an order
- * that the list fixes.  Steps and conversions to 32 bits reserve LDS that they
+ * depend on what else runs, on the stream, nor on where the arrays lie: every
+ * sum is taken in an order that the tensors' sizes and the world fix, so
+ * replicas with the same gradients have the same sum of squares.  Steps and conversions to 32 bits reserve LDS that they
  * do not use, as zs_step does; zs_set_residency_cap turns it off.
  */
 #ifndef ZS_TENSORS_H

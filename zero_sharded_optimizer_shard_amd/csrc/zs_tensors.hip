@@ -19,7 +19,11 @@
 // elements, each taken by one to four one-wave workgroups, so one launch takes
 // any number of tensors of any sizes.  A workgroup finds its tensor in the
 // list's table in device memory: the tensor's number for each piece, then the
-// tensor's record, both wave-uniform scalar loads.  As in zs_step.hip every
+// tensor's record, both wave-uniform scalar loads.  A tensor's own pieces, one
+// for each kPiece elements, lie together; where a step's units start later than
+// the tensor it may need one more, and those lie behind all tensors' own, so
+// that the sum of squares, which has no need to start late, takes the same
+// elements in the same order wherever the arrays lie.  As in zs_step.hip every
 // load or store of a wave covers one contiguous run, all loads of a part are
 // issued before its arithmetic, loads are non-temporal and aligned stores
 // stream to HBM with system scope.
@@ -91,7 +95,7 @@ struct Rec {
     int64_t numel;
     int32_t piece0;     // its first piece
     int32_t group;
-    int32_t pre;        // places before its first element in that piece
+    int32_t pre;        // places before its first element in a step's units
     int32_t flags;
 };
 // Four elements from a unit's start on are aligned; so are lines of all ranks'
@@ -110,6 +114,7 @@ struct Hp {
 struct Table {
     const Rec* recs;
     const int32_t* tensor;      // of each piece
+    int32_t own;                // the tensors' own pieces; more lie behind
     int32_t first;              // a launch's first piece
 };
 
@@ -195,14 +200,18 @@ __device__ __forceinline__ int32_t record_of(const Table& t, uint32_t i)
     return t.tensor[t.first + (int32_t)(i / (4 / U))];
 }
 
-template <int U>
+// LATE: units may start later than their tensor, as those of lists with fp32
+// states do.
+template <int U, bool LATE>
 __device__ __forceinline__ Part<U> part_of(const Table& t, const Rec& r,
                                            uint32_t i)
 {
     const int32_t p = t.first + (int32_t)(i / (4 / U));
+    int64_t piece = p - r.piece0;
+    if (LATE && p >= t.own)     // the one behind the tensor's own
+        piece = (r.numel + kPiece - 1) / kPiece;
     Part<U> q;
-    q.off = (int64_t)(p - r.piece0) * kPiece +
-            (int)(i % (4 / U)) * (U * kBlock) - r.pre;
+    q.off = piece * kPiece + (int)(i % (4 / U)) * (U * kBlock) - r.pre;
     const int64_t left = r.numel - q.off;
     q.lo = q.off < 0 ? (int)-q.off : 0;
     q.n = left < U * kBlock ? (int)left : U * kBlock;
@@ -837,7 +846,7 @@ __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
 {
     const uint32_t part = part_index<step_run<BITS, WM>()>();
     const Rec r = a.t.recs[record_of<U>(a.t, part)];
-    const Part<U> q = part_of<U>(a.t, r, part);
+    const Part<U> q = part_of<U, BITS == 32>(a.t, r, part);
     if (q.n <= 0)
         return;
     if constexpr (WT != 1)
@@ -869,7 +878,6 @@ constexpr int64_t kSumOne = 32;         // pieces that one workgroup takes alone
 
 struct SumArgs {
     Table t;
-    int32_t pieces;
     int32_t per_wave;           // consecutive pieces of a wave
     Ranks ranks;
     double* out;                // one per workgroup
@@ -980,24 +988,24 @@ __global__ __launch_bounds__(kSumThreads) void sumsq_kernel(SumArgs a)
     const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.y);
     const int64_t first =
         ((int64_t)blockIdx.x * kSumWaves + wave) * a.per_wave;
-    const int64_t end = min(first + a.per_wave, (int64_t)a.pieces);
+    const int64_t end = min(first + a.per_wave, (int64_t)a.t.own);
     double s = 0.0;
     for (int64_t p = first; p < end;) {
         const Rec r = a.t.recs[a.t.tensor[p]];
-        const int64_t off = (p - r.piece0) * kPiece - r.pre;
+        const int64_t off = (p - r.piece0) * kPiece;
         const int64_t left = r.numel - off;
-        if (left < kPiece || off < 0) {
-            s += sum_piece<kEdge, WT, G>(
-                a, r, off, {off < 0 ? (int)-off : 0,
-                            left < kPiece ? (int)left : kPiece});
+        if (left < kPiece) {
+            s += sum_piece<kEdge, WT, G>(a, r, off, {0, (int)left});
             ++p;
         } else if constexpr (WT == 1) {
             const int n = (int)min(left / kPiece, end - p);
             s += sum_run<G>(global<const G>(r.grad) + off, n);
             p += n;
         } else {
-            s += r.flags & kRecFours ? sum_piece<kAligned, WT, G>(a, r, off, {0, kPiece})
-                       : sum_piece<kWhole, WT, G>(a, r, off, {0, kPiece});
+            // the flag is of where a step's units start
+            s += r.flags & kRecFours && r.pre % 4 == 0
+                     ? sum_piece<kAligned, WT, G>(a, r, off, {0, kPiece})
+                     : sum_piece<kWhole, WT, G>(a, r, off, {0, kPiece});
             ++p;
         }
     }
@@ -1116,7 +1124,7 @@ __global__ __launch_bounds__(kWave) void convert_kernel(ConvertArgs a)
     const int32_t i = record_of<U>(held, blockIdx.x);
     const Rec f = a.from.recs[i];
     const Rec t = a.to.recs[i];
-    const Part<U> q = part_of<U>(held, PACK ? t : f, blockIdx.x);
+    const Part<U> q = part_of<U, false>(held, PACK ? t : f, blockIdx.x);
     if (q.n <= 0)
         return;
     if (q.whole && aligned16(PACK ? f : t))
@@ -1149,8 +1157,9 @@ struct zs_tensors {
     std::vector<int64_t> numel;         // of every tensor, empty ones too
     std::vector<Rec> recs;              // of those with elements
     std::vector<int32_t> tensor;        // record of each piece
+    int32_t own = 0;                    // the tensors' own pieces
     std::vector<Span> states;           // m, v and scales, in order
-    Table table = {nullptr, nullptr, 0};
+    Table table = {nullptr, nullptr, 0, 0};
     int device = -1;
 };
 
@@ -1300,6 +1309,7 @@ void place(const zs_tensors* L, Rec& r)
 int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)
 {
     std::vector<Span> spans;
+    std::vector<int32_t> late;          // records with one piece more
     int64_t pieces = 0;
     const int gs = L->grad_type == ZS_F32 ? 4 : 2;
     const int ps = L->param_type == ZS_F32 ? 4 : 2;
@@ -1335,8 +1345,11 @@ int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)
         r.piece0 = (int32_t)pieces;
         r.group = t.group;
         place(L, r);
-        pieces += (r.pre + t.numel + kPiece - 1) / kPiece;
-        if (pieces > kMaxPieces)
+        const int64_t own = (t.numel + kPiece - 1) / kPiece;
+        if ((r.pre + t.numel + kPiece - 1) / kPiece > own)
+            late.push_back((int32_t)L->recs.size());
+        pieces += own;
+        if (pieces + (int64_t)late.size() > kMaxPieces)
             return fail(ZS_ERANGE, "tensors 0 to %d have too many elements",
                         k);
         L->tensor.resize((size_t)pieces, (int32_t)L->recs.size());
@@ -1352,6 +1365,8 @@ int build_list(zs_tensors* L, int32_t count, const zs_tensor* ts)
                          (int64_t)s * r.gstride * gs, r.numel * gs, false);
         }
     }
+    L->own = (int32_t)pieces;
+    L->tensor.insert(L->tensor.end(), late.begin(), late.end());
     spans.insert(spans.end(), L->states.begin(), L->states.end());
     if (overlap(spans))
         return fail(ZS_EINVAL, "arrays that a step writes overlap one "
@@ -1509,7 +1524,7 @@ void launch_convert(int64_t pieces, ConvertArgs& a, hipStream_t s)
 // How zs_tensors_sumsq cuts a list: pieces of each wave, and workgroups.
 void sum_plan(const zs_tensors* L, int32_t& per_wave, int32_t& groups)
 {
-    const int64_t pieces = (int64_t)L->tensor.size();
+    const int64_t pieces = L->own;
     const int64_t most = pieces <= kSumOne ? 1 : kSumMaxGroups;
     const int64_t waves = most * kSumWaves;
     per_wave = (int32_t)std::max<int64_t>(1, (pieces + waves - 1) / waves);
@@ -1628,6 +1643,7 @@ extern "C" int zs_tensors_upload(zs_tensors* L, void* table, int64_t bytes,
     }
     L->table.recs = reinterpret_cast<const Rec*>(at);
     L->table.tensor = reinterpret_cast<const int32_t*>(at + recs_bytes(L));
+    L->table.own = L->own;
     L->device = dev;
     return ZS_OK;
 }
@@ -1710,7 +1726,6 @@ extern "C" int zs_tensors_sumsq(const zs_tensors* L, double* out,
     int32_t groups;
     sum_plan(L, a.per_wave, groups);
     a.t = L->table;
-    a.pieces = (int32_t)L->tensor.size();
     a.ranks = ranks_of(L->world);
     a.out = groups > 1 ? static_cast<double*>(workspace) : out;
     hipStream_t s = static_cast<hipStream_t>(hip_stream);

@@ -138,7 +138,8 @@ int zs_tensors_upload(zs_tensors* list, void* table, int64_t bytes,
  * to nearest even.  With states in 32 bits the results are zs_step's, bit for
  * bit.  With states in 8 bits w is computed from the fp32 m and v of this
  * step, the two divisions as products with reciprocals (the update within
- * 4 * 2^-23 of itself), and m and v are then held as above, from the fp32
+ * 4 * 2^-23 of itself, or its quotient within 2^-149 where that is below
+ * 2^-126), and m and v are then held as above, from the fp32
  * values and their correctly rounded roots.  A NaN or an infinity stays with
  * its element in 32 bits, and with its block's states in 8.
  *

@@ -1406,7 +1406,8 @@ Ranks ranks_of(int32_t W)
     return {W, (float)W, (float)(1.0 / (double)W), (W & (W - 1)) == 0};
 }
 
-int make_hp(const zs_adamw& hp, int64_t t, int32_t k, Hp& h)
+// bits: of the states.
+int make_hp(const zs_adamw& hp, int64_t t, int32_t k, int bits, Hp& h)
 {
     if (!std::isfinite(hp.lr) || !std::isfinite(hp.weight_decay))
         return fail(ZS_EINVAL, "group %d: lr and weight_decay must be "
@@ -1431,6 +1432,14 @@ int make_hp(const zs_adamw& hp, int64_t t, int32_t k, Hp& h)
     if (!std::isfinite(h.ss) || !std::isfinite(h.dec))
         return fail(ZS_EINVAL, "group %d: lr/(1-beta1^t) or "
                     "1-lr*weight_decay is not finite in fp32", k);
+    // the 8-bit step's reciprocals have no subnormal results: an eps that
+    // would need them is taken with its step size by a sixteenth, as are the
+    // roots beside it
+    if (bits == 8 && h.eps > 0x1p124f) {
+        h.eps *= 0x1p-4f;
+        h.ibc2s *= 0x1p-4f;
+        h.ss *= 0x1p-4f;
+    }
     return ZS_OK;
 }
 
@@ -1665,7 +1674,7 @@ extern "C" int zs_tensors_step(const zs_tensors* L, const zs_adamw* hp,
     if (!aligned(sumsq, 8)) return fail(ZS_EALIGN, "sumsq not 8-byte aligned");
     StepArgs a = {};
     for (int32_t k = 0; k < n_hp; ++k)
-        if (int rc = make_hp(hp[k], step, k, a.hp[k]))
+        if (int rc = make_hp(hp[k], step, k, L->state, a.hp[k]))
             return rc;
     if (L->recs.empty())
         return ZS_OK;

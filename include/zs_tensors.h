@@ -18,8 +18,9 @@
  * captured step repeats with its lr, step and max_norm).  Results do not
  * depend on what else runs, on the stream, nor on where the arrays lie: every
  * sum is taken in an order that the tensors' sizes and the world fix, so
- * replicas with the same gradients have the same sum of squares.  Steps and conversions to 32 bits reserve LDS that they
- * do not use, as zs_step does; zs_set_residency_cap turns it off.
+ * replicas with the same gradients have the same sum of squares.  Steps and
+ * conversions to 32 bits reserve LDS that they do not use, as zs_step does;
+ * zs_set_residency_cap turns it off.
  */
 #ifndef ZS_TENSORS_H
 #define ZS_TENSORS_H
@@ -52,13 +53,25 @@ extern "C" {
  * A block with A below 2^-100 has S = 0 and q = 0.  One with a NaN or an
  * infinity has S = NaN and q = 0: it stands for NaN from then on (with a
  * sum of squares, below, such a step is not taken).
+ * A step rounds m's codes of 1 to 9 towards zero (q^2 <= y < (q + 1)^2) for an
+ * element that has no gradient, that is 0 on every rank, while another of its
+ * block has one: to the nearest they would stay, as a tenth of m (beta1 0.9) is
+ * less than half a step there, and its weight would go on moving.  So m fades
+ * and the weight comes to rest after some lr, as with fp32 states.  In a block
+ * without any gradient the codes stay and the scales fade.
  *
  * What it costs: on noise with a mean of a tenth of its sigma, beside fp32
  * states after 1000 steps at beta2 0.95 (4000 at 0.999), an update is off by
  * 2 % (5 %) of its norm where the sigmas of a block's elements differ by
  * factors of about 1.35, by 6 % (10 %) where by e, and by more than half where
  * by e^2: the small ones then change by less than half a step of their codes.
- * The roots of v are right on average (to 1 %, 4 % in the last case). */
+ * The roots of v are right on average (to 1 %, 4 % in the last case).
+ * Elements whose gradients fall to a thousandth of their block's are stepped as
+ * with fp32 states at betas 0.9 and 0.95 (to 10 %); where they fall to a
+ * millionth but not to 0, codes of 1 stay, and such weights move by about a
+ * quarter of lr a step to one side.  With a beta1 above 0.9, codes of m above 9
+ * fade only where the block's A moves by as much as their half step
+ * (noise does that; at 0.99 it took 2000 steps). */
 #define ZS_STATE_NONE 0
 #define ZS_STATE_32 32
 #define ZS_STATE_8  8

@@ -106,6 +106,26 @@ def encode(x, top):
     return q[:len(x)], S
 
 
+FADE = 9
+
+
+def faded(q, m, blank):
+    """Codes q of fp32 values m, as a step holds them: where `blank` (no
+    gradient on any rank) and another of the block is not, codes of up to FADE
+    are rounded towards zero."""
+    q, m = np.array(q), np.asarray(m, F)
+    with np.errstate(all="ignore"):
+        for b in range(0, len(m), BLOCK):
+            s = slice(b, b + BLOCK)
+            A = np.abs(m[s]).max()
+            if blank[s].all() or not A >= F(2.0 ** -100):
+                continue
+            y = np.abs(m[s]) * (F(127 ** 2) / A)
+            k = np.abs(q[s])
+            q[s] -= np.sign(q[s]) * (blank[s] & (k <= FADE) & (k * k > y))
+    return q
+
+
 def decode(q, S):
     """fp32 values of codes."""
     q = np.asarray(q).astype(F)

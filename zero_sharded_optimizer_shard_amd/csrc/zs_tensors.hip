@@ -386,11 +386,15 @@ __device__ __forceinline__ void store_codes(Global<uint8_t> p, int i,
 // rows at multiples of 16 bytes 1481 against 1511 (8-bit states 1026 against
 // 1085).  Rows of several ranks that start at lines are non-temporal: W = 8
 // 1390 against 1447, W = 5 1198 against 1242.
-template <int MODE, int U, int WT, class T>
+//
+// SEEN: the bits of all ranks' gradients are kept, for blank().
+template <int MODE, int U, int WT, class T, bool SEEN = false>
 struct Gradients {
     static constexpr bool kAll = WT == 1 || (WT > 0 && MODE != kEdge);
     static constexpr int NB = kAll ? WT : MODE == kEdge ? 2 : 8;
     Raw<T> x[NB][U];
+    using Words = std::conditional_t<sizeof(T) == 2, u32x2, u32x4>;
+    Words seen[U];
 
     __device__ __forceinline__ void load(const Rec& r, int64_t off, int s0,
                                          int W, Places q)
@@ -406,7 +410,7 @@ struct Gradients {
                         4 * (k * kWave + (int)threadIdx.x), q);
     }
 
-    __device__ __forceinline__ void add(int s0, int W, V4 (&g)[U]) const
+    __device__ __forceinline__ void add(int s0, int W, V4 (&g)[U])
     {
 #pragma unroll
         for (int s = 0; s < NB; ++s)
@@ -418,7 +422,50 @@ struct Gradients {
                     for (int j = 0; j < 4; ++j)
                         g[k].x[j] =
                             s0 + s == 0 ? y.x[j] : g[k].x[j] + y.x[j];
+                    if constexpr (SEEN && !kAll) {
+                        const Words w = __builtin_bit_cast(Words, x[s][k]);
+                        seen[k] = s0 + s == 0 ? w : seen[k] | w;
+                    }
                 }
+    }
+
+    // Bit 4 k + j: element j of unit k is zero, of either sign, on every rank,
+    // though another of its block is not.  g: the mean, which has to be zero
+    // for that, so that the ranks' bits are looked at in few waves only.
+    __device__ __forceinline__ uint32_t blank(const V4 (&g)[U]) const
+    {
+        float least = INFINITY;
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)     // the smaller of both
+                least = __builtin_amdgcn_fmed3f(least, fabsf(g[k].x[j]),
+                                                0.0f);
+        if (__builtin_expect(!__any(least == 0.0f), 1))
+            return 0;
+        uint32_t r = 0;
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            Words w;
+            if constexpr (kAll) {
+                w = __builtin_bit_cast(Words, x[0][k]);
+#pragma unroll
+                for (int s = 1; s < NB; ++s)
+                    w |= __builtin_bit_cast(Words, x[s][k]);
+            } else {
+                w = seen[k];
+            }
+            uint32_t b = 0;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t y = sizeof(T) == 4 ? w[j] & 0x7fffffffu
+                    : w[j / 2] & (j % 2 ? 0x7fff0000u : 0x7fffu);
+                b |= (uint32_t)(y == 0) << j;
+            }
+            if (__any(b != 15))
+                r |= b << (4 * k);
+        }
+        return r;
     }
 
     // The mean, the first slices loaded by load(rec, off, 0, W, q).
@@ -598,11 +645,36 @@ __device__ __forceinline__ void codes(const float (&m)[4],
 
 constexpr float kTopM = 127.0f * 127.0f, kTopR = 255.0f * 255.0f;
 
+// Codes of four m, those up to kFade that `blank` has a bit for rounded towards
+// zero.  A step takes a tenth of m away at a beta1 of 0.9, less than half a
+// step of the codes up to 9: to the nearest they would stay for ever, and the
+// weight of an element that has no gradient any more would go on moving, by a
+// third of lr a step.  Larger codes go down by themselves, and where elements
+// are without a gradient now and then their roundings have to be right on
+// average (all towards zero took 5 to 9 % off what such weights move, those up
+// to 9 nothing).  Looking for zeros costs 0 to 1 % (bf16 weights, 218 M
+// elements: 358 us of 356), gradients with many of them 3 to 9 % (392 of 359).
+constexpr float kFade = 9.0f;
+
+__device__ __forceinline__ uint32_t faded(const float (&m)[4], float im,
+                                          uint32_t c, uint32_t blank)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const int q = (int8_t)(c >> (8 * j));
+        const float a = fabsf((float)q);
+        if ((blank >> j & 1) && a <= kFade && a * a > fabsf(m[j]) * im)
+            c = (c & ~(0xffu << (8 * j))) |
+                (uint32_t)(uint8_t)(q < 0 ? q + 1 : q - 1) << (8 * j);
+    }
+    return c;
+}
+
 // Holds U units' m and roots of v: codes, and scales in the lanes that
-// wave_max() has them in.
+// wave_max() has them in.  blank: as Gradients has it.
 template <int U>
 __device__ __forceinline__ void hold(const float (&m)[U][4],
-                                     const float (&r)[U][4],
+                                     const float (&r)[U][4], uint32_t blank,
                                      uint32_t (&cm)[U], uint32_t (&cr)[U],
                                      float& S)
 {
@@ -632,17 +704,25 @@ __device__ __forceinline__ void hold(const float (&m)[U][4],
         if (a >= 0x7f800000u)           // an infinity or a NaN
             S = __uint_as_float(0x7fc00000u);
     }
+    auto lane = [](float x, int i) {
+        return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
+            (int)__float_as_uint(x), i));
+    };
 #pragma unroll
-    for (int k = 0; k < U; ++k) {
-        const int at = 16 * k;
-        auto lane = [](float x, int i) {
-            return __uint_as_float((uint32_t)__builtin_amdgcn_readlane(
-                (int)__float_as_uint(x), i));
-        };
-        codes(m[k], r[k], lane(inv, at), lane(inv, at + 32), cm[k], cr[k]);
-        if (__builtin_expect(odd, 0)) {
-            cm[k] = lane(S, at) == lane(S, at) ? cm[k] : 0;
-            cr[k] = lane(S, at + 32) == lane(S, at + 32) ? cr[k] : 0;
+    for (int k = 0; k < U; ++k)
+        codes(m[k], r[k], lane(inv, 16 * k), lane(inv, 16 * k + 32), cm[k],
+              cr[k]);
+    if (__builtin_expect(__any(blank != 0), 0)) {
+#pragma unroll
+        for (int k = 0; k < U; ++k)
+            cm[k] = faded(m[k], lane(inv, 16 * k), cm[k], blank >> (4 * k));
+    }
+    if (__builtin_expect(odd, 0)) {
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+            const float sm = lane(S, 16 * k), sr = lane(S, 16 * k + 32);
+            cm[k] = sm == sm ? cm[k] : 0;
+            cr[k] = sr == sr ? cr[k] : 0;
         }
     }
 }
@@ -767,7 +847,7 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
     Weights<MODE, U, WM> wx;
     uint32_t mq[U], vq[U];
     float ms[U], vs[U];
-    Gradients<MODE, U, WT, G> gx;
+    Gradients<MODE, U, WT, G, true> gx;
     wx.load(r, off, q);
 #pragma unroll
     for (int k = 0; k < U; ++k) {
@@ -784,6 +864,7 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
         return;
     V4 g[U];
     gx.mean(r, off, a.ranks, q, g);
+    const uint32_t blank = gx.blank(g);
     if (a.sumsq) {
 #pragma unroll
         for (int k = 0; k < U; ++k)
@@ -821,7 +902,7 @@ __device__ __forceinline__ void step8_part(const StepArgs& a, const Rec& r,
     }
     uint32_t cm[U], cr[U];
     float S;
-    hold<U>(m, root, cm, cr, S);
+    hold<U>(m, root, blank, cm, cr, S);
     store_held<MODE, U>(mp, vp, msp, vsp, q, cm, cr, S);
 }
 
@@ -1058,7 +1139,7 @@ __device__ __forceinline__ void pack_part(const Rec& f, const Rec& t,
     roots<U>(v, root);
     uint32_t cm[U], cr[U];
     float S;
-    hold<U>(m, root, cm, cr, S);
+    hold<U>(m, root, 0, cm, cr, S);
     store_held<MODE, U>(global<uint8_t>(t.m) + off, global<uint8_t>(t.v) + off,
                         global<float>(t.ms) + off / kBlock,
                         global<float>(t.vs) + off / kBlock, q, cm, cr, S);

@@ -60,18 +60,31 @@ extern "C" {
  * and the weight comes to rest after some lr, as with fp32 states.  In a block
  * without any gradient the codes stay and the scales fade.
  *
- * What it costs: on noise with a mean of a tenth of its sigma, beside fp32
- * states after 1000 steps at beta2 0.95 (4000 at 0.999), an update is off by
- * 2 % (5 %) of its norm where the sigmas of a block's elements differ by
- * factors of about 1.35, by 6 % (10 %) where by e, and by more than half where
- * by e^2: the small ones then change by less than half a step of their codes.
- * The roots of v are right on average (to 1 %, 4 % in the last case).
- * Elements whose gradients fall to a thousandth of their block's are stepped as
- * with fp32 states at betas 0.9 and 0.95 (to 10 %); where they fall to a
- * millionth but not to 0, codes of 1 stay, and such weights move by about a
- * quarter of lr a step to one side.  With a beta1 above 0.9, codes of m above 9
- * fade only where the block's A moves by as much as their half step
- * (noise does that; at 0.99 it took 2000 steps). */
+ * What it costs, on noise with a mean of a tenth of its sigma, beside fp32
+ * states at beta1 0.9:
+ * - beta2 0.95 to 0.99: after some thousand steps an update is off by 2 % of
+ *   its norm where a block's elements have one sigma or sigmas that differ by
+ *   factors of about 1.35, by 6 to 8 % where by e, and by more than half where
+ *   by e^2 (the small ones then change by less than half a step of their
+ *   codes).  The roots of v are right on average, to 2 % (10 % at e^2).  Where
+ *   half of a block's gradients fall to a tenth its roots follow (to 4 %).
+ * - Above 0.99 the roots do not follow.  A step takes beta2^(1/4) of a code at
+ *   most, less than half of 1 from any code at a beta2 of 0.9922 and more, so
+ *   only a growing A lowers a code, while every large gradient may raise it.
+ *   At 0.999 and one sigma the roots are too large by 10 to 25 % after 4000
+ *   steps and by 35 to 50 % after 16000, and still grow (updates off by 16 and
+ *   27 %); sigmas that differ by 1.35 or e move A enough (2 % off, updates 5
+ *   and 9 %).  Gradients that fall to a tenth have roots 9 times too large
+ *   6000 steps later: their weights are stepped by a ninth.  With such a beta2
+ *   take fp32 states, or the 8-bit ones for their size in the knowledge that
+ *   steps get shorter.
+ * - Elements whose gradients fall to a thousandth of their block's are stepped
+ *   as with fp32 states at beta2 0.95 (to 10 %); where they fall to a millionth
+ *   but not to 0, codes of 1 stay, and such weights move by about a quarter of
+ *   lr a step to one side.
+ * - With a beta1 above 0.9, codes of m above 9 fade only where the block's A
+ *   moves by as much as their half step (noise does that; at 0.99 it took 2000
+ *   steps). */
 #define ZS_STATE_NONE 0
 #define ZS_STATE_32 32
 #define ZS_STATE_8  8

@@ -188,3 +188,52 @@ def test_gradients_that_fall(fall, like_fp32):
         assert abs(move8 / move - 1) < 0.1
     else:
         assert 0.15 < move8 < 0.5 and move < 0.12
+
+
+# ---- the roots of v
+
+@pytest.mark.parametrize("beta2,stays", [(0.95, 39), (0.98, 99), (0.99, 199),
+                                         (0.995, 255), (0.999, 255)])
+def test_codes_of_roots_that_stay(beta2, stays):
+    """A root that a step without a gradient takes sqrt(beta2) of keeps its
+    code up to a half step of it, beside an A that stays."""
+    q = np.arange(1, 256)
+    r = OT.decode(q, F([1 / 255 ** 2]))
+    down = np.where(q == 255, r, r * F(beta2) ** F(0.5)).astype(F)
+    k = OT.encode(down, 255)[0]
+    assert np.array_equal(k == q, (q <= stays) | (q == 255))
+    assert np.all(k[(q > stays) & (q < 255)] < q[(q > stays) & (q < 255)])
+
+
+@pytest.mark.parametrize("beta2,spread,steps,root,off", [
+    (0.95, 0.0, 3000, (0.99, 1.01), (0.005, 0.03)),
+    (0.95, 0.3, 3000, (0.99, 1.01), (0.01, 0.04)),
+    (0.95, 1.0, 3000, (0.98, 1.02), (0.03, 0.12)),
+    (0.98, 0.0, 3000, (0.99, 1.01), (0.005, 0.03)),
+    (0.99, 0.0, 3000, (0.98, 1.02), (0.005, 0.04)),
+    (0.995, 0.0, 3000, (0.98, 1.04), (0.01, 0.05)),
+    (0.999, 0.3, 4000, (0.97, 1.04), (0.02, 0.08)),
+    (0.999, 1.0, 4000, (0.97, 1.04), (0.05, 0.15)),
+    (0.999, 0.0, 4000, (1.08, 1.30), (0.08, 0.25)),
+    (0.999, 0.0, 16000, (1.25, 1.60), (0.20, 0.40))])
+def test_updates_after_many_steps(beta2, spread, steps, root, off):
+    """The held roots over fp32's, and what an update is off by."""
+    new, T = Noise(spread), Training(beta2=beta2)
+    for _ in range(steps):
+        T.step(new())
+    assert root[0] < T.roots().mean() < root[1]
+    assert off[0] < T.off() < off[1]
+
+
+@pytest.mark.parametrize("beta2,root", [(0.95, (0.98, 1.05)),
+                                        (0.99, (0.98, 1.10)),
+                                        (0.999, (5.0, 12.0))])
+def test_roots_of_gradients_that_fall_to_a_tenth(beta2, root):
+    """Half a block's, 5000 steps later."""
+    low = np.zeros((NB, BLOCK), bool)
+    low[:, ::2] = True
+    new, T = Noise(), Training(beta2=beta2)
+    for t in range(6000):
+        g = new()
+        T.step(np.where(low, g * F(0.1), g) if t >= 1000 else g)
+    assert root[0] < T.roots()[low].mean() < root[1]

@@ -95,7 +95,12 @@ extern "C" {
 
 /* One tensor: numel elements that lie one behind the other.
  * grad: its gradients from `world` ranks, slice s at grad + s*grad_stride
- *   elements (grad_stride is not read when world is 1).
+ *   elements (grad_stride is not read when world is 1).  A list keeps the
+ *   address: each step reads what lies there then, so gradients are written
+ *   into the same buffers every time.  Where a framework hands over new
+ *   gradient tensors, they are copied there, or the list is made anew.  A
+ *   tensor that has no gradient in some step has zeros there (its moments
+ *   fade and its weight decays) or a list of its own, which is not stepped.
  * param: its parameters, of the list's param_type.
  * master: fp32 master weights; then param (bf16) is written only.  NULL:
  *   param itself is read and updated.
@@ -123,7 +128,8 @@ typedef struct zs_tensors zs_tensors;
 /* Make a list.  Of the pointers, grad, param, master, and m with v are each
  * given for every tensor that has elements or for none (a list for
  * zs_tensors_sumsq needs gradients alone, one for zs_tensors_convert states
- * alone); a step needs grad, param, m and v.  grad_type, param_type: ZS_BF16
+ * alone); a step needs grad, param, m and v.  The addresses are the list's for
+ * good; nothing is read from them before a call runs.  grad_type, param_type: ZS_BF16
  * or ZS_F32 for all tensors.  state: ZS_STATE_32, ZS_STATE_8, or
  * ZS_STATE_NONE with m and v NULL.
  * fp32 pointers are aligned to 4 bytes, bf16 to 2, codes to 4; those aligned

@@ -138,7 +138,13 @@ def zs_tensors_create(*, params: Optional[Sequence] = None,
     codes with m_scale and v_scale of ceil(numel / ZS_STATE8_BLOCK) floats;
     groups: each tensor's index into a step's hyper-parameters (0 unless
     given).  A step needs params, grads, m and v; zs_tensors_sumsq grads;
-    zs_tensors_convert m and v.  zs_tensors_upload makes the list ready."""
+    zs_tensors_convert m and v.  zs_tensors_upload makes the list ready.
+
+    The list keeps these tensors, and every step reads the gradients from the
+    same grads: let autograd add into them (each parameter's .grad set to its
+    buffer once, and zero_grad(set_to_none=False)), or copy into them.  After
+    zero_grad(), whose set_to_none is True by default, a parameter's next .grad
+    is another tensor, and a step would take the old values again."""
     import torch
     if (m is None) != (v is None):
         raise ValueError("m and v belong together")

@@ -134,7 +134,8 @@ typedef struct zs_tensors zs_tensors;
  * ZS_STATE_NONE with m and v NULL.
  * fp32 pointers are aligned to 4 bytes, bf16 to 2, codes to 4; those aligned
  * to four elements go faster.  Arrays that a step writes must not overlap
- * one another nor the gradients (a tensor listed twice, say).
+ * one another nor the gradients (a tensor listed twice, say).  Tables, sums and
+ * workspaces lie apart from all arrays of a list; that is not checked.
  * Errors: ZS_EINVAL (NULL out, NULL tensors with count > 0, count < 0,
  * world < 1, unknown types or state, numel < 0, group outside
  * [0, ZS_TENSORS_MAX_GROUPS), pointers given for some tensors only, scales

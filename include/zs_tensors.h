@@ -68,9 +68,10 @@ extern "C" {
  *   by e^2 (the small ones then change by less than half a step of their
  *   codes).  The roots of v are right on average, to 2 % (10 % at e^2).  Where
  *   half of a block's gradients fall to a tenth its roots follow (to 4 %).
- * - Above 0.99 the roots do not follow.  A step takes beta2^(1/4) of a code at
- *   most, less than half of 1 from any code at a beta2 of 0.9922 and more, so
- *   only a growing A lowers a code, while every large gradient may raise it.
+ * - Above 0.99 the roots do not follow.  A step leaves beta2^(1/4) of a code
+ *   or more: at a beta2 of 0.9922 and above it takes less than half of 1 from
+ *   any, so only a growing A lowers a code, while every large gradient may
+ *   raise it.
  *   At 0.999 and one sigma the roots are too large by 10 to 25 % after 4000
  *   steps and by 35 to 50 % after 16000, and still grow (updates off by 16 and
  *   27 %); sigmas that differ by 1.35 or e move A enough (2 % off, updates 5
@@ -129,8 +130,8 @@ typedef struct zs_tensors zs_tensors;
  * given for every tensor that has elements or for none (a list for
  * zs_tensors_sumsq needs gradients alone, one for zs_tensors_convert states
  * alone); a step needs grad, param, m and v.  The addresses are the list's for
- * good; nothing is read from them before a call runs.  grad_type, param_type: ZS_BF16
- * or ZS_F32 for all tensors.  state: ZS_STATE_32, ZS_STATE_8, or
+ * good; nothing is read from them before a call runs.  grad_type, param_type:
+ * ZS_BF16 or ZS_F32 for all tensors.  state: ZS_STATE_32, ZS_STATE_8, or
  * ZS_STATE_NONE with m and v NULL.
  * fp32 pointers are aligned to 4 bytes, bf16 to 2, codes to 4; those aligned
  * to four elements go faster.  Arrays that a step writes must not overlap

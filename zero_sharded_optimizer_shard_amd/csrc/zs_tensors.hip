@@ -568,9 +568,9 @@ __device__ __forceinline__ void roots(const float (&x)[U][4],
 // weight of an element that has no gradient any more would go on moving, by a
 // third of lr a step.  Larger codes go down by themselves, and where elements
 // are without a gradient now and then their roundings have to be right on
-// average (all towards zero took 5 to 9 % off what such weights move, those up
-// to 9 nothing).  Looking for zeros costs 0 to 1 % (bf16 weights, 218 M
-// elements: 358 us of 356), gradients with many of them 3 to 9 % (392 of 359).
+// average (all towards zero took 5 to 12 % off what such weights move, those
+// up to 9 nothing).  Looking for zeros costs 0 to 1 % (bf16 weights, 218 M
+// elements: 358 us of 356), gradients with many of them 3 to 11 % (392 of 359).
 constexpr float kFade = 9.0f;
 
 __device__ __forceinline__ uint32_t faded(const float (&m)[4], float im,
@@ -864,7 +864,8 @@ __global__ __launch_bounds__(kWave) void step_kernel(StepArgs a)
 // here, so no gradient's square overflows or is lost.  Each wave takes a run
 // of consecutive pieces (32 waves to a CU), workgroups leave one partial sum
 // each, and a second launch adds those: 70 us over 218 M bf16 elements, 5 of
-// them the second launch.
+// them the second launch; 154, 295 and 575 us for two, four and eight ranks
+// (5.7 to 6.1 TB/s, 6.1 with fp32 gradients), 1 % more with rows off lines.
 constexpr int kSumThreads = 256;
 constexpr int kSumWaves = kSumThreads / kWave;
 constexpr int kSumMaxGroups = 2048;     // workgroups, and so partial sums

@@ -219,7 +219,7 @@ def between(x, w, off, where):
 
 
 # a few whole parts, what is left of one, and tensors that have no whole one
-SIZES = [1, 300, 4 * 512 + 7, 3 * 1024]
+SIZES = [1, 300, 4 * 512 + 7, 4 * 1024]
 WAYS = {"lines": "lines", "fours": "aligned", "odd": "whole"}
 
 
@@ -256,6 +256,23 @@ def test_rows_at_lines_behind_a_lead(weights, grad, world):
     assert c.ways() == {"lines", "edge"}
     c.step()
     c.check()
+
+
+@pytest.mark.parametrize("weights", ["master", "bf16", "f32"])
+@pytest.mark.parametrize("shift", [1, 37, 60])
+def test_tensors_that_need_one_piece_more(weights, shift):
+    """Units that start late in tensors of whole pieces, or nearly: their last
+    elements are in pieces behind all others, one behind the other."""
+    sizes = [1024, 2048, 5, 4095, 1, 5120, 1000, 300, 1023, 2049]
+    c = Rows(sizes, 32, weights, "bf16", 1, shift=shift, seed=17)
+    for t in (1, 2):
+        c.step(t=t)
+        c.check()
+        for h, d in zip(c.host, c.dev):
+            x = d["master" if "master" in d else "param"]
+            h["master" if "master" in h else "param"] = \
+                x.cpu().numpy() if x.dtype == torch.float32 else \
+                OT.to_bf16(x.float().cpu().numpy())
 
 
 @pytest.mark.parametrize("state", [32, 8])

@@ -60,7 +60,7 @@ extern "C" {
  * and the weight comes to rest after some lr, as with fp32 states.  In a block
  * without any gradient the codes stay and the scales fade.
  *
- * What it costs, on noise with a mean of a tenth of its sigma, beside fp32
+ * What ZS_STATE_8 costs, on noise with a mean of a tenth of its sigma, beside fp32
  * states at beta1 0.9:
  * - beta2 0.95 to 0.99: after some thousand steps an update is off by 2 % of
  *   its norm where a block's elements have one sigma or sigmas that differ by
@@ -178,7 +178,8 @@ int zs_tensors_upload(zs_tensors* list, void* table, int64_t bytes,
  * its element in 32 bits, and with its block's states in 8.
  *
  * hp: n_hp (1 .. ZS_TENSORS_MAX_GROUPS) hyper-parameter groups, read during
- *   the call.  step: the 1-based counter t of all tensors.
+ *   the call.  With states in 8 bits a beta2 above 0.99 is taken, at the cost
+ *   that ZS_STATE_8 states.  step: the 1-based counter t of all tensors.
  * sumsq: DEVICE pointer to one double (8-byte aligned), or NULL.  With it the
  *   gradients are clipped by their global norm n = sqrt(*sumsq):
  *   c = f32(max_norm / n) where n > max_norm, else 1 (in double, rounded

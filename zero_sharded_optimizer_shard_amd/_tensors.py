@@ -235,7 +235,9 @@ def zs_tensors_step(lst: TensorList, hp, *, step: int, sumsq=None,
     for each hyper-parameter group; step: the counter t, from 1.  sumsq: a
     device float64 that zs_tensors_sumsq wrote (or ranks added up): the
     gradients are clipped to the global norm max_norm, and where it is
-    negative or not finite the step writes nothing."""
+    negative or not finite the step writes nothing.  With states in 8 bits
+    keep beta2 to 0.99: above it the roots of v do not follow gradients that
+    fall (include/zs_tensors.h has the figures)."""
     hps = [hp] if isinstance(hp, zs_adamw) else hp
     arr = (zs_adamw * max(len(hps), 1))(*hps)
     ptr = None
